@@ -443,6 +443,161 @@ bitnet_status bitnet_chain_run(const bitnet_chain *chain, hipStream_t stream);
  * barriers).  Synchronises with the device. */
 bitnet_status bitnet_chain_error(const bitnet_chain *chain, int *error);
 
+/* ---------------------------------------------------------------------------
+ * What lies between a layer's ternary products: the cache of keys and values,
+ * attention over it, and the join with the residual stream.  (communeify.com,
+ * section on BitNet b1.58 2B4T, architecture item: a Transformer whose linear
+ * layers are BitLinear, with rotary position embeddings and subln norms.  The
+ * page gives no cache format; this one follows the layer's activations: absmax
+ * int8, here with one scale for each page and head.)
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Paged cache of one layer (device memory, caller-owned).  A page holds `page`
+ * tokens of every kv head; a value is its code times its page's and head's scale.
+ * Keys lie token by token and values dim by dim, the order in which the matrix
+ * cores take them.
+ *   page      16, 32, 64 or 128.
+ *   head_dim  a multiple of 16, 16 to 256.
+ *   kv_heads  1 to 65535; pages 1 to 2^31 - 1 (the arrays may pass 4 GiB).
+ *   k, v      16-byte aligned; the scales 4-byte aligned.
+ * Memory of pages that were never written may hold anything.
+ */
+typedef struct bitnet_kv_cache {
+  int8_t *k;       /* [pages][kv_heads][page][head_dim] */
+  int8_t *v;       /* [pages][kv_heads][head_dim][page] */
+  float *k_scale;  /* [pages][kv_heads] */
+  float *v_scale;  /* [pages][kv_heads] */
+  int64_t pages;
+  int kv_heads, page, head_dim;
+} bitnet_kv_cache;
+
+/*
+ * A ragged batch (the arrays are device memory, read when the work runs, so that a
+ * captured graph follows their contents).  The new rows of sequence b are rows
+ * [q_start[b], q_start[b+1]) of the batch's row arrays; they are its last tokens:
+ * with kv_len[b] tokens in all, row i has position kv_len[b] - (rows of b) + i.
+ * Position j lies in page table[b][j / page], slot j % page.
+ *   seqs     1 to 65535 (0: nothing to do).
+ *   width    page ids a row of the table holds, width * page <= 2^30.
+ *   tokens   rows of the row arrays (rows outside every sequence are left alone).
+ *   max_new  1 .. tokens: no sequence has more new rows (rows past it are left alone).
+ *   max_len  0 .. width * page: no kv_len is larger (a larger one counts as max_len).
+ * The contents are not trusted: row numbers are clamped to the batch, a kv_len
+ * below 0 counts as 0, and a page id outside the cache is a page without tokens
+ * (nothing is written to it, and its keys are not seen).  A row whose position is
+ * negative (more new rows than tokens) has no place in the cache and sees no key.
+ */
+typedef struct bitnet_kv_batch {
+  const int32_t *table;    /* [seqs][width] */
+  const int32_t *q_start;  /* [seqs + 1], not decreasing */
+  const int32_t *kv_len;   /* [seqs], with the new rows */
+  int64_t seqs, width, tokens, max_new, max_len;
+} bitnet_kv_batch;
+
+/*
+ * New rows of one layer: keys and values for the cache, and the queries that are
+ * rotated with them.
+ *   dtype     type of k, v, q and q_out (bitnet_dtype); element-aligned.
+ *   k, v      [tokens] rows of [kv_heads][head_dim], k_stride / v_stride elements
+ *             from one token to the next (>= kv_heads * head_dim).
+ *   q, q_out  NULL, or the queries [tokens] rows of [q_heads][head_dim], q_stride
+ *             elements apart, and the rotated ones, contiguous and 16-byte
+ *             aligned.  q_out may be q where q is contiguous.
+ *   cos, sin  [positions][rotary / 2] fp32, positions >= max_len; NULL when
+ *             rotary = 0.
+ *   rotary    rotated dims, even, 0 to head_dim; the others pass through.
+ *   interleaved  0: pairs (i, i + rotary/2); 1: pairs (2i, 2i + 1).
+ */
+typedef struct bitnet_kv_rows {
+  const void *k, *v, *q;
+  void *q_out;
+  int64_t k_stride, v_stride, q_stride;
+  int dtype, q_heads;
+  const float *cos, *sin;
+  int64_t positions;
+  int rotary, interleaved;
+} bitnet_kv_rows;
+
+/*
+ * Rotates the keys (and queries) by their positions and appends keys and values to
+ * the cache, in one launch.
+ *   pair (a, b) at angle (c, s): (RN32(RN32(a c) - RN32(b s)), RN32(RN32(b c) + RN32(a s)));
+ *   a page's new rows x (all heads by themselves): need = RN32(max(max|x|, RN32(1e-5)) / 127);
+ *   a page whose slot 0 is written takes the scale d' = need, another d' = max(d, need);
+ *   codes clip(rne(RN32(x * RN32(1 / d'))), -127, 127); where d' > d the page's
+ *   earlier codes c become rne(RN32(c * RN32(d / d'))).
+ * All results are bit-exact against that definition.  Rows must be finite (others
+ * spoil their own page and head).  Slots past a sequence's last token keep their
+ * bytes.  Two sequences of a batch may share pages that the call does not write;
+ * a page that it writes must belong to one sequence (otherwise its contents are
+ * unspecified).
+ */
+bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, const bitnet_kv_batch *batch,
+                               const bitnet_kv_rows *rows, hipStream_t stream);
+
+/*
+ * Attention of the batch's rows over the cache: row at position p sees the keys
+ * max(0, p - window + 1) .. p (window 0: 0 .. p), which bitnet_kv_append has
+ * written, its own among them.
+ *   s_j = softmax_scale * (q . k_j),  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),
+ *   lse = m + ln sum_j e^(s_j - m),  m = max_j s_j.
+ * A row that sees no key gets zeros and lse = -inf.
+ *   q        [tokens] rows of [q_heads][head_dim], q_stride elements apart (>= q_heads *
+ *            head_dim), fp32 or bf16 (q_dtype), finite; query head h reads kv head
+ *            h / (q_heads / kv_heads), q_heads a multiple of kv_heads, <= 65535.
+ *   out      [tokens][q_heads][head_dim], contiguous, fp32 or bf16 (out_dtype).
+ *   lse      [tokens][q_heads] fp32, or NULL.
+ *   softmax_scale  finite; window >= 0.
+ *   workspace  bitnet_attention_workspace_bytes() bytes of device memory, 16-byte
+ *            aligned; clobbered; calls that overlap need one each.  NULL when the
+ *            size is 0.
+ */
+bitnet_status bitnet_attention(const bitnet_kv_cache *cache, const bitnet_kv_batch *batch,
+                               const void *q, int q_dtype, int64_t q_stride, int q_heads,
+                               float softmax_scale, int64_t window, void *out, int out_dtype,
+                               float *lse, void *workspace, size_t workspace_bytes,
+                               hipStream_t stream);
+
+/* Workspace of bitnet_attention for this cache's and batch's sizes (their arrays are
+ * not read; the pointers may be NULL).  0 for sizes that bitnet_attention refuses. */
+size_t bitnet_attention_workspace_bytes(const bitnet_kv_cache *cache,
+                                        const bitnet_kv_batch *batch, int q_heads);
+
+/*
+ * A block's output y joins the residual stream h, and the next block's input u
+ * leaves normalised, quantised, or both, in one launch:
+ *   z = y, or RN32(RN32(y * r) * post_weight) with the RMS norm behind the block;
+ *   z = RN32(z * gate) where there is a gate;
+ *   h' = RN(RN32(h + RN32(z * scale))), RN to h_dtype, written to h_out;
+ *   u = h', or RN32(RN32(h' * r) * pre_weight) with the norm before the next block;
+ *   x_q, x_scale = the codes and scales that bitnet_quantize_acts forms of u.
+ * r = RN32(1 / sqrt(RN32(ms + eps))) of the row it scales, ms the exactly rounded
+ * mean of squares, as in bitnet_act_prologue.  Bit-exact against that definition.
+ *   M, K         M >= 0, K >= 1 (M == 0 is a no-op), M <= 2^31 - 1.
+ *   y            [M][K] fp32 or bf16 (y_dtype); gate has the same type.
+ *   h, h_out     [M][K] fp32 or bf16 (h_dtype); h_out may be h.
+ *   gate         NULL, or [M] rows of [K], gate_stride elements apart (0: one row
+ *                for every token, else >= K).
+ *   post_weight, pre_weight  NULL (no norm) or [K] fp32.
+ *   u            NULL, or [M][K] fp32 or bf16 (u_dtype; not looked at when u is NULL).
+ *   x_q, x_scale both NULL, or [M][K] int8 and [M] fp32.
+ *   scale        finite; eps >= 0, finite.
+ * Values must be finite.
+ */
+typedef struct bitnet_residual {
+  const void *y, *h, *gate;
+  void *h_out, *u;
+  const float *post_weight, *pre_weight;
+  int8_t *x_q;
+  float *x_scale;
+  int64_t M, K, gate_stride;
+  int y_dtype, h_dtype, u_dtype;
+  float scale, eps;
+} bitnet_residual;
+
+bitnet_status bitnet_residual_norm(const bitnet_residual *args, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

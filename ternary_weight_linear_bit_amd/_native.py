@@ -627,3 +627,296 @@ def bitnet_prefill_tile(m, ns, k):
                                                             ctypes.byref(bn), ctypes.byref(first),
                                                             ctypes.byref(rows)))
     return bm.value, bn.value, first.value, rows.value
+
+
+# ---------------------------------------------------------------------------
+# cache of keys and values, attention over it, residual join
+# ---------------------------------------------------------------------------
+
+class BitnetKvCache(ctypes.Structure):
+    """struct bitnet_kv_cache of the public header."""
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("pages", _I64),
+                ("kv_heads", _I), ("page", _I), ("head_dim", _I)]
+
+
+class BitnetKvBatch(ctypes.Structure):
+    """struct bitnet_kv_batch of the public header."""
+    _fields_ = [("table", _P), ("q_start", _P), ("kv_len", _P), ("seqs", _I64), ("width", _I64),
+                ("tokens", _I64), ("max_new", _I64), ("max_len", _I64)]
+
+
+class BitnetKvRows(ctypes.Structure):
+    """struct bitnet_kv_rows of the public header."""
+    _fields_ = [("k", _P), ("v", _P), ("q", _P), ("q_out", _P), ("k_stride", _I64),
+                ("v_stride", _I64), ("q_stride", _I64), ("dtype", _I), ("q_heads", _I),
+                ("cos", _P), ("sin", _P), ("positions", _I64), ("rotary", _I),
+                ("interleaved", _I)]
+
+
+class BitnetResidual(ctypes.Structure):
+    """struct bitnet_residual of the public header."""
+    _fields_ = [("y", _P), ("h", _P), ("gate", _P), ("h_out", _P), ("u", _P), ("post_weight", _P),
+                ("pre_weight", _P), ("x_q", _P), ("x_scale", _P), ("M", _I64), ("K", _I64),
+                ("gate_stride", _I64), ("y_dtype", _I), ("h_dtype", _I), ("u_dtype", _I),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+SIGNATURES["bitnet_kv_append"] = (_I, [ctypes.POINTER(BitnetKvCache),
+                                       ctypes.POINTER(BitnetKvBatch),
+                                       ctypes.POINTER(BitnetKvRows), _P])
+SIGNATURES["bitnet_attention_workspace_bytes"] = (_SZ, [ctypes.POINTER(BitnetKvCache),
+                                                        ctypes.POINTER(BitnetKvBatch), _I])
+SIGNATURES["bitnet_attention"] = (_I, [ctypes.POINTER(BitnetKvCache),
+                                       ctypes.POINTER(BitnetKvBatch), _P, _I, _I64, _I,
+                                       ctypes.c_float, _I64, _P, _I, _P, _P, _SZ, _P])
+SIGNATURES["bitnet_residual_norm"] = (_I, [ctypes.POINTER(BitnetResidual), _P])
+
+
+def _one_device(*ts):
+    """Every tensor (None: absent) on one device: its kernels read them all."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors lie on {dev} and {t.device}")
+    return dev
+
+
+class _On:
+    """The tensors' device made current (kernels launch on the current device) and
+    the stream the call goes to: the caller's, which has to be one of that device, or
+    the device's current one.  Tensors that the call allocates belong to that stream."""
+
+    def __init__(self, device, stream):
+        import torch
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is one of {stream.device}, the tensors lie on {device}")
+        self._guard = None
+        if stream is not None:
+            self._guard = torch.cuda.stream(stream)       # its device too
+        elif torch.cuda.current_device() != device.index:
+            self._guard = torch.cuda.device(device)
+        self._device = device
+
+    def __enter__(self):
+        import torch
+        if self._guard is not None:
+            self._guard.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+class KVCache:
+    """Paged 8-bit cache of one layer: int8 k [pages, kv_heads, page, head_dim] and
+    v [pages, kv_heads, head_dim, page], fp32 scales [pages, kv_heads].  Holds the
+    tensors and the C struct; sizes are fixed, contents are the caller's."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, kv_heads, page, head_dim]")
+        pages, heads, page, dim = k.shape
+        _expect(k, (pages, heads, page, dim), torch.int8, "k")
+        _expect(v, (pages, heads, dim, page), torch.int8, "v")
+        _expect(k_scale, (pages, heads), torch.float32, "k_scale")
+        _expect(v_scale, (pages, heads), torch.float32, "v_scale")
+        if page not in (16, 32, 64, 128):
+            raise ValueError("a page holds 16, 32, 64 or 128 tokens")
+        if dim % 16 or not 16 <= dim <= 256:
+            raise ValueError("head_dim must be a multiple of 16, up to 256")
+        self.device = _one_device(k, v, k_scale, v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.kv_heads, self.page, self.head_dim = pages, heads, page, dim
+        self.handle = BitnetKvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                    v_scale.data_ptr(), pages, heads, page, dim)
+        self.ref = ctypes.byref(self.handle)
+
+    @staticmethod
+    def empty(pages, kv_heads, page, head_dim, device="cuda"):
+        """A cache of uninitialised pages."""
+        import torch
+        return KVCache(torch.empty((pages, kv_heads, page, head_dim), dtype=torch.int8, device=device),
+                       torch.empty((pages, kv_heads, head_dim, page), dtype=torch.int8, device=device),
+                       torch.empty((pages, kv_heads), dtype=torch.float32, device=device),
+                       torch.empty((pages, kv_heads), dtype=torch.float32, device=device))
+
+
+class KVBatch:
+    """Ragged batch over a paged cache: int32 table [seqs, width] of page ids, q_start
+    [seqs + 1] (rows of each sequence's new tokens), kv_len [seqs] (cached tokens with
+    the new ones).  max_new and max_len bound what q_start and kv_len say; the arrays'
+    contents may change between calls (and between replays of a captured graph)."""
+
+    def __init__(self, table, q_start, kv_len, max_new, max_len):
+        import torch
+        if table.dim() != 2:
+            raise ValueError("table must be [seqs, width]")
+        seqs, width = table.shape
+        _expect(table, (seqs, width), torch.int32, "table")
+        _expect(q_start, (seqs + 1,), torch.int32, "q_start")
+        _expect(kv_len, (seqs,), torch.int32, "kv_len")
+        if max_new < 1 or max_len < 0:
+            raise ValueError("max_new must be at least 1 and max_len at least 0")
+        self.device = _one_device(table, q_start, kv_len)
+        self.table, self.q_start, self.kv_len = table, q_start, kv_len
+        self.seqs, self.max_new, self.max_len = seqs, max_new, max_len
+        self._struct = (-1, None)   # (tokens, reference to the C struct): one object, so
+                                    # that threads with different rows do not mix them
+
+    def _of(self, tokens):
+        """The C struct for row arrays of `tokens` rows (max_new is at most that)."""
+        st = self._struct
+        if st[0] != tokens:
+            st = (tokens, ctypes.byref(BitnetKvBatch(
+                self.table.data_ptr(), self.q_start.data_ptr(), self.kv_len.data_ptr(), self.seqs,
+                self.table.shape[1], tokens, min(self.max_new, max(tokens, 1)), self.max_len)))
+            self._struct = st
+        return st[1]
+
+
+def _rows(t, heads, dim, name):
+    """t [tokens, heads, dim]: dims and heads adjacent, any distance between tokens.
+    Returns that distance in elements."""
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
+        raise ValueError(f"{name}: expected [tokens, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    h = t.shape[1]
+    if t.numel() == 0:
+        return h * dim
+    st = t.stride()
+    if st[2] != 1 or (h > 1 and st[1] != dim) or (t.shape[0] > 1 and st[0] < h * dim):
+        raise ValueError(f"{name}: a token's heads and dims must lie one after another")
+    return st[0] if t.shape[0] > 1 else h * dim
+
+
+def bitnet_kv_append(cache, batch, k, v, cos=None, sin=None, interleaved=False, q=None, q_out=None,
+                     stream=None):
+    """Rotates new keys k [T, kv_heads, D] (and queries q [T, q_heads, D]) by their
+    positions and appends k and v to the cache.  cos / sin: fp32 [positions, rotary/2]
+    (None: no rotation).  Returns the rotated queries (None without q)."""
+    import torch
+    dim = cache.head_dim
+    ks, vs = _rows(k, cache.kv_heads, dim, "k"), _rows(v, cache.kv_heads, dim, "v")
+    tokens = k.shape[0]
+    dt = _dtype_code(k.dtype)
+    if v.dtype != k.dtype or v.shape[0] != tokens:
+        raise ValueError("v must match k in tokens and dtype")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    rot = positions = 0
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError("cos must be [positions, rotary / 2]")
+        positions, rot = cos.shape[0], 2 * cos.shape[1]
+        _expect(cos, cos.shape, torch.float32, "cos")
+        _expect(sin, cos.shape, torch.float32, "sin")
+    qs = q_heads = 0
+    if q is not None:
+        qs = _rows(q, None, dim, "q")
+        if q.dtype != k.dtype or q.shape[0] != tokens:
+            raise ValueError("q must match k in tokens and dtype")
+        q_heads = q.shape[1]
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    device = _one_device(cache.k, batch.table, k, v, cos, sin, q, q_out)
+    with _On(device, stream) as s:
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        if q_out is not None:
+            _expect(q_out, q.shape, q.dtype, "q_out")
+        rows = BitnetKvRows(k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
+                            None if q is None else q_out.data_ptr(), ks, vs, qs, dt, q_heads,
+                            None if cos is None else cos.data_ptr(),
+                            None if sin is None else sin.data_ptr(), positions, rot,
+                            1 if interleaved else 0)
+        _check("bitnet_kv_append", lib().bitnet_kv_append(cache.ref, batch._of(tokens),
+                                                          ctypes.byref(rows), s))
+    return q_out
+
+
+def bitnet_attention_workspace_bytes(cache, batch, tokens, q_heads) -> int:
+    """Workspace of bitnet_attention for `tokens` rows of q_heads heads."""
+    return lib().bitnet_attention_workspace_bytes(cache.ref, batch._of(tokens), q_heads)
+
+
+def bitnet_attention(cache, batch, q, scale=None, window=0, out=None, out_dtype=None, lse=None,
+                     workspace=None, stream=None):
+    """Attention of queries q [T, q_heads, D] over the cache -> out [T, q_heads, D]
+    (q's dtype unless out_dtype).  scale: of the products (D**-0.5); window: keys a
+    row sees, itself included (0: all earlier ones); lse: optional fp32 [T, q_heads]."""
+    import torch
+    dim = cache.head_dim
+    qs = _rows(q, None, dim, "q")
+    tokens, q_heads = q.shape[0], q.shape[1]
+    if q_heads % cache.kv_heads:
+        raise ValueError("q_heads must be a multiple of the cache's kv_heads")
+    if out is not None:
+        _expect(out, q.shape, _floats(), "out")
+    if lse is not None:
+        _expect(lse, (tokens, q_heads), torch.float32, "lse")
+    if workspace is not None:
+        _need_cuda(workspace)
+    device = _one_device(cache.k, batch.table, q, out, lse, workspace)
+    with _On(device, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=device)
+        b = batch._of(tokens)
+        need = lib().bitnet_attention_workspace_bytes(cache.ref, b, q_heads)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        _check("bitnet_attention", lib().bitnet_attention(
+            cache.ref, b, q.data_ptr(), _dtype_code(q.dtype), qs, q_heads,
+            dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+            _dtype_code(out.dtype), None if lse is None else lse.data_ptr(),
+            None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), s))
+    return out
+
+
+def bitnet_residual_norm(y, h, h_out=None, post_weight=None, gate=None, scale=1.0, pre_weight=None,
+                         eps=1e-5, u=None, x_q=None, x_scale=None, quantize=True, stream=None):
+    """h_out = h + scale * gate * post_norm(y); u = pre_norm(h_out), written to `u`
+    where one is given, and (unless quantize=False) quantised per token.  y [M, K]
+    fp32/bf16, h [M, K] fp32/bf16, gate [K] or [M, K] like y, weights fp32 [K] (None:
+    no norm).  h_out may be h.  Returns (h_out, x_q, x_scale) (None unless quantised)."""
+    import torch
+    if y.dim() != 2:
+        raise ValueError("y must be 2-D [M, K]")
+    m, k = y.shape
+    _expect(y, (m, k), _floats(), "y")
+    _expect(h, (m, k), _floats(), "h")
+    _expect(post_weight, (k,), torch.float32, "post_weight")
+    _expect(pre_weight, (k,), torch.float32, "pre_weight")
+    _expect(u, (m, k), _floats(), "u")
+    gate_stride = 0
+    if gate is not None:
+        gate_stride = k if gate.dim() == 2 else 0
+        _expect(gate, (m, k) if gate.dim() == 2 else (k,), y.dtype, "gate")
+    if not quantize and (x_q is not None or x_scale is not None):
+        raise ValueError("x_q / x_scale with quantize=False")
+    device = _one_device(y, h, h_out, post_weight, gate, pre_weight, u, x_q, x_scale)
+    with _On(device, stream) as s:
+        if h_out is None:
+            h_out = torch.empty((m, k), dtype=h.dtype, device=device)
+        _expect(h_out, (m, k), h.dtype, "h_out")
+        if quantize:
+            if x_q is None:
+                x_q = torch.empty((m, k), dtype=torch.int8, device=device)
+            if x_scale is None:
+                x_scale = torch.empty(m, dtype=torch.float32, device=device)
+            _expect(x_q, (m, k), torch.int8, "x_q")
+            _expect(x_scale, (m,), torch.float32, "x_scale")
+        p = lambda t: None if t is None else t.data_ptr()
+        args = BitnetResidual(p(y), p(h), p(gate), p(h_out), p(u), p(post_weight), p(pre_weight),
+                              p(x_q), p(x_scale), m, k, gate_stride, _dtype_code(y.dtype),
+                              _dtype_code(h.dtype), 0 if u is None else _dtype_code(u.dtype),
+                              scale, eps)
+        _check("bitnet_residual_norm", lib().bitnet_residual_norm(ctypes.byref(args), s))
+    return h_out, x_q, x_scale

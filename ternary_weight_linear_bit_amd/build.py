@@ -19,7 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbitnet_mi355x.so")
-SOURCES = ("api.hip", "wq.hip", "aq.hip", "gemv.hip", "gemm.hip", "lut.hip", "chain.hip")
+SOURCES = ("api.hip", "wq.hip", "aq.hip", "gemv.hip", "gemm.hip", "lut.hip", "chain.hip",
+           "kvcache.hip", "attn.hip", "residual.hip")
 # bench-only diagnostics (int8 matrix-core rate, HBM read rates, launch cost), their
 # own library: not part of the ABI
 PROBE_SRCS = [os.path.join(PKG, "bench_probe", f) for f in ("mfma_probe.hip", "hbm_probe.hip")]

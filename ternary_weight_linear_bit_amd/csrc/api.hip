@@ -231,6 +231,54 @@ bitnet_status quant_linear_t1(const bitnet_matrix* mats, int count, const void* 
   return run_linear_t1(mats, count, x_q, x_scale, M, K, y_dtype, stream);
 }
 
+// ---------------------------------------------------------------------------
+// cache, attention, residual join
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kMaxSeqs = 65535;       // a grid dimension
+constexpr int64_t kMaxCached = 1 << 30;   // positions are 32-bit
+
+bool finite(float f) { return f - f == 0.0f; }
+
+// Sizes of a cache and a batch (their arrays are not looked at).
+bitnet_status check_kv_sizes(const bitnet_kv_cache& c, const bitnet_kv_batch& b) {
+  if (c.page != 16 && c.page != 32 && c.page != 64 && c.page != 128) return BITNET_ERR_SHAPE;
+  if (c.head_dim < 16 || c.head_dim > 256 || c.head_dim % 16 != 0) return BITNET_ERR_SHAPE;
+  if (c.kv_heads < 1 || c.kv_heads > 65535 || c.pages < 1 || c.pages > kInt32Max)
+    return BITNET_ERR_SHAPE;
+  if (b.seqs < 0 || b.seqs > kMaxSeqs || b.tokens < 0 || b.tokens > kInt32Max)
+    return BITNET_ERR_SHAPE;
+  if (b.seqs == 0 || b.tokens == 0) return BITNET_OK;
+  if (b.width < 1 || b.width > kMaxCached / c.page || b.max_new < 1 || b.max_new > b.tokens ||
+      b.max_len < 0 || b.max_len > b.width * c.page)
+    return BITNET_ERR_SHAPE;
+  return BITNET_OK;
+}
+
+// Arrays of a cache and a batch that have something to do.
+bitnet_status check_kv_arrays(const bitnet_kv_cache& c, const bitnet_kv_batch& b) {
+  if (!c.k || !c.v || !c.k_scale || !c.v_scale || !b.table || !b.q_start || !b.kv_len)
+    return BITNET_ERR_NULL;
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.k_scale, 4) ||
+      !aligned(c.v_scale, 4) || !aligned(b.table, 4) || !aligned(b.q_start, 4) ||
+      !aligned(b.kv_len, 4))
+    return BITNET_ERR_ALIGN;
+  return BITNET_OK;
+}
+
+bitnet::KvCache kv_cache(const bitnet_kv_cache& c) {
+  return {c.k, c.v, c.k_scale, c.v_scale, (int)c.pages, c.kv_heads, c.page, c.head_dim};
+}
+bitnet::KvBatch kv_batch(const bitnet_kv_batch& b) {
+  return {b.table, b.q_start, b.kv_len, (int)b.seqs, (int)b.width, (int)b.tokens, (int)b.max_new,
+          (int)b.max_len};
+}
+
+// q_heads over a cache's kv_heads.
+bool heads_fit(const bitnet_kv_cache& c, int q_heads) {
+  return q_heads >= 1 && q_heads <= 65535 && q_heads % c.kv_heads == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -611,6 +659,103 @@ bitnet_status bitnet_chain_error(const bitnet_chain* chain, int* error) {
   if (hipMemcpy(&word, at, sizeof(word), hipMemcpyDeviceToHost) != hipSuccess) return BITNET_ERR_HIP;
   *error = (int)word;
   return BITNET_OK;
+}
+
+bitnet_status bitnet_kv_append(const bitnet_kv_cache* cache, const bitnet_kv_batch* batch,
+                               const bitnet_kv_rows* rows, hipStream_t stream) {
+  if (!cache || !batch || !rows) return BITNET_ERR_NULL;
+  const bitnet_kv_cache& c = *cache;
+  const bitnet_kv_batch& b = *batch;
+  const bitnet_kv_rows& r = *rows;
+  bitnet_status st = check_kv_sizes(c, b);
+  if (st != BITNET_OK) return st;
+  if (!valid_dtype(r.dtype)) return BITNET_ERR_DTYPE;
+  if (r.rotary < 0 || r.rotary > c.head_dim || r.rotary % 2 != 0 ||
+      (r.interleaved != 0 && r.interleaved != 1))
+    return BITNET_ERR_SHAPE;
+  if (r.q && !heads_fit(c, r.q_heads)) return BITNET_ERR_SHAPE;
+  if (b.seqs == 0 || b.tokens == 0) return BITNET_OK;
+  const int64_t kv_row = (int64_t)c.kv_heads * c.head_dim, q_row = (int64_t)r.q_heads * c.head_dim;
+  if (r.k_stride < kv_row || r.v_stride < kv_row || (r.q && r.q_stride < q_row))
+    return BITNET_ERR_SHAPE;
+  if (r.rotary > 0 && r.positions < b.max_len) return BITNET_ERR_SHAPE;
+  st = check_kv_arrays(c, b);
+  if (st != BITNET_OK) return st;
+  if (!r.k || !r.v || (r.q && !r.q_out) || (r.rotary > 0 && (!r.cos || !r.sin)))
+    return BITNET_ERR_NULL;
+  if (r.q && r.q_out == r.q && r.q_stride != q_row) return BITNET_ERR_SHAPE;
+  if (!aligned(r.k, esize(r.dtype)) || !aligned(r.v, esize(r.dtype)) ||
+      (r.q && (!aligned(r.q, esize(r.dtype)) || !aligned(r.q_out, 16))) || !aligned(r.cos, 4) ||
+      !aligned(r.sin, 4))
+    return BITNET_ERR_ALIGN;
+  const bitnet::KvRows k{r.k, r.v, r.q, r.q_out, r.k_stride, r.v_stride, r.q_stride, r.q_heads,
+                         r.cos, r.sin, r.rotary, r.interleaved};
+  return from_hip(bitnet::launch_kv_append(kv_cache(c), kv_batch(b), k, r.dtype == BITNET_BF16,
+                                           stream));
+}
+
+size_t bitnet_attention_workspace_bytes(const bitnet_kv_cache* cache, const bitnet_kv_batch* batch,
+                                        int q_heads) {
+  if (!cache || !batch || check_kv_sizes(*cache, *batch) != BITNET_OK ||
+      !heads_fit(*cache, q_heads) || batch->seqs == 0 || batch->tokens == 0)
+    return 0;
+  return bitnet::attention_workspace_bytes(kv_cache(*cache), kv_batch(*batch), q_heads);
+}
+
+bitnet_status bitnet_attention(const bitnet_kv_cache* cache, const bitnet_kv_batch* batch,
+                               const void* q, int q_dtype, int64_t q_stride, int q_heads,
+                               float softmax_scale, int64_t window, void* out, int out_dtype,
+                               float* lse, void* workspace, size_t workspace_bytes,
+                               hipStream_t stream) {
+  if (!cache || !batch) return BITNET_ERR_NULL;
+  const bitnet_kv_cache& c = *cache;
+  const bitnet_kv_batch& b = *batch;
+  bitnet_status st = check_kv_sizes(c, b);
+  if (st != BITNET_OK) return st;
+  if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype)) return BITNET_ERR_DTYPE;
+  if (!heads_fit(c, q_heads) || window < 0 || !finite(softmax_scale)) return BITNET_ERR_SHAPE;
+  if (b.seqs == 0 || b.tokens == 0) return BITNET_OK;
+  if (q_stride < (int64_t)q_heads * c.head_dim) return BITNET_ERR_SHAPE;
+  st = check_kv_arrays(c, b);
+  if (st != BITNET_OK) return st;
+  if (!q || !out) return BITNET_ERR_NULL;
+  if (!aligned(q, esize(q_dtype)) || !aligned(out, esize(out_dtype)) || !aligned(lse, 4))
+    return BITNET_ERR_ALIGN;
+  const bitnet::KvCache kc = kv_cache(c);
+  const bitnet::KvBatch kb = kv_batch(b);
+  const size_t need = bitnet::attention_workspace_bytes(kc, kb, q_heads);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return BITNET_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return BITNET_ERR_ALIGN;
+  }
+  const bitnet::AttnArgs a{q, out, lse, q_stride, q_heads,
+                           (int)(window > kMaxCached ? kMaxCached : window), softmax_scale};
+  return from_hip(bitnet::launch_attention(kc, kb, a, q_dtype == BITNET_BF16,
+                                           out_dtype == BITNET_BF16, workspace, stream));
+}
+
+bitnet_status bitnet_residual_norm(const bitnet_residual* args, hipStream_t stream) {
+  if (!args) return BITNET_ERR_NULL;
+  const bitnet_residual& r = *args;
+  if (!valid_dtype(r.y_dtype) || !valid_dtype(r.h_dtype) || (r.u && !valid_dtype(r.u_dtype)))
+    return BITNET_ERR_DTYPE;
+  if (r.M < 0 || r.M > kInt32Max || r.K < 1 || r.K > kInt32Max ||
+      (r.gate && r.gate_stride != 0 && r.gate_stride < r.K) || !finite(r.scale) ||
+      !finite(r.eps) || r.eps < 0.0f)
+    return BITNET_ERR_SHAPE;
+  if (r.M == 0) return BITNET_OK;
+  if (!r.y || !r.h || !r.h_out || (r.x_q != nullptr) != (r.x_scale != nullptr))
+    return BITNET_ERR_NULL;
+  if (!aligned(r.y, esize(r.y_dtype)) || !aligned(r.h, esize(r.h_dtype)) ||
+      !aligned(r.gate, esize(r.y_dtype)) || !aligned(r.h_out, esize(r.h_dtype)) ||
+      (r.u && !aligned(r.u, esize(r.u_dtype))) || !aligned(r.post_weight, 4) ||
+      !aligned(r.pre_weight, 4) || !aligned(r.x_scale, 4))
+    return BITNET_ERR_ALIGN;
+  const bitnet::ResidualArgs a{r.y,   r.h,       r.gate, r.h_out,       r.u,     r.post_weight,
+                               r.pre_weight, r.x_q, r.x_scale, r.K, r.gate ? r.gate_stride : 0,
+                               r.scale, r.eps};
+  return from_hip(bitnet::launch_residual(a, r.y_dtype == BITNET_BF16, r.h_dtype == BITNET_BF16,
+                                          r.u && r.u_dtype == BITNET_BF16, r.M, stream));
 }
 
 }  // extern "C"
