@@ -1,0 +1,506 @@
+// Attention over the paged 8-bit cache for few query rows: single tokens, drafted
+// tokens (long ones: attn_prompt.hip).
+//
+// Query row i of a sequence with n new rows and len cached tokens has position
+// pos = len - n + i and sees the keys j with max(0, pos - window + 1) <= j <= pos
+// (window 0: from 0).  With codes kc, vc and the page's scales dk, dv:
+//   s_j = scale dk (q . kc_j),  out = sum_j e^(s_j - m) dv vc_j / sum_j e^(s_j - m),
+//   lse = m + ln sum_j e^(s_j - m).
+// A row without keys gives zeros and lse = -inf; a page id outside the cache holds
+// no keys.
+//
+// Bound by memory: every visible code is read once.  The codes go from memory to
+// the int8 matrix cores as they are, with no conversion and no LDS: it is the other
+// operand that is turned into 8-bit digits, a query row (once) and the weights of a
+// step (16 a lane).  A value x with |x| <= X is held as the integer
+// v = rne(x V / X), V = 127 * 256^(ND - 1), in ND signed base-256 digits, each with
+// its own product; the int32 sums are exact.  ND = 2 (bf16 in or out) holds the
+// queries to 2^-16 of their row's largest value and the weights to 2^-16 of the
+// row's largest, finer than bf16's 2^-9 of each; ND = 3 (fp32 in and out) to 2^-24.
+// Converting the codes to 16-bit floats instead would take 320 vector instructions
+// a lane and step of 64 keys, the digits take about 60.
+//
+// The page's scale dv joins the exponent: x_j = log2 e s_j + log2 dv, weights
+// 2^(x_j - max x), so that the weights' fixed-point range fits the largest product
+// whatever the pages' scales are; the softmax sum takes each weight over its dv.
+//
+// A wave takes 64 keys a step.  Products: S[key][row] = K Q^T from 16-key tiles,
+// where row r of tile t reads key 16 (r / 4) + 4 t + r % 4, so that the lane with
+// row column c and quarter g (lanes 16 g ..) ends up with the 16 consecutive keys
+// 16 g .. 16 g + 15: exactly the operand of O[dim][row] = V^T P^T, whose other side
+// is 16 consecutive bytes of the cache's value rows.  Weights never leave their lane.
+// Columns are (row, query head of the group) pairs, 16 a workgroup.  The four waves
+// of a workgroup take every fourth step and are joined in LDS; the keys of a
+// sequence are split over workgroups (attn_splits) and joined by a second kernel.
+#include "bitnet_internal.h"
+
+namespace bitnet {
+namespace {
+
+constexpr int kThreads = 256, kWaves = 4, kStep = 64, kCols = 16;
+
+// Fixed point of a digit count.
+template <int ND>
+struct Digits {
+  static constexpr float kTop = ND == 2 ? 32512.0f : 8323072.0f;   // 127 * 256^(ND - 1)
+};
+
+// Byte K of four dwords, a first.
+template <int K>
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  constexpr uint32_t sel = 0x0c0c0000u | ((4u + K) << 8) | K;
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, sel);
+  const uint32_t hi = __builtin_amdgcn_perm(d, c, sel);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
+// Digits (most significant first) of four values x >= -1, <= 1 times kTop.  With
+// u = v + 0x80 (ND 2) or v + 0x8080 (ND 3) byte j of u is digit j, its top bit
+// flipped for all but the highest.
+template <int ND>
+__device__ __forceinline__ void digits4(const float x[4], uint32_t out[ND]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (ND == 2)   // one addition rounds to nearest even and adds 0x80 (see rne_bits)
+      u[j] = __float_as_uint(__fadd_rn(__fmul_rn(x[j], Digits<2>::kTop), kRneMagic + 128.0f));
+    else
+      u[j] = (uint32_t)((int)rintf(__fmul_rn(x[j], Digits<3>::kTop)) + 0x8080);
+  }
+  out[ND - 1] = bytes4<0>(u[0], u[1], u[2], u[3]) ^ 0x80808080u;
+  out[ND - 2] = bytes4<1>(u[0], u[1], u[2], u[3]) ^ (ND == 3 ? 0x80808080u : 0u);
+  if (ND == 3) out[0] = bytes4<2>(u[0], u[1], u[2], u[3]);
+}
+
+// The number that ND int32 digit sums stand for.
+template <int ND>
+__device__ __forceinline__ float joined(const int d[ND]) {
+  const float t = (float)((d[0] << 8) + d[1]);   // |digit sum| < 2^22: exact in int32
+  return ND == 2 ? t : __builtin_fmaf(t, 256.0f, (float)d[ND - 1]);
+}
+
+// max / sum over the four 16-lane rows of the wave (lanes with equal lane % 16)
+__device__ __forceinline__ float rows_max(float v) {
+  const uint32_t u = __float_as_uint(v);
+  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const float w = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(w), __float_as_uint(w), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float rows_sum(float v) {
+  const uint32_t u = __float_as_uint(v);
+  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const float w = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(w), __float_as_uint(w), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// The part of a sequence's steps that split s of `splits` takes: [lo, hi) of the
+// steps [first, last).  Parts are equal and at least kMinSteps long, so that a short
+// sequence uses few of them.
+constexpr int kMinSteps = 4;
+__device__ __forceinline__ int split_len(int steps, int splits) {
+  return max((steps + splits - 1) / splits, kMinSteps);
+}
+
+// What one workgroup works on: columns [c0, c0 + nc) of a sequence's rows x group.
+struct Tile {
+  SeqSpan sp;
+  int c0, nc;              // nc <= 0: nothing
+  int step0, steps;        // 64-key steps that the tile's rows see
+};
+__device__ __forceinline__ Tile tile_of(const KvBatch& b, int seq, int ct, int group, int window) {
+  Tile t;
+  t.sp = seq_span(b, seq);
+  t.c0 = ct * kCols;
+  t.nc = min(min(t.sp.n, b.max_new) * group - t.c0, kCols);
+  const int p0 = t.sp.first + t.c0 / group;                       // first and last row's positions
+  const int p1 = t.sp.first + (t.c0 + max(t.nc, 1) - 1) / group;
+  const int lo = window > 0 ? max(p0 - window + 1, 0) : 0;
+  t.step0 = lo / kStep;
+  t.steps = p1 < lo ? 0 : p1 / kStep + 1 - t.step0;
+  return t;
+}
+
+template <int DP, int ND, bool QB, bool OB>
+__global__ __launch_bounds__(kThreads) void attn_decode_kernel(
+    const KvCache c, const KvBatch b, const AttnArgs a, int group, int page_shift, int col_tiles,
+    int splits, int part_cols, float* __restrict__ part) {
+  constexpr int KC = DP / 64, DT = DP / 16, HT = DT < 8 ? DT : 8;   // dims joined at a time: 16 HT
+  __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
+  __shared__ float so[kWaves][kCols][16 * HT + 4];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 15, g = lane >> 4;
+  int unit = blockIdx.x;
+  const int split = unit % splits;
+  unit /= splits;
+  const int ct = unit % col_tiles;
+  const int head = unit / col_tiles % c.kv_heads;
+  const int seq = unit / col_tiles / c.kv_heads;
+  const Tile tile = tile_of(b, seq, ct, group, a.window);
+  if (tile.nc <= 0) return;
+  const int len_split = split_len(tile.steps, splits);
+  const int s_lo = split * len_split, s_hi = min(s_lo + len_split, tile.steps);
+  if (split > 0 && s_lo >= s_hi) return;
+  const bool alone = tile.steps <= len_split;   // the only split of this tile
+
+  const int D = c.head_dim, P = c.page;
+  const int cc = tile.c0 + min(col, tile.nc - 1);
+  const int row = cc / group;
+  const int64_t t_row = tile.sp.s0 + row;
+  const int q_head = head * group + (cc - row * group);
+  const int pos = tile.sp.first + row;
+  const int from = a.window > 0 ? max(pos - a.window + 1, 0) : 0;   // visible: from .. pos
+
+  // queries: digits of dims 64 kc + 16 g .. + 15 of the lane's column
+  v4i qd[ND][KC];
+  float qscale;
+  {
+    float q[KC][16];
+    float amax = 0.0f;
+    const int64_t base = t_row * a.q_stride + (int64_t)q_head * D;
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc) {
+      const int d0 = kc * 64 + g * 16;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        q[kc][j] = 0.0f;
+        if (d0 < D)
+          q[kc][j] = QB ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(a.q)[base + d0 + j])
+                        : reinterpret_cast<const float*>(a.q)[base + d0 + j];
+        amax = fmaxf(amax, fabsf(q[kc][j]));
+      }
+    }
+    amax = rows_max(amax);
+    const float up = amax < 0x1p-64f ? 0x1p64f : 1.0f;   // keeps 1 / amax finite
+    const float inv = amax > 0.0f ? 1.0f / (amax * up) : 0.0f;
+    qscale = amax / Digits<ND>::kTop * a.scale * 1.44269504088896340736f;
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(__fmul_rn(q[kc][4 * w + j], up), inv);
+        uint32_t d[ND];
+        digits4<ND>(x, d);
+#pragma unroll
+        for (int n = 0; n < ND; ++n) qd[n][kc][w] = (int)d[n];
+      }
+  }
+
+  // page ids of the groups of 16 keys that the lane reads: keys of group col / 4,
+  // values of group g
+  const int last = max(tile.sp.len - 1, 0);
+  const int32_t* table = b.table + (int64_t)seq * b.width;
+  auto page_of = [&](int step, int quarter) -> int {
+    const int j = min(step * kStep + quarter * 16, last);
+    return table[j >> page_shift];
+  };
+  int64_t koff[KC];   // clamped: dims past the head read dim 0 (their query digits are 0)
+#pragma unroll
+  for (int kc = 0; kc < KC; ++kc) koff[kc] = kc * 64 + g * 16 < D ? kc * 64 + g * 16 : 0;
+  v4i kr[4][KC], vr[DT];
+  auto load_k = [&](int step, int pid) {
+    const int64_t p = (uint32_t)pid < (uint32_t)c.pages ? pid : 0;
+    const int slot = (step * kStep + (col >> 2) * 16) & (P - 1);
+    const int8_t* at = c.k + ((p * c.kv_heads + head) * P + slot + (col & 3)) * D;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int kc = 0; kc < KC; ++kc)
+        kr[t][kc] = *reinterpret_cast<const v4i*>(at + 4 * t * D + koff[kc]);
+  };
+  auto load_v = [&](int step, int pid) {
+    const int64_t p = (uint32_t)pid < (uint32_t)c.pages ? pid : 0;
+    const int slot = (step * kStep + g * 16) & (P - 1);
+    const int8_t* at = c.v + (p * c.kv_heads + head) * P * D + slot;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+      vr[dt] = *reinterpret_cast<const v4i*>(at + min(16 * dt + col, D - 1) * P);
+  };
+
+  float m = -INFINITY, l = 0.0f;
+  float o[DT][4];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[dt][i] = 0.0f;
+
+  const int s_begin = tile.step0 + s_lo + wave, s_end = tile.step0 + s_hi;
+  int pid_v = 0, pid_k1 = 0, pid_v1 = 0;   // this step's, the next one's
+  float dk = 0.0f, dv = 1.0f;
+  auto scales = [&](int pid) {
+    const int64_t at = (int64_t)((uint32_t)pid < (uint32_t)c.pages ? pid : 0) * c.kv_heads + head;
+    dk = c.k_scale[at];
+    dv = c.v_scale[at];
+  };
+  if (s_begin < s_end) {
+    const int pk = page_of(s_begin, col >> 2);
+    pid_v = page_of(s_begin, g);
+    pid_k1 = page_of(s_begin + kWaves, col >> 2);
+    pid_v1 = page_of(s_begin + kWaves, g);
+    load_k(s_begin, pk);
+    scales(pid_v);
+    load_v(s_begin, pid_v);
+  }
+  for (int step = s_begin; step < s_end; step += kWaves) {
+    const bool more = step + kWaves < s_end;
+    float x[4][4];   // the products first, as numbers
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      v4i s[ND];
+#pragma unroll
+      for (int n = 0; n < ND; ++n) {
+        s[n] = (v4i){0, 0, 0, 0};
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc)
+          s[n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kr[t][kc], qd[n][kc], s[n], 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int d[ND];
+#pragma unroll
+        for (int n = 0; n < ND; ++n) d[n] = s[n][i];
+        x[t][i] = joined<ND>(d);
+      }
+    }
+    if (more) load_k(step + kWaves, pid_k1);
+
+    // x = log2 e s + log2 dv of the lane's 16 keys; -inf where the row sees none
+    const int j0 = step * kStep + g * 16;
+    const bool there = (uint32_t)pid_v < (uint32_t)c.pages;
+    const float rdv = there && j0 <= pos && j0 + 15 >= from ? 1.0f / dv : 0.0f;
+    const float ck = qscale * dk, lv = __builtin_amdgcn_logf(dv);   // log2
+    const int hi = there ? pos - j0 : -1, lo = from - j0;   // visible: lo <= key <= hi
+    float mx = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float y = __builtin_fmaf(x[t][i], ck, lv);
+        x[t][i] = 4 * t + i <= hi && 4 * t + i >= lo ? y : -INFINITY;
+        mx = fmaxf(mx, x[t][i]);
+      }
+    mx = fmaxf(rows_max(mx), m);
+    const float ref = mx == -INFINITY ? 0.0f : mx;
+    const float alpha = __builtin_amdgcn_exp2f(m - ref);
+    m = mx;
+    float sum = 0.0f;
+    v4i pd[ND];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[t][i] = __builtin_amdgcn_exp2f(x[t][i] - ref);
+        sum += x[t][i];
+      }
+      uint32_t d[ND];
+      digits4<ND>(x[t], d);
+#pragma unroll
+      for (int n = 0; n < ND; ++n) pd[n][t] = (int)d[n];
+    }
+    l = __builtin_fmaf(l, alpha, sum * rdv);
+    if (more) scales(pid_v1);
+
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      v4i y[ND];
+#pragma unroll
+      for (int n = 0; n < ND; ++n)
+        y[n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vr[dt], pd[n], (v4i){0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int d[ND];
+#pragma unroll
+        for (int n = 0; n < ND; ++n) d[n] = y[n][i];
+        o[dt][i] = __builtin_fmaf(o[dt][i], alpha, joined<ND>(d));
+      }
+    }
+    if (more) {
+      load_v(step + kWaves, pid_v1);
+      pid_v = pid_v1;
+      pid_k1 = page_of(step + 2 * kWaves, col >> 2);
+      pid_v1 = page_of(step + 2 * kWaves, g);
+    }
+  }
+
+  // join the waves: each scales its sums to the common maximum
+  l = rows_sum(l);
+  if (g == 0) {
+    sm[wave][col] = m;
+    sl[wave][col] = l;
+  }
+  __syncthreads();
+  float top = sm[0][col], total = 0.0f;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm[w][col]);
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w)
+    total += sm[w][col] == -INFINITY ? 0.0f : sl[w][col] * __builtin_amdgcn_exp2f(sm[w][col] - top);
+  const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+  const int64_t pu = alone ? 0 : ((int64_t)blockIdx.x * part_cols);
+#pragma unroll
+  for (int h0 = 0; h0 < DT; h0 += HT) {
+    if (h0 > 0) __syncthreads();
+    if (col < tile.nc)
+#pragma unroll
+      for (int dt = 0; dt < HT; ++dt)
+        *reinterpret_cast<float4*>(&so[wave][col][16 * dt + 4 * g]) =
+            make_float4(o[h0 + dt][0] * f, o[h0 + dt][1] * f, o[h0 + dt][2] * f, o[h0 + dt][3] * f);
+    __syncthreads();
+    // 4 dims a thread
+    const int nd = min(16 * HT, D - 16 * h0);
+    for (int e = tid; e < tile.nc * (nd / 4); e += kThreads) {
+      const int ec = e / (nd / 4), d = (e - ec * (nd / 4)) * 4;
+      float4 y = *reinterpret_cast<const float4*>(&so[0][ec][d]);
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) {
+        const float4 z = *reinterpret_cast<const float4*>(&so[w][ec][d]);
+        y.x += z.x;
+        y.y += z.y;
+        y.z += z.z;
+        y.w += z.w;
+      }
+      if (alone) {
+        float et = sm[0][ec], el = 0.0f;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) et = fmaxf(et, sm[w][ec]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+          el += sm[w][ec] == -INFINITY ? 0.0f : sl[w][ec] * __builtin_amdgcn_exp2f(sm[w][ec] - et);
+        const float r = el > 0.0f ? 1.0f / (el * Digits<ND>::kTop) : 0.0f;
+        const int oc = tile.c0 + ec, orow = oc / group;
+        const int64_t at = ((tile.sp.s0 + orow) * a.q_heads + head * group + (oc - orow * group)) * D +
+                           16 * h0 + d;
+        if (OB)
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+              make_uint2(bf16x2_rne(y.x * r, y.y * r), bf16x2_rne(y.z * r, y.w * r));
+        else
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) =
+              make_float4(y.x * r, y.y * r, y.z * r, y.w * r);
+      } else {
+        *reinterpret_cast<float4*>(part + (pu + ec) * (D + 4) + 4 + 16 * h0 + d) = y;
+      }
+    }
+  }
+  if (wave == 0 && g == 0 && col < tile.nc) {
+    if (!alone)
+      *reinterpret_cast<float2*>(part + (pu + col) * (D + 4)) = make_float2(top, total);
+    else if (a.lse)
+      a.lse[t_row * a.q_heads + q_head] =
+          total > 0.0f ? 0.69314718055994530942f * (top + __builtin_amdgcn_logf(total)) : -INFINITY;
+  }
+}
+
+// Joins the splits of one tile: the same formula over their maxima and sums, always in
+// the order of the splits.
+template <int ND, bool OB>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(const KvCache c, const KvBatch b,
+                                                             const AttnArgs a, int group,
+                                                             int col_tiles, int splits,
+                                                             int part_cols,
+                                                             const float* __restrict__ part) {
+  int unit = blockIdx.x;
+  const int ct = unit % col_tiles;
+  const int head = unit / col_tiles % c.kv_heads;
+  const int seq = unit / col_tiles / c.kv_heads;
+  const Tile tile = tile_of(b, seq, ct, group, a.window);
+  if (tile.nc <= 0) return;
+  const int len_split = split_len(tile.steps, splits);
+  if (tile.steps <= len_split) return;   // written by its only split
+  const int used = (tile.steps + len_split - 1) / len_split;
+  const int D = c.head_dim, tid = threadIdx.x;
+  const int64_t stride = (int64_t)part_cols * (D + 4);
+  for (int e = tid; e < tile.nc * (D / 4); e += kThreads) {
+    const int col = e / (D / 4), d = (e - col * (D / 4)) * 4;
+    const float* p = part + (int64_t)unit * splits * stride + (int64_t)col * (D + 4);
+    float top = -INFINITY;
+    for (int s = 0; s < used; ++s) top = fmaxf(top, p[s * stride]);
+    float l = 0.0f;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < used; ++s) {
+      const float2 ml = *reinterpret_cast<const float2*>(p + s * stride);
+      const float4 z = *reinterpret_cast<const float4*>(p + s * stride + 4 + d);
+      const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+      l = __builtin_fmaf(ml.y, f, l);
+      y.x = __builtin_fmaf(z.x, f, y.x);
+      y.y = __builtin_fmaf(z.y, f, y.y);
+      y.z = __builtin_fmaf(z.z, f, y.z);
+      y.w = __builtin_fmaf(z.w, f, y.w);
+    }
+    const float r = l > 0.0f ? 1.0f / (l * Digits<ND>::kTop) : 0.0f;
+    const int oc = tile.c0 + col, row = oc / group;
+    const int64_t at = (tile.sp.s0 + row) * a.q_heads + head * group + (oc - row * group);
+    if (OB)
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at * D + d) =
+          make_uint2(bf16x2_rne(y.x * r, y.y * r), bf16x2_rne(y.z * r, y.w * r));
+    else
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at * D + d) =
+          make_float4(y.x * r, y.y * r, y.z * r, y.w * r);
+    if (d == 0 && a.lse)
+      a.lse[at] = l > 0.0f ? 0.69314718055994530942f * (top + __builtin_amdgcn_logf(l)) : -INFINITY;
+  }
+}
+
+// ND = 3 for fp32 in and out, else 2.
+template <int DP>
+const void* pick_decode(bool qb, bool ob) {
+  return qb ? (ob ? (const void*)attn_decode_kernel<DP, 2, true, true>
+                  : (const void*)attn_decode_kernel<DP, 2, true, false>)
+            : (ob ? (const void*)attn_decode_kernel<DP, 2, false, true>
+                  : (const void*)attn_decode_kernel<DP, 3, false, false>);
+}
+
+// Splits of a launch: enough workgroups for the chip at two per compute unit, and
+// four times that where sequences may differ in length, but none shorter than
+// kMinSteps steps.
+int plan_splits(const KvCache& c, const KvBatch& b, int col_tiles) {
+  const int64_t units = (int64_t)b.seqs * c.kv_heads * col_tiles;
+  const int64_t steps = ((int64_t)b.max_len + kStep - 1) / kStep;
+  const int64_t want = ((b.seqs > 1 ? 2048 : 512) + units - 1) / units;
+  const int64_t most = (steps + kMinSteps - 1) / kMinSteps;
+  const int64_t s = want < most ? want : most;
+  return s < 1 ? 1 : (int)s;
+}
+
+}  // namespace
+
+size_t attn_decode_workspace(const KvCache& c, const KvBatch& b, int q_heads) {
+  const int64_t cols = (int64_t)b.max_new * (q_heads / c.kv_heads);
+  const int col_tiles = (int)((cols + kCols - 1) / kCols);
+  const int splits = plan_splits(c, b, col_tiles);
+  if (splits == 1) return 0;
+  const int64_t part_cols = cols < kCols ? cols : kCols;
+  return (size_t)b.seqs * c.kv_heads * col_tiles * splits * part_cols * (c.head_dim + 4) * sizeof(float);
+}
+
+hipError_t launch_attn_decode(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool q_bf16,
+                              bool out_bf16, void* workspace, hipStream_t s) {
+  const int group = a.q_heads / c.kv_heads;
+  const int64_t cols = (int64_t)b.max_new * group;
+  const int64_t tiles = (cols + kCols - 1) / kCols;
+  if ((int64_t)b.seqs * c.kv_heads * tiles > 2147483647) return hipErrorInvalidValue;
+  int col_tiles = (int)tiles, splits = plan_splits(c, b, col_tiles);
+  int part_cols = (int)(cols < kCols ? cols : kCols);
+  const int64_t grid = (int64_t)b.seqs * c.kv_heads * col_tiles * splits;
+  if (grid > 2147483647) return hipErrorInvalidValue;
+  int shift = 4;
+  while ((1 << shift) < c.page) ++shift;
+  float* part = static_cast<float*>(workspace);
+  const int dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
+  const void* kern = dp == 64 ? pick_decode<64>(q_bf16, out_bf16)
+                     : dp == 128 ? pick_decode<128>(q_bf16, out_bf16) : pick_decode<256>(q_bf16, out_bf16);
+  int grp = group;
+  void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&grp, (void*)&shift, (void*)&col_tiles,
+                  (void*)&splits, (void*)&part_cols, (void*)&part};
+  hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(kThreads), args, 0, s);
+  if (e != hipSuccess || splits == 1) return e;
+  const void* join = out_bf16 ? (const void*)attn_join_kernel<2, true>
+                     : q_bf16 ? (const void*)attn_join_kernel<2, false>
+                              : (const void*)attn_join_kernel<3, false>;
+  void* jargs[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&grp, (void*)&col_tiles, (void*)&splits,
+                   (void*)&part_cols, (void*)&part};
+  return hipLaunchKernel(join, dim3((unsigned)(grid / splits)), dim3(kThreads), jargs, 0, s);
+}
+
+}  // namespace bitnet
