@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbitnet_mi355x.so")
 SOURCES = ("api.hip", "wq.hip", "aq.hip", "gemv.hip", "gemm.hip", "lut.hip", "chain.hip",
-           "kvcache.hip", "attn.hip", "attn_decode.hip", "residual.hip")
+           "kvcache.hip", "attn.hip", "attn_decode.hip", "attn_prompt.hip",
+           "residual.hip")
 # bench-only diagnostics (int8 matrix-core rate, HBM read rates, launch cost), their
 # own library: not part of the ABI
 PROBE_SRCS = [os.path.join(PKG, "bench_probe", f) for f in ("mfma_probe.hip", "hbm_probe.hip")]
@@ -46,7 +47,8 @@ FLAGS = [
 # stay in arch VGPRs, where the softmax reads them: in AGPRs the 128-wide decode
 # kernel needs 310 registers instead of 250 (one wave per SIMD instead of two).
 EXTRA = {"gemv.hip": ("-mllvm", "-amdgpu-kernarg-preload-count=10"),
-         "attn_decode.hip": ("-mllvm", "-amdgpu-mfma-vgpr-form=1")}
+         "attn_decode.hip": ("-mllvm", "-amdgpu-mfma-vgpr-form=1"),
+         "attn_prompt.hip": ("-mllvm", "-amdgpu-mfma-vgpr-form=1")}
 
 
 def _run(cmd):

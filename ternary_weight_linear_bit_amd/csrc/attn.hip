@@ -1,15 +1,90 @@
-// Attention over the paged 8-bit cache: which kernel a call takes.
-#include "bitnet_internal.h"
+// Attention over the paged 8-bit cache: which kernel a call takes, and the join of
+// the parts that either of them leaves.
+#include "attn_internal.h"
 
 namespace bitnet {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Joins the parts of one tile: the softmax formula over their maxima and sums, always
+// in the order of the parts.  One workgroup a tile; a thread takes 4 dims of a column.
+template <bool OB>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(const KvCache c, const KvBatch b,
+                                                             const AttnArgs a,
+                                                             const AttnPlan plan, float unit,
+                                                             const float* __restrict__ part) {
+  const int u = blockIdx.x;
+  const int ct = u % plan.tiles;
+  const int head = u / plan.tiles % c.kv_heads;
+  const int seq = u / plan.tiles / c.kv_heads;
+  const AttnTile tile = attn_tile(b, seq, ct, plan.cols, plan.group, a.window);
+  if (tile.nc <= 0) return;
+  const int each = attn_part(tile.steps, plan.splits, plan.least);
+  if (tile.steps <= each) return;   // written by its only part
+  const int used = (tile.steps + each - 1) / each;
+  const int D = c.head_dim;
+  const int64_t stride = (int64_t)plan.part_cols * (D + 4);
+  for (int e = threadIdx.x; e < tile.nc * (D / 4); e += kThreads) {
+    const int col = e / (D / 4), d = (e - col * (D / 4)) * 4;
+    const float* p = part + (int64_t)u * plan.splits * stride + (int64_t)col * (D + 4);
+    float top = -INFINITY;
+    for (int s = 0; s < used; ++s) top = fmaxf(top, p[s * stride]);
+    float l = 0.0f;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < used; ++s) {
+      const float2 ml = *reinterpret_cast<const float2*>(p + s * stride);
+      const float4 z = *reinterpret_cast<const float4*>(p + s * stride + 4 + d);
+      const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+      l = __builtin_fmaf(ml.y, f, l);
+      y.x = __builtin_fmaf(z.x, f, y.x);
+      y.y = __builtin_fmaf(z.y, f, y.y);
+      y.z = __builtin_fmaf(z.z, f, y.z);
+      y.w = __builtin_fmaf(z.w, f, y.w);
+    }
+    const float r = l > 0.0f ? 1.0f / (l * unit) : 0.0f;
+    const int oc = tile.c0 + col, row = oc / plan.group;
+    const int64_t at =
+        (tile.sp.s0 + row) * (int64_t)a.q_heads + head * plan.group + (oc - row * plan.group);
+    if (OB)
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at * D + d) =
+          make_uint2(bf16x2_rne(y.x * r, y.y * r), bf16x2_rne(y.z * r, y.w * r));
+    else
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at * D + d) =
+          make_float4(y.x * r, y.y * r, y.z * r, y.w * r);
+    if (d == 0 && a.lse)
+      a.lse[at] = l > 0.0f ? 0.69314718055994530942f * (top + __builtin_amdgcn_logf(l)) : -INFINITY;
+  }
+}
+
+// Columns (rows x query heads of a kv head) from which the prompt kernel is taken.
+constexpr int64_t kPromptCols = 64;
+bool many_rows(const KvCache& c, const KvBatch& b, int q_heads) {
+  return (int64_t)b.max_new * (q_heads / c.kv_heads) >= kPromptCols;
+}
+
+}  // namespace
+
+hipError_t launch_attn_join(const KvCache& c, const KvBatch& b, const AttnArgs& a,
+                            const AttnPlan& p, float unit, bool out_bf16, const float* part,
+                            hipStream_t s) {
+  void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&p, (void*)&unit, (void*)&part};
+  return hipLaunchKernel(out_bf16 ? (const void*)attn_join_kernel<true>
+                                  : (const void*)attn_join_kernel<false>,
+                         dim3((unsigned)((int64_t)b.seqs * c.kv_heads * p.tiles)), dim3(kThreads), args,
+                         0, s);
+}
 
 size_t attention_workspace_bytes(const KvCache& c, const KvBatch& b, int q_heads) {
-  return attn_decode_workspace(c, b, q_heads);
+  return attn_workspace(c, b, many_rows(c, b, q_heads) ? attn_prompt_plan(c, b, q_heads)
+                                                       : attn_decode_plan(c, b, q_heads));
 }
 
 hipError_t launch_attention(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool q_bf16,
                             bool out_bf16, void* workspace, hipStream_t s) {
-  return launch_attn_decode(c, b, a, q_bf16, out_bf16, workspace, s);
+  if (many_rows(c, b, a.q_heads))
+    return launch_attn_prompt(c, b, a, attn_prompt_plan(c, b, a.q_heads), q_bf16, out_bf16, workspace, s);
+  return launch_attn_decode(c, b, a, attn_decode_plan(c, b, a.q_heads), q_bf16, out_bf16, workspace, s);
 }
 
 }  // namespace bitnet

@@ -32,12 +32,12 @@
 // Columns are (row, query head of the group) pairs, 16 a workgroup.  The four waves
 // of a workgroup take every fourth step and are joined in LDS; the keys of a
 // sequence are split over workgroups (attn_splits) and joined by a second kernel.
-#include "bitnet_internal.h"
+#include "attn_internal.h"
 
 namespace bitnet {
 namespace {
 
-constexpr int kThreads = 256, kWaves = 4, kStep = 64, kCols = 16;
+constexpr int kThreads = 256, kWaves = 4, kStep = kAttnStep, kCols = 16;
 
 // Fixed point of a digit count.
 template <int ND>
@@ -95,53 +95,27 @@ __device__ __forceinline__ float rows_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// The part of a sequence's steps that split s of `splits` takes: [lo, hi) of the
-// steps [first, last).  Parts are equal and at least kMinSteps long, so that a short
-// sequence uses few of them.
-constexpr int kMinSteps = 4;
-__device__ __forceinline__ int split_len(int steps, int splits) {
-  return max((steps + splits - 1) / splits, kMinSteps);
-}
-
-// What one workgroup works on: columns [c0, c0 + nc) of a sequence's rows x group.
-struct Tile {
-  SeqSpan sp;
-  int c0, nc;              // nc <= 0: nothing
-  int step0, steps;        // 64-key steps that the tile's rows see
-};
-__device__ __forceinline__ Tile tile_of(const KvBatch& b, int seq, int ct, int group, int window) {
-  Tile t;
-  t.sp = seq_span(b, seq);
-  t.c0 = ct * kCols;
-  t.nc = min(min(t.sp.n, b.max_new) * group - t.c0, kCols);
-  const int p0 = t.sp.first + t.c0 / group;                       // first and last row's positions
-  const int p1 = t.sp.first + (t.c0 + max(t.nc, 1) - 1) / group;
-  const int lo = window > 0 ? max(p0 - window + 1, 0) : 0;
-  t.step0 = lo / kStep;
-  t.steps = p1 < lo ? 0 : p1 / kStep + 1 - t.step0;
-  return t;
-}
-
 template <int DP, int ND, bool QB, bool OB>
 __global__ __launch_bounds__(kThreads) void attn_decode_kernel(
-    const KvCache c, const KvBatch b, const AttnArgs a, int group, int page_shift, int col_tiles,
-    int splits, int part_cols, float* __restrict__ part) {
+    const KvCache c, const KvBatch b, const AttnArgs a, const AttnPlan plan,
+    float* __restrict__ part) {
   constexpr int KC = DP / 64, DT = DP / 16, HT = DT < 8 ? DT : 8;   // dims joined at a time: 16 HT
   __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
   __shared__ float so[kWaves][kCols][16 * HT + 4];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 15, g = lane >> 4;
   int unit = blockIdx.x;
-  const int split = unit % splits;
-  unit /= splits;
-  const int ct = unit % col_tiles;
-  const int head = unit / col_tiles % c.kv_heads;
-  const int seq = unit / col_tiles / c.kv_heads;
-  const Tile tile = tile_of(b, seq, ct, group, a.window);
+  const int split = unit % plan.splits;
+  unit /= plan.splits;
+  const int ct = unit % plan.tiles;
+  const int head = unit / plan.tiles % c.kv_heads;
+  const int seq = unit / plan.tiles / c.kv_heads;
+  const int group = plan.group;
+  const AttnTile tile = attn_tile(b, seq, ct, kCols, group, a.window);
   if (tile.nc <= 0) return;
-  const int len_split = split_len(tile.steps, splits);
-  const int s_lo = split * len_split, s_hi = min(s_lo + len_split, tile.steps);
+  const int each = attn_part(tile.steps, plan.splits, plan.least);
+  const int s_lo = split * each, s_hi = min(s_lo + each, tile.steps);
   if (split > 0 && s_lo >= s_hi) return;
-  const bool alone = tile.steps <= len_split;   // the only split of this tile
+  const bool alone = tile.steps <= each;   // the only part of this tile
 
   const int D = c.head_dim, P = c.page;
   const int cc = tile.c0 + min(col, tile.nc - 1);
@@ -161,14 +135,9 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(
 #pragma unroll
     for (int kc = 0; kc < KC; ++kc) {
       const int d0 = kc * 64 + g * 16;
+      load_dims<QB, 16>(a.q, base, d0, D, q[kc]);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        q[kc][j] = 0.0f;
-        if (d0 < D)
-          q[kc][j] = QB ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(a.q)[base + d0 + j])
-                        : reinterpret_cast<const float*>(a.q)[base + d0 + j];
-        amax = fmaxf(amax, fabsf(q[kc][j]));
-      }
+      for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(q[kc][j]));
     }
     amax = rows_max(amax);
     const float up = amax < 0x1p-64f ? 0x1p64f : 1.0f;   // keeps 1 / amax finite
@@ -194,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(
   const int32_t* table = b.table + (int64_t)seq * b.width;
   auto page_of = [&](int step, int quarter) -> int {
     const int j = min(step * kStep + quarter * 16, last);
-    return table[j >> page_shift];
+    return table[j >> plan.page_shift];
   };
   int64_t koff[KC];   // clamped: dims past the head read dim 0 (their query digits are 0)
 #pragma unroll
@@ -338,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(
   for (int w = 0; w < kWaves; ++w)
     total += sm[w][col] == -INFINITY ? 0.0f : sl[w][col] * __builtin_amdgcn_exp2f(sm[w][col] - top);
   const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-  const int64_t pu = alone ? 0 : ((int64_t)blockIdx.x * part_cols);
+  const int64_t pu = (int64_t)blockIdx.x * plan.part_cols;
 #pragma unroll
   for (int h0 = 0; h0 < DT; h0 += HT) {
     if (h0 > 0) __syncthreads();
@@ -392,56 +361,6 @@ __global__ __launch_bounds__(kThreads) void attn_decode_kernel(
   }
 }
 
-// Joins the splits of one tile: the same formula over their maxima and sums, always in
-// the order of the splits.
-template <int ND, bool OB>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(const KvCache c, const KvBatch b,
-                                                             const AttnArgs a, int group,
-                                                             int col_tiles, int splits,
-                                                             int part_cols,
-                                                             const float* __restrict__ part) {
-  int unit = blockIdx.x;
-  const int ct = unit % col_tiles;
-  const int head = unit / col_tiles % c.kv_heads;
-  const int seq = unit / col_tiles / c.kv_heads;
-  const Tile tile = tile_of(b, seq, ct, group, a.window);
-  if (tile.nc <= 0) return;
-  const int len_split = split_len(tile.steps, splits);
-  if (tile.steps <= len_split) return;   // written by its only split
-  const int used = (tile.steps + len_split - 1) / len_split;
-  const int D = c.head_dim, tid = threadIdx.x;
-  const int64_t stride = (int64_t)part_cols * (D + 4);
-  for (int e = tid; e < tile.nc * (D / 4); e += kThreads) {
-    const int col = e / (D / 4), d = (e - col * (D / 4)) * 4;
-    const float* p = part + (int64_t)unit * splits * stride + (int64_t)col * (D + 4);
-    float top = -INFINITY;
-    for (int s = 0; s < used; ++s) top = fmaxf(top, p[s * stride]);
-    float l = 0.0f;
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < used; ++s) {
-      const float2 ml = *reinterpret_cast<const float2*>(p + s * stride);
-      const float4 z = *reinterpret_cast<const float4*>(p + s * stride + 4 + d);
-      const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-      l = __builtin_fmaf(ml.y, f, l);
-      y.x = __builtin_fmaf(z.x, f, y.x);
-      y.y = __builtin_fmaf(z.y, f, y.y);
-      y.z = __builtin_fmaf(z.z, f, y.z);
-      y.w = __builtin_fmaf(z.w, f, y.w);
-    }
-    const float r = l > 0.0f ? 1.0f / (l * Digits<ND>::kTop) : 0.0f;
-    const int oc = tile.c0 + col, row = oc / group;
-    const int64_t at = (tile.sp.s0 + row) * a.q_heads + head * group + (oc - row * group);
-    if (OB)
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at * D + d) =
-          make_uint2(bf16x2_rne(y.x * r, y.y * r), bf16x2_rne(y.z * r, y.w * r));
-    else
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at * D + d) =
-          make_float4(y.x * r, y.y * r, y.z * r, y.w * r);
-    if (d == 0 && a.lse)
-      a.lse[at] = l > 0.0f ? 0.69314718055994530942f * (top + __builtin_amdgcn_logf(l)) : -INFINITY;
-  }
-}
-
 // ND = 3 for fp32 in and out, else 2.
 template <int DP>
 const void* pick_decode(bool qb, bool ob) {
@@ -451,56 +370,28 @@ const void* pick_decode(bool qb, bool ob) {
                   : (const void*)attn_decode_kernel<DP, 3, false, false>);
 }
 
-// Splits of a launch: enough workgroups for the chip at two per compute unit, and
-// four times that where sequences may differ in length, but none shorter than
-// kMinSteps steps.
-int plan_splits(const KvCache& c, const KvBatch& b, int col_tiles) {
-  const int64_t units = (int64_t)b.seqs * c.kv_heads * col_tiles;
-  const int64_t steps = ((int64_t)b.max_len + kStep - 1) / kStep;
-  const int64_t want = ((b.seqs > 1 ? 2048 : 512) + units - 1) / units;
-  const int64_t most = (steps + kMinSteps - 1) / kMinSteps;
-  const int64_t s = want < most ? want : most;
-  return s < 1 ? 1 : (int)s;
-}
-
 }  // namespace
 
-size_t attn_decode_workspace(const KvCache& c, const KvBatch& b, int q_heads) {
-  const int64_t cols = (int64_t)b.max_new * (q_heads / c.kv_heads);
-  const int col_tiles = (int)((cols + kCols - 1) / kCols);
-  const int splits = plan_splits(c, b, col_tiles);
-  if (splits == 1) return 0;
-  const int64_t part_cols = cols < kCols ? cols : kCols;
-  return (size_t)b.seqs * c.kv_heads * col_tiles * splits * part_cols * (c.head_dim + 4) * sizeof(float);
+// Two workgroups per compute unit, four times that where sequences may differ in
+// length; no part is shorter than one step a wave.
+AttnPlan attn_decode_plan(const KvCache& c, const KvBatch& b, int q_heads) {
+  return attn_plan(c, b, q_heads, kCols, 512, 2048, kWaves);
 }
 
-hipError_t launch_attn_decode(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool q_bf16,
-                              bool out_bf16, void* workspace, hipStream_t s) {
-  const int group = a.q_heads / c.kv_heads;
-  const int64_t cols = (int64_t)b.max_new * group;
-  const int64_t tiles = (cols + kCols - 1) / kCols;
-  if ((int64_t)b.seqs * c.kv_heads * tiles > 2147483647) return hipErrorInvalidValue;
-  int col_tiles = (int)tiles, splits = plan_splits(c, b, col_tiles);
-  int part_cols = (int)(cols < kCols ? cols : kCols);
-  const int64_t grid = (int64_t)b.seqs * c.kv_heads * col_tiles * splits;
+hipError_t launch_attn_decode(const KvCache& c, const KvBatch& b, const AttnArgs& a,
+                              const AttnPlan& p, bool q_bf16, bool out_bf16, void* workspace,
+                              hipStream_t s) {
+  const int64_t grid = (int64_t)b.seqs * c.kv_heads * p.tiles * p.splits;
   if (grid > 2147483647) return hipErrorInvalidValue;
-  int shift = 4;
-  while ((1 << shift) < c.page) ++shift;
   float* part = static_cast<float*>(workspace);
   const int dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
   const void* kern = dp == 64 ? pick_decode<64>(q_bf16, out_bf16)
                      : dp == 128 ? pick_decode<128>(q_bf16, out_bf16) : pick_decode<256>(q_bf16, out_bf16);
-  int grp = group;
-  void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&grp, (void*)&shift, (void*)&col_tiles,
-                  (void*)&splits, (void*)&part_cols, (void*)&part};
-  hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(kThreads), args, 0, s);
-  if (e != hipSuccess || splits == 1) return e;
-  const void* join = out_bf16 ? (const void*)attn_join_kernel<2, true>
-                     : q_bf16 ? (const void*)attn_join_kernel<2, false>
-                              : (const void*)attn_join_kernel<3, false>;
-  void* jargs[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&grp, (void*)&col_tiles, (void*)&splits,
-                   (void*)&part_cols, (void*)&part};
-  return hipLaunchKernel(join, dim3((unsigned)(grid / splits)), dim3(kThreads), jargs, 0, s);
+  void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&p, (void*)&part};
+  const hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(kThreads), args, 0, s);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const float unit = !q_bf16 && !out_bf16 ? Digits<3>::kTop : Digits<2>::kTop;
+  return launch_attn_join(c, b, a, p, unit, out_bf16, part, s);
 }
 
 }  // namespace bitnet

@@ -1,0 +1,438 @@
+// Attention over the paged 8-bit cache for many query rows: prompts, and parts of
+// prompts behind cached tokens.  Definition, and the kernel for few rows:
+// attn_decode.hip.
+//
+// Bound by the matrix cores and, beside them, the exponentials (one a pair of row
+// and key, at a quarter of the vector rate).  A workgroup takes 128 columns, (row,
+// query head of the group) pairs, 32 a wave; the four waves share each step of 64
+// keys in LDS.  The codes are turned into fp16 on their way there, exactly (a code's
+// byte becomes the low mantissa bits of 1024 + code + 128, one permute and half a
+// packed subtraction a value), once for all 128 columns: the int8 products of the
+// decode kernel would need two digits of the weights, 6 more vector instructions a
+// pair, at the same matrix rate.
+//   * Queries: scaled by a power of two to a largest value in [2^10, 2^11), then fp16
+//     (bf16 queries fit exactly); fp32 queries take two fp16 terms (22 bits).
+//   * Weights p = 2^(x - m + 7), x = log2 e s + log2 dv (the page's scale joins the
+//     exponent), rounded to fp16 (2^-12 of each, finer than bf16's 2^-9); for fp32 in
+//     and out two terms.  m follows the running maximum only when it grows by more
+//     than 2^8, so that the accumulators are seldom rescaled; p stays below 2^15.
+//   * Sums over keys and the softmax sum are fp32 (the latter of the unrounded p, over
+//     each page's dv).
+// Products: S[key][column] = K Q^T in 32 x 32 tiles, where row r of a tile reads key
+// 16 (r / 16) + 8 (r / 4 % 2) + 4 (r / 8 % 2) + r % 4: a lane's 16 results are then keys
+// 8 h .. 8 h + 7 and 16 + 8 h .. of its column (h = lane / 32), the operands of
+// O[dim][column] = V^T P^T as they stand, so the weights never leave their lane.
+// LDS rows are 16-byte groups permuted by the row's low bits (reads and writes of 8
+// lanes then fall on different banks).  Two buffers, one barrier a step; the next
+// step's codes are loaded while this one's are used.
+#include "attn_internal.h"
+
+namespace bitnet {
+namespace {
+
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+constexpr int kThreads = 256, kStep = kAttnStep, kCols = 128;
+// Byte offset of 16-byte group `at` of a key's row in LDS.
+template <int DP>
+__device__ __forceinline__ int k_group(int key, int at) {
+  const int f = DP == 64 ? key >> 1 : key;   // two 128-byte rows span the banks
+  return key * DP * 2 + ((at ^ f) & (DP / 8 - 1)) * 16;
+}
+__device__ __forceinline__ int v_group(int dim, int at) {
+  return dim * kStep * 2 + ((at ^ dim) & 7) * 16;
+}
+constexpr float kLift = 7.0f, kSlack = 8.0f;   // p <= 2^(kLift + kSlack)
+
+// Four codes as fp16 pairs.
+__device__ __forceinline__ void codes_to_h4(uint32_t w, uint32_t out[2]) {
+  const uint32_t u = w ^ 0x80808080u;   // code + 128
+  const v2h off = {(_Float16)1152.0f, (_Float16)1152.0f};
+  const v2h a = __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - off;
+  const v2h b = __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - off;
+  out[0] = __builtin_bit_cast(uint32_t, a);
+  out[1] = __builtin_bit_cast(uint32_t, b);
+}
+
+__device__ __forceinline__ uint32_t h2_of(float a, float b) {
+  const f32x2_t f = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, v2h));
+}
+__device__ __forceinline__ void h2_rest(uint32_t h, float& a, float& b) {
+  const v2h v = __builtin_bit_cast(v2h, h);
+  a -= (float)v[0];
+  b -= (float)v[1];
+}
+
+__device__ __forceinline__ float halves_max(float v) {
+  const uint32_t u = __float_as_uint(v);
+  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+__device__ __forceinline__ float halves_sum(float v) {
+  const uint32_t u = __float_as_uint(v);
+  auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ float lane_of(float v, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
+// QT / PT: fp16 terms of a query and of a weight.
+template <int DP, int QT, int PT, bool QB, bool OB>
+__global__ __launch_bounds__(kThreads) void attn_prompt_kernel(
+    const KvCache c, const KvBatch b, const AttnArgs a, const AttnPlan plan,
+    float* __restrict__ part) {
+  constexpr int KC = DP / 16, DT = DP / 32, NL = DP / 64;   // NL: 16-code loads of K (and of V) a thread
+  constexpr int kKBytes = kStep * DP * 2, kBuf = 2 * kKBytes;
+  extern __shared__ uint4 lds4[];
+  uint8_t* lds = reinterpret_cast<uint8_t*>(lds4);
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31, h = lane >> 5;
+
+  // kv heads run fastest (a head's workgroups then meet in few XCDs' L2), the last
+  // rows, which see most keys, start first
+  int unit = blockIdx.x;
+  const int head = unit % c.kv_heads;
+  unit /= c.kv_heads;
+  const int split = unit % plan.splits;
+  unit /= plan.splits;
+  const int seq = unit % b.seqs;
+  const int ct = plan.tiles - 1 - unit / b.seqs;
+  const int group = plan.group;
+  const AttnTile tile = attn_tile(b, seq, ct, kCols, group, a.window);
+  if (tile.nc <= 0) return;
+  const int each = attn_part(tile.steps, plan.splits, plan.least);
+  const int s_lo = split * each, s_hi = min(s_lo + each, tile.steps);
+  if (split > 0 && s_lo >= s_hi) return;
+  const bool alone = tile.steps <= each;
+
+  const int D = c.head_dim, P = c.page;
+  const bool live = wave * 32 + col < tile.nc;
+  const int cc = tile.c0 + min(wave * 32 + col, tile.nc - 1);
+  const int row = cc / group;
+  const int64_t t_row = tile.sp.s0 + row;
+  const int q_head = head * group + (cc - row * group);
+  const int pos = tile.sp.first + row;
+  const int from = a.window > 0 ? max(pos - a.window + 1, 0) : 0;   // visible: from .. pos
+  // positions of the wave's first and last columns (its mask-free steps)
+  const int pos_lo = __builtin_amdgcn_readlane(pos, 0), pos_hi = __builtin_amdgcn_readlane(pos, 31);
+  const int from_hi = __builtin_amdgcn_readlane(from, 31), from_lo = __builtin_amdgcn_readlane(from, 0);
+
+  // queries: dims 16 kc + 8 h .. + 7 of the lane's column
+  v8h q[QT][KC];
+  float qscale;
+  {
+    const int64_t base = t_row * a.q_stride + (int64_t)q_head * D;
+    auto load8 = [&](int d0, float x[8]) { load_dims<QB, 8>(a.q, base, d0, D, x); };
+    float amax = 0.0f;
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc) {
+      float x[8];
+      load8(16 * kc + 8 * h, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+    }
+    amax = halves_max(amax);
+    // 2^10 over the power of two at or below amax (a row below 2^-107 keeps fewer bits)
+    const int e = max((int)(__float_as_uint(amax) >> 23), 20);
+    float up = __uint_as_float((uint32_t)(264 - e) << 23);
+    qscale = __uint_as_float((uint32_t)(e - 10) << 23) * fabsf(a.scale) * 1.44269504088896340736f;
+    if (a.scale < 0.0f) up = -up;   // scales of the products are then never negative
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc) {
+      float x[8];
+      load8(16 * kc + 8 * h, x);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= up;
+#pragma unroll
+      for (int n = 0; n < QT; ++n) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = h2_of(x[2 * j], x[2 * j + 1]);
+          if (n + 1 < QT) h2_rest(w[j], x[2 * j], x[2 * j + 1]);
+        }
+        const uint4 u = make_uint4(w[0], w[1], w[2], w[3]);
+        q[n][kc] = __builtin_bit_cast(v8h, u);
+      }
+    }
+  }
+
+  // Codes of a step: thread t stages 16 dims of keys t / (DP / 16) + .., and 16 keys of
+  // dims t / 4 + ..
+  const int last = max(tile.sp.len - 1, 0);
+  const int32_t* table = b.table + (int64_t)seq * b.width;
+  auto page_of = [&](int key) -> int { return table[min(key, last) >> plan.page_shift]; };
+  auto clamped = [&](int pid) -> int64_t { return (uint32_t)pid < (uint32_t)c.pages ? pid : 0; };
+  const int kc_of = tid % (DP / 16), vq = tid & 3;
+  auto key_of = [&](int n) -> int { return (tid + n * kThreads) / (DP / 16); };
+  int pk[NL], pv;   // pages of the next load
+  auto find = [&](int step) {
+#pragma unroll
+    for (int n = 0; n < NL; ++n) pk[n] = page_of(step * kStep + key_of(n));
+    pv = page_of(step * kStep + vq * 16);
+  };
+  uint4 kr[NL], vr[NL];
+  auto load = [&](int step) {
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int key = step * kStep + key_of(n);
+      const int d0 = kc_of * 16 < D ? kc_of * 16 : 0;   // dims past the head: their queries are 0
+      kr[n] = *reinterpret_cast<const uint4*>(
+          c.k + ((clamped(pk[n]) * c.kv_heads + head) * P + (key & (P - 1))) * D + d0);
+    }
+    const int8_t* vp = c.v + (clamped(pv) * c.kv_heads + head) * P * D +
+                       ((step * kStep + vq * 16) & (P - 1));
+#pragma unroll
+    for (int n = 0; n < NL; ++n)
+      vr[n] = *reinterpret_cast<const uint4*>(vp + min((tid >> 2) + 64 * n, D - 1) * P);
+  };
+  auto stage = [&](uint8_t* buf) {
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const uint32_t kw[4] = {kr[n].x, kr[n].y, kr[n].z, kr[n].w};
+      const uint32_t vw[4] = {vr[n].x, vr[n].y, vr[n].z, vr[n].w};
+      uint32_t x[8], y[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        codes_to_h4(kw[j], x + 2 * j);
+        codes_to_h4(vw[j], y + 2 * j);
+      }
+      const int key = key_of(n), dim = (tid >> 2) + 64 * n;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        *reinterpret_cast<uint4*>(buf + k_group<DP>(key, 2 * kc_of + j)) =
+            make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        *reinterpret_cast<uint4*>(buf + kKBytes + v_group(dim, 2 * vq + j)) =
+            make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+      }
+    }
+  };
+
+  // scales of a step's four groups of 16 keys, in lanes 0 .. 3 of every wave
+  int gp;   // page of the step after the one whose scales are at hand
+  float dk, dv;
+  auto scales = [&](int pid) {
+    const int64_t at = clamped(pid) * c.kv_heads + head;
+    dk = (uint32_t)pid < (uint32_t)c.pages ? c.k_scale[at] : -1.0f;   // -1: no keys there
+    dv = c.v_scale[at];
+    if (!(dv > 0.0f && dv < INFINITY)) dv = 1.0f;   // a page that no visible key is in
+  };
+
+  const int first = tile.step0 + s_lo, end = tile.step0 + s_hi;
+  float m = -INFINITY, l = 0.0f;
+  v16f o[DT];
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[dt][j] = 0.0f;
+
+  // row of a 32-key tile that the lane's operand reads
+  const int krow = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
+
+  if (first < end) {
+    find(first);
+    load(first);
+    gp = page_of(first * kStep + (lane & 3) * 16);
+    scales(gp);
+    stage(lds);
+    if (first + 1 < end) {
+      find(first + 1);
+      load(first + 1);
+      gp = page_of((first + 1) * kStep + (lane & 3) * 16);
+      if (first + 2 < end) find(first + 2);
+    }
+  }
+  lds_barrier();
+  for (int step = first; step < end; ++step) {
+    uint8_t* buf = lds + ((step - first) & 1) * kBuf;
+    const float dk_now = dk, dv_now = dv;
+    if (step + 1 < end) {
+      scales(gp);
+      if (step + 2 < end) gp = page_of((step + 2) * kStep + (lane & 3) * 16);
+    }
+    const int key0 = step * kStep;
+    // some column of the wave sees some key of this step
+    const bool any = wave * 32 < tile.nc && key0 <= pos_hi && key0 + kStep - 1 >= from_lo;
+    v16f s[2];
+    if (any) {
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[kt][j] = 0.0f;
+        const int key = kt * 32 + krow;
+#pragma unroll
+        for (int kc = 0; kc < KC; ++kc) {
+          const v8h kk = *reinterpret_cast<const v8h*>(
+              buf + k_group<DP>(key, 2 * kc + h));
+#pragma unroll
+          for (int n = 0; n < QT; ++n)
+            s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, q[n][kc], s[kt], 0, 0, 0);
+        }
+      }
+    }
+    if (step + 1 < end) {
+      stage(lds + ((step - first + 1) & 1) * kBuf);
+      if (step + 2 < end) {
+        load(step + 2);
+        if (step + 3 < end) find(step + 3);
+      }
+    }
+    if (any) {
+      const float lv = __builtin_amdgcn_logf(dv_now), rdv = 1.0f / dv_now;
+      float ck[4], lg[4], rg[4];
+      bool there[4], hole = false;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float k = lane_of(dk_now, g);
+        there[g] = k > 0.0f;
+        hole = hole || !there[g];
+        ck[g] = fmaxf(qscale * k, 1e-38f);   // above 0: unseen keys' -inf stays -inf
+        lg[g] = lane_of(lv, g);
+        rg[g] = lane_of(rdv, g);
+      }
+      // group g holds s[g / 2][8 (g % 2) + j], j = 0 .. 7: key 16 g + 8 h + j
+      if (hole || key0 + kStep - 1 > pos_lo || key0 < from_hi) {
+        const int hi = pos - key0 - 8 * h, lo = from - key0 - 8 * h;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float x = s[g >> 1][8 * (g & 1) + j];
+            s[g >> 1][8 * (g & 1) + j] =
+                (there[g] & (16 * g + j <= hi) & (16 * g + j >= lo)) ? x : -INFINITY;
+          }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float t = s[g >> 1][8 * (g & 1)];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) t = fmaxf(t, s[g >> 1][8 * (g & 1) + j]);
+        mx = fmaxf(mx, __builtin_fmaf(t, ck[g], lg[g]));
+      }
+      mx = halves_max(mx);
+      if (__builtin_amdgcn_ballot_w64(mx > m + kSlack)) {
+        const float to = fmaxf(m, mx);
+        const float alpha = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        l *= alpha;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[dt][j] *= alpha;
+      }
+      const float ref = m == -INFINITY ? 0.0f : m - kLift;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float p[8], sum = 0.0f;
+        const float off = lg[g] - ref;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g >> 1][8 * (g & 1) + j], ck[g], off));
+          sum += p[j];
+        }
+        l = __builtin_fmaf(sum, rg[g], l);
+        v8h pf[PT];
+#pragma unroll
+        for (int n = 0; n < PT; ++n) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w[j] = h2_of(p[2 * j], p[2 * j + 1]);
+            if (n + 1 < PT) h2_rest(w[j], p[2 * j], p[2 * j + 1]);
+          }
+          const uint4 u = make_uint4(w[0], w[1], w[2], w[3]);
+          pf[n] = __builtin_bit_cast(v8h, u);
+        }
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          const int dim = 32 * dt + col;
+          const v8h vv = *reinterpret_cast<const v8h*>(
+              buf + kKBytes + v_group(dim, 2 * g + h));
+#pragma unroll
+          for (int n = 0; n < PT; ++n)
+            o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, pf[n], o[dt], 0, 0, 0);
+        }
+      }
+    }
+    lds_barrier();
+  }
+
+  l = halves_sum(l);
+  if (!live) return;
+  const float top = m - kLift;   // l and o are over 2^(m - kLift)
+  if (!alone) {
+    float* p = part + (((int64_t)(seq * c.kv_heads + head) * plan.tiles + ct) * plan.splits + split) *
+                          plan.part_cols * (D + 4) +
+               (int64_t)(wave * 32 + col) * (D + 4);
+    if (h == 0) *reinterpret_cast<float2*>(p) = make_float2(top, l);
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int d = 32 * dt + 8 * w + 4 * h;
+        if (d < D)
+          *reinterpret_cast<float4*>(p + 4 + d) =
+              make_float4(o[dt][4 * w], o[dt][4 * w + 1], o[dt][4 * w + 2], o[dt][4 * w + 3]);
+      }
+    return;
+  }
+  const float r = l > 0.0f ? 1.0f / l : 0.0f;
+  const int64_t at = (t_row * a.q_heads + q_head) * D;
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int d = 32 * dt + 8 * w + 4 * h;
+      if (d >= D) continue;
+      const float y0 = o[dt][4 * w] * r, y1 = o[dt][4 * w + 1] * r, y2 = o[dt][4 * w + 2] * r,
+                  y3 = o[dt][4 * w + 3] * r;
+      if (OB)
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at + d) =
+            make_uint2(bf16x2_rne(y0, y1), bf16x2_rne(y2, y3));
+      else
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at + d) = make_float4(y0, y1, y2, y3);
+    }
+  if (h == 0 && a.lse)
+    a.lse[t_row * a.q_heads + q_head] =
+        l > 0.0f ? 0.69314718055994530942f * (top + __builtin_amdgcn_logf(l)) : -INFINITY;
+}
+
+template <int DP>
+const void* pick_prompt(bool qb, bool ob) {
+  return qb ? (ob ? (const void*)attn_prompt_kernel<DP, 1, 1, true, true>
+                  : (const void*)attn_prompt_kernel<DP, 1, 1, true, false>)
+            : (ob ? (const void*)attn_prompt_kernel<DP, 2, 1, false, true>
+                  : (const void*)attn_prompt_kernel<DP, 2, 2, false, false>);
+}
+
+}  // namespace
+
+AttnPlan attn_prompt_plan(const KvCache& c, const KvBatch& b, int q_heads) {
+  return attn_plan(c, b, q_heads, kCols, 512, 512, 8);
+}
+
+hipError_t launch_attn_prompt(const KvCache& c, const KvBatch& b, const AttnArgs& a,
+                              const AttnPlan& p, bool q_bf16, bool out_bf16, void* workspace,
+                              hipStream_t s) {
+  const int64_t grid = (int64_t)b.seqs * c.kv_heads * p.tiles * p.splits;
+  if (grid > 2147483647) return hipErrorInvalidValue;
+  float* part = static_cast<float*>(workspace);
+  const int dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
+  const void* kern = dp == 64 ? pick_prompt<64>(q_bf16, out_bf16)
+                     : dp == 128 ? pick_prompt<128>(q_bf16, out_bf16) : pick_prompt<256>(q_bf16, out_bf16);
+  const size_t lds = (size_t)2 * 2 * kStep * dp * 2;   // two buffers of K and V in fp16
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&p, (void*)&part};
+  const hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(kThreads), args, lds, s);
+  if (e != hipSuccess || p.splits == 1) return e;
+  return launch_attn_join(c, b, a, p, 1.0f, out_bf16, part, s);
+}
+
+}  // namespace bitnet

@@ -560,11 +560,6 @@ struct AttnArgs {
 size_t attention_workspace_bytes(const KvCache& c, const KvBatch& b, int q_heads);
 hipError_t launch_attention(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool q_bf16,
                             bool out_bf16, void* workspace, hipStream_t s);
-// Its kernel for few rows, splitting the keys over workgroups.
-size_t attn_decode_workspace(const KvCache& c, const KvBatch& b, int q_heads);
-hipError_t launch_attn_decode(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool q_bf16,
-                              bool out_bf16, void* workspace, hipStream_t s);
-
 // Residual join (bitnet_residual, validated).
 struct ResidualArgs {
   const void *y, *h, *gate;
