@@ -96,7 +96,7 @@ __device__ __forceinline__ float rows_sum(float v) {
 }
 
 template <int DP, int ND, bool QB, bool OB>
-__global__ __launch_bounds__(kThreads) void attn_decode_kernel(
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kernel(
     const KvCache c, const KvBatch b, const AttnArgs a, const AttnPlan plan,
     float* __restrict__ part) {
   constexpr int KC = DP / 64, DT = DP / 16, HT = DT < 8 ? DT : 8;   // dims joined at a time: 16 HT
@@ -372,10 +372,12 @@ const void* pick_decode(bool qb, bool ob) {
 
 }  // namespace
 
-// Two workgroups per compute unit, four times that where sequences may differ in
-// length; no part is shorter than one step a wave.
+// Two workgroups per compute unit; no part is shorter than one step a wave.  (Four
+// times as many for batches of uneven lengths: 64 sequences of 1 .. 8191 tokens 131 ->
+// 130 us, but four of 65536 115 -> 175 us: a part's start and end cost about as much as
+// four steps.)
 AttnPlan attn_decode_plan(const KvCache& c, const KvBatch& b, int q_heads) {
-  return attn_plan(c, b, q_heads, kCols, 512, 2048, kWaves);
+  return attn_plan(c, b, q_heads, kCols, 512, kWaves);
 }
 
 hipError_t launch_attn_decode(const KvCache& c, const KvBatch& b, const AttnArgs& a,

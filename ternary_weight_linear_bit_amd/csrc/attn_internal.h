@@ -71,7 +71,7 @@ hipError_t launch_attn_join(const KvCache& c, const KvBatch& b, const AttnArgs& 
                             hipStream_t s);
 
 inline AttnPlan attn_plan(const KvCache& c, const KvBatch& b, int q_heads, int cols,
-                          int workgroups, int ragged, int least) {
+                          int workgroups, int least) {
   AttnPlan p;
   p.group = q_heads / c.kv_heads;
   p.page_shift = 4;
@@ -83,7 +83,7 @@ inline AttnPlan attn_plan(const KvCache& c, const KvBatch& b, int q_heads, int c
   p.least = least;
   const int64_t units = (int64_t)b.seqs * c.kv_heads * p.tiles;
   const int64_t steps = ((int64_t)b.max_len + kAttnStep - 1) / kAttnStep;
-  const int64_t want = ((b.seqs > 1 ? ragged : workgroups) + units - 1) / units;
+  const int64_t want = (workgroups + units - 1) / units;
   const int64_t most = (steps + least - 1) / least;
   const int64_t s = want < most ? want : most;
   p.splits = s < 1 ? 1 : (int)s;

@@ -82,7 +82,7 @@ __device__ __forceinline__ float lane_of(float v, int lane) {
 
 // QT / PT: fp16 terms of a query and of a weight.
 template <int DP, int QT, int PT, bool QB, bool OB>
-__global__ __launch_bounds__(kThreads) void attn_prompt_kernel(
+__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kernel(
     const KvCache c, const KvBatch b, const AttnArgs a, const AttnPlan plan,
     float* __restrict__ part) {
   constexpr int KC = DP / 16, DT = DP / 32, NL = DP / 64;   // NL: 16-code loads of K (and of V) a thread
@@ -412,7 +412,7 @@ const void* pick_prompt(bool qb, bool ob) {
 }  // namespace
 
 AttnPlan attn_prompt_plan(const KvCache& c, const KvBatch& b, int q_heads) {
-  return attn_plan(c, b, q_heads, kCols, 512, 512, 8);
+  return attn_plan(c, b, q_heads, kCols, 512, 8);
 }
 
 hipError_t launch_attn_prompt(const KvCache& c, const KvBatch& b, const AttnArgs& a,

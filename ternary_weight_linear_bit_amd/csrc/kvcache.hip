@@ -17,7 +17,13 @@
 //
 // One workgroup per (sequence, touched page, kv head, keys or values), so that the
 // page's new maximum, its scale and its earlier codes have one owner; further
-// workgroups of the same launch rotate the queries.
+// workgroups of the same launch rotate the queries.  A thread's item is a pair of
+// groups of W dims that rotate into each other (so that queries can be rotated in
+// place); it stays in registers from the maximum to the codes.
+//
+// Prompts are bound by memory, single tokens by the chain of dependent loads (row
+// numbers and length; page id, row, angles; scale and earlier codes): each link's
+// loads are issued together.
 #include "bitnet_internal.h"
 
 namespace bitnet {
@@ -25,19 +31,17 @@ namespace {
 
 constexpr int kKvThreads = 256;
 
-template <bool BF16>
-__device__ __forceinline__ float kv_load1(const void* x, int64_t i) {
-  if (BF16) return bf16_bits_to_float(reinterpret_cast<const uint16_t*>(x)[i]);
-  return reinterpret_cast<const float*>(x)[i];
-}
+template <int W>
+using vec = float __attribute__((ext_vector_type(W)));
 
-// 8 consecutive elements from index i; VEC: the address is 16-byte aligned.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void kv_load8(const void* x, int64_t i, float v[8]) {
-  if (!VEC) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = kv_load1<BF16>(x, i + j);
-  } else if (BF16) {
+// W consecutive elements from element i; W = 8: the address is 16-byte aligned.
+template <bool BF16, int W>
+__device__ __forceinline__ vec<W> kv_load(const void* x, int64_t i) {
+  vec<W> v;
+  if constexpr (W == 1) {
+    v[0] = BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(x)[i])
+                : reinterpret_cast<const float*>(x)[i];
+  } else if constexpr (BF16) {
     const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + i);
     const uint32_t d[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -47,55 +51,70 @@ __device__ __forceinline__ void kv_load8(const void* x, int64_t i, float v[8]) {
     }
   } else {
     const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + i);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 a = p[h];
-      v[4 * h] = a.x;
-      v[4 * h + 1] = a.y;
-      v[4 * h + 2] = a.z;
-      v[4 * h + 3] = a.w;
-    }
+    const float4 a = p[0], b = p[1];
+    v = (vec<8>){a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
+  return v;
 }
 
-// Dims d0 .. d0 + 7 of one head's row at `x`, rotated: cs / sn are the position's
-// rows of the tables (rot / 2 entries).  Dims from rot on pass through.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void rotated8(const void* x, int64_t base, int d0, int rot,
-                                         bool neighbours, const float* cs, const float* sn,
-                                         float v[8]) {
-  kv_load8<BF16, VEC>(x, base + d0, v);
-  if (d0 >= rot) return;
+// A pair of groups of W dims: dims a .. a + W - 1 and b .. b + W - 1.  Of a rotated
+// head's D / (2 W) pairs the first rot / (2 W) hold, in the order of halves, dims that
+// turn into each other; the others, and all in the order of neighbours, lie side by side.
+template <int W>
+struct Pair {
+  vec<W> x, y;
+  int a, b;
+};
+template <int W>
+__device__ __forceinline__ void place(Pair<W>& p, int j, int rot, bool neighbours) {
   const int half = rot >> 1;
-  if (neighbours) {
-#pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      if (d0 + j < rot) {
-        const float c = cs[(d0 + j) >> 1], s = sn[(d0 + j) >> 1];
-        const float a = v[j], b = v[j + 1];
-        v[j] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-        v[j + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-      }
-    }
-    return;
+  const bool apart = !neighbours && j * W < half;
+  p.a = apart ? j * W : neighbours ? 2 * W * j : rot + 2 * (j * W - half);
+  p.b = apart ? p.a + half : p.a + W;
+}
+// The angles that turn a pair: W entries of the position's table rows, from the one
+// of dim a on.  (W = 8 takes rot % 16 == 0, so a pair is rotated as a whole or not.)
+template <int W>
+struct Angles {
+  vec<W> c, s;
+};
+template <int W>
+__device__ __forceinline__ bool turned(const Pair<W>& p, int rot, bool neighbours) {
+  return p.a < (neighbours ? rot : rot >> 1);
+}
+template <int W>
+__device__ __forceinline__ void load_angles(Angles<W>& g, const Pair<W>& p, const float* cs,
+                                            const float* sn, int rot, bool neighbours) {
+  if (turned(p, rot, neighbours)) {
+    const int at = neighbours ? p.a >> 1 : p.a;
+    g.c = kv_load<false, W>(cs, at);
+    g.s = kv_load<false, W>(sn, at);
   }
-  float w[8];
-  if (VEC && (half & 7) == 0) {   // the 8 partners are one group too
-    kv_load8<BF16, true>(x, base + (d0 < half ? d0 + half : d0 - half), w);
+}
+__device__ __forceinline__ float turn_a(float a, float b, float c, float s) {
+  return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+}
+__device__ __forceinline__ float turn_b(float a, float b, float c, float s) {
+  return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+}
+template <int W>
+__device__ __forceinline__ void rotate(Pair<W>& p, const Angles<W>& g, int rot, bool neighbours) {
+  if (!turned(p, rot, neighbours)) return;
+  const vec<W> x = p.x, y = p.y;
+  if (!neighbours || W == 1) {
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      p.x[j] = turn_a(x[j], y[j], g.c[j], g.s[j]);
+      p.y[j] = turn_b(x[j], y[j], g.c[j], g.s[j]);
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int d = d0 + j;
-      w[j] = d < rot ? kv_load1<BF16>(x, base + (d < half ? d + half : d - half)) : 0.0f;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int d = d0 + j;
-    if (d < half) {
-      v[j] = __fsub_rn(__fmul_rn(v[j], cs[d]), __fmul_rn(w[j], sn[d]));
-    } else if (d < rot) {
-      v[j] = __fadd_rn(__fmul_rn(v[j], cs[d - half]), __fmul_rn(w[j], sn[d - half]));
+    for (int j = 0; j + 1 < W; j += 2) {
+      const int k = (W + j) / 2;
+      p.x[j] = turn_a(x[j], x[j + 1], g.c[j / 2], g.s[j / 2]);
+      p.x[j + 1] = turn_b(x[j], x[j + 1], g.c[j / 2], g.s[j / 2]);
+      p.y[j] = turn_a(y[j], y[j + 1], g.c[k], g.s[k]);
+      p.y[j + 1] = turn_b(y[j], y[j + 1], g.c[k], g.s[k]);
     }
   }
 }
@@ -121,7 +140,46 @@ __device__ __forceinline__ uint32_t below_mask(int s, int lim) {
   return n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
 }
 
-template <bool BF16, bool VEC>
+// W codes of one group to consecutive bytes.
+template <int W>
+__device__ __forceinline__ void store_codes(int8_t* at, vec<W> x, float inv) {
+  if constexpr (W == 1) {
+    *at = (int8_t)kv_code(x[0], inv);
+  } else {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j >> 2] |= ((uint32_t)kv_code(x[j], inv) & 0xffu) << (8 * (j & 3));
+    *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+  }
+}
+
+template <bool BF16, int W>
+__device__ __forceinline__ void store_row(void* out, int64_t i, vec<W> v) {
+  if (BF16) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(out) + i;
+    if constexpr (W == 1) {
+      *p = float_to_bf16_rne(v[0]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < W / 2; ++j) w[j] = bf16x2_rne(v[2 * j], v[2 * j + 1]);
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    float* p = reinterpret_cast<float*>(out) + i;
+    if constexpr (W == 1) {
+      *p = v[0];
+    } else {
+#pragma unroll
+      for (int h = 0; h < W / 4; ++h)
+        reinterpret_cast<float4*>(p)[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+    }
+  }
+}
+
+// W: dims a group (8, or 1 where rows, angles or the number of rotated dims do not
+// allow 16-byte groups).  H: pairs that a thread keeps; a page with more reads its rows again.
+template <bool BF16, int W, int H>
 __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(const KvCache c, const KvBatch b,
                                                                const KvRows r, int pages_per_seq,
                                                                int page_units, int q_blocks) {
@@ -129,43 +187,43 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(const KvCache c, 
   __shared__ float wmax[kKvThreads / 64];
   const int tid = threadIdx.x;
   int unit = blockIdx.x;
-  const int D = c.head_dim, P = c.page, G = D / 8;
+  const int D = c.head_dim, P = c.page, J = D / (2 * W);   // J: pairs of a head
 
   if (unit >= page_units) {   // rotate queries: kKvQRows rows of one sequence
     unit -= page_units;
     const int seq = unit / q_blocks;
     const SeqSpan sp = seq_span(b, seq);
     const int i0 = (unit - seq * q_blocks) * kKvQRows;
-    const int i1 = min(min(i0 + kKvQRows, sp.n), b.max_new);
-    const int per_row = r.q_heads * G;
-    for (int i = i0; i < i1; ++i) {
-      const int64_t t = sp.s0 + i;
-      const int pos = sp.first + i;
-      const float* cs = r.cos + (int64_t)max(pos, 0) * (r.rot >> 1);
-      const float* sn = r.sin + (int64_t)max(pos, 0) * (r.rot >> 1);
-      const int rot = pos < 0 ? 0 : r.rot;   // a row without a place is copied
-      // a pass covers whole heads and reads all of its values before it writes
-      // any, which makes q_out == q safe
-      for (int g0 = 0; g0 < per_row; g0 += kKvThreads / G * G) {
-        const int g = g0 + tid;
-        const bool on = tid < kKvThreads / G * G && g < per_row;
-        float v[8];
-        const int d0 = on ? g % G * 8 : 0;
-        const int64_t head = on ? g / G : 0;
-        if (on) rotated8<BF16, VEC>(r.q, t * r.q_stride + head * D, d0, rot, r.neighbours, cs, sn, v);
-        __syncthreads();
-        if (!on) continue;
-        const int64_t o = t * ((int64_t)r.q_heads * D) + head * D + d0;
-        if (BF16) {
-          uint32_t w[4];
+    const int rows = min(min(i0 + kKvQRows, sp.n), b.max_new) - i0;
+    // a thread keeps its pair of dims: of every row and kKvThreads / J heads
+    const int lanes = kKvThreads / J * J;
+    if (W == 8 && tid >= lanes) return;
+    for (int it = tid; it < r.q_heads * J; it += W == 8 ? lanes : kKvThreads) {
+      const int head = it / J, j = it - head * J;
+      Pair<W> p[kKvQRows];
+      Angles<W> g[kKvQRows];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = bf16x2_rne(v[2 * j], v[2 * j + 1]);
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(r.q_out) + o) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-          float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(r.q_out) + o);
-          p[0] = make_float4(v[0], v[1], v[2], v[3]);
-          p[1] = make_float4(v[4], v[5], v[6], v[7]);
+      for (int i = 0; i < kKvQRows; ++i) {
+        if (i < rows) {
+          const int64_t t = sp.s0 + i0 + i;
+          const int pos = sp.first + i0 + i;
+          const int64_t at = (int64_t)max(pos, 0) * (r.rot >> 1);
+          place(p[i], j, r.rot, r.neighbours);
+          const int64_t base = t * r.q_stride + (int64_t)head * D;
+          p[i].x = kv_load<BF16, W>(r.q, base + p[i].a);
+          p[i].y = kv_load<BF16, W>(r.q, base + p[i].b);
+          load_angles(g[i], p[i], r.cos + at, r.sin + at, r.rot, r.neighbours);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kKvQRows; ++i) {
+        if (i < rows) {
+          const int64_t t = sp.s0 + i0 + i;
+          if (sp.first + i0 + i >= 0)   // a row without a place is copied
+            rotate(p[i], g[i], r.rot, r.neighbours);
+          const int64_t o = (t * r.q_heads + head) * D;
+          store_row<BF16, W>(r.q_out, o + p[i].a, p[i].x);
+          store_row<BF16, W>(r.q_out, o + p[i].b, p[i].y);
         }
       }
     }
@@ -185,29 +243,62 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(const KvCache c, 
   const int lo = max(at0 - pg * P, 0), hi = min(end - pg * P, P);
   if (lo >= hi) return;
   const int pid = b.table[(int64_t)seq * b.width + pg];
-  if (pid < 0 || pid >= c.pages) return;
 
+  // items: pairs of the new rows; values lane by slot (their codes go side by side)
+  const int n = hi - lo, items = n * J;
   const int64_t t0 = sp.s0 + (pg * P + lo - sp.first);
   const void* src = vals ? r.v : r.k;
   const int64_t stride = vals ? r.v_stride : r.k_stride;
   const int rot = vals ? 0 : r.rot;
-  const int items = (hi - lo) * G;
-  auto load = [&](int it, float v[8]) {
-    const int slot = it / G, d0 = (it - slot * G) * 8;
-    const int64_t pos = (int64_t)pg * P + lo + slot;
-    const int half = rot >> 1;
-    rotated8<BF16, VEC>(src, (t0 + slot) * stride + (int64_t)head * D, d0, rot, r.neighbours,
-                        r.cos + pos * half, r.sin + pos * half, v);
+  const bool neighbours = vals || r.neighbours;
+  auto slot_of = [&](int it) -> int { return vals ? it % n : it / J; };
+  auto load = [&](int it, Pair<W>& p, Angles<W>& g) {
+    const int slot = slot_of(it), j = vals ? it / n : it - slot * J;
+    place(p, j, rot, neighbours);
+    const int64_t base = (t0 + slot) * stride + (int64_t)head * D;
+    p.x = kv_load<BF16, W>(src, base + p.a);
+    p.y = kv_load<BF16, W>(src, base + p.b);
+    const int64_t at = ((int64_t)pg * P + lo + slot) * (rot >> 1);
+    load_angles(g, p, r.cos + at, r.sin + at, rot, neighbours);
   };
-
+  Pair<W> p[H];
+  {
+    Angles<W> g[H];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (tid + h * kKvThreads < items) load(tid + h * kKvThreads, p[h], g[h]);
+    if (pid < 0 || pid >= c.pages) return;
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (tid + h * kKvThreads < items) rotate(p[h], g[h], rot, neighbours);
+  }
   float* scale = (vals ? c.v_scale : c.k_scale) + (int64_t)pid * c.kv_heads + head;
   const float d_old = lo > 0 ? *scale : 0.0f;
+  const int64_t page_at = ((int64_t)pid * c.kv_heads + head) * P * D;
+  int8_t* vdst = c.v + page_at;
+  uint8_t* tile = reinterpret_cast<uint8_t*>(tile4);
+  const int c0 = lo / 16, c1 = (hi + 15) / 16;
+  if (vals) {   // 16-byte groups of slots that hold other tokens too: first and last
+    for (int i = tid; i < 2 * D; i += kKvThreads) {
+      const int row = i >> 1, s = (i & 1 ? c1 - 1 : c0) * 16;
+      if ((i & 1) && c1 - 1 == c0) continue;
+      if (s < lo || s + 16 > hi)
+        *reinterpret_cast<uint4*>(tile + row * P + s) = *reinterpret_cast<const uint4*>(vdst + row * P + s);
+    }
+  }
   float a = 0.0f;
-  for (int it = tid; it < items; it += kKvThreads) {
-    float v[8];
-    load(it, v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[j]));
+  for (int h = 0; h < H; ++h)
+    if (tid + h * kKvThreads < items)
+#pragma unroll
+      for (int j = 0; j < W; ++j) a = fmaxf(a, fmaxf(fabsf(p[h].x[j]), fabsf(p[h].y[j])));
+  for (int it = tid + H * kKvThreads; it < items; it += kKvThreads) {
+    Pair<W> q;
+    Angles<W> g;
+    load(it, q, g);
+    rotate(q, g, rot, neighbours);
+#pragma unroll
+    for (int j = 0; j < W; ++j) a = fmaxf(a, fmaxf(fabsf(q.x[j]), fabsf(q.y[j])));
   }
   a = wave_max(a);
   if ((tid & 63) == 0) wmax[tid >> 6] = a;
@@ -220,59 +311,68 @@ __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(const KvCache c, 
   const float f = d_old / d, inv = 1.0f / d;
   if (tid == 0) *scale = d;
 
-  const int64_t page_at = ((int64_t)pid * c.kv_heads + head) * P * D;
+  auto each = [&](auto put) {
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (tid + h * kKvThreads < items) put(tid + h * kKvThreads, p[h]);
+    for (int it = tid + H * kKvThreads; it < items; it += kKvThreads) {
+      Pair<W> q;
+      Angles<W> g;
+      load(it, q, g);
+      rotate(q, g, rot, neighbours);
+      put(it, q);
+    }
+  };
   if (!vals) {
     int8_t* dst = c.k + page_at;
     if (grown) {
       for (int i = tid; i < lo * D / 16; i += kKvThreads) {
-        uint4* p = reinterpret_cast<uint4*>(dst) + i;
-        const uint4 w = *p;
-        *p = make_uint4(rescale4(w.x, ~0u, f), rescale4(w.y, ~0u, f), rescale4(w.z, ~0u, f),
-                        rescale4(w.w, ~0u, f));
+        uint4* w4 = reinterpret_cast<uint4*>(dst) + i;
+        const uint4 w = *w4;
+        *w4 = make_uint4(rescale4(w.x, ~0u, f), rescale4(w.y, ~0u, f), rescale4(w.z, ~0u, f),
+                         rescale4(w.w, ~0u, f));
       }
     }
-    for (int it = tid; it < items; it += kKvThreads) {
-      float v[8];
-      load(it, v);
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        w[j >> 2] |= ((uint32_t)kv_code(v[j], inv) & 0xffu) << (8 * (j & 3));
-      *reinterpret_cast<uint2*>(dst + (int64_t)lo * D + (int64_t)it * 8) = make_uint2(w[0], w[1]);
-    }
+    each([&](int it, const Pair<W>& q) {
+      int8_t* at = dst + (lo + slot_of(it)) * D;
+      store_codes<W>(at + q.a, q.x, inv);
+      store_codes<W>(at + q.b, q.y, inv);
+    });
     return;
   }
 
-  // values: the 16-byte groups of slots that hold new (or, with a larger scale,
-  // earlier) tokens pass through LDS, where the new codes take their bytes
-  int8_t* dst = c.v + page_at;
-  uint8_t* tile = reinterpret_cast<uint8_t*>(tile4);
-  const int c0 = grown ? 0 : lo / 16, c1 = (hi + 15) / 16, nc = c1 - c0;
-  for (int i = tid; i < D * nc; i += kKvThreads) {
-    const int row = i / nc, s = (c0 + i - row * nc) * 16;
-    if (s >= lo && s + 16 <= hi) continue;   // new tokens only
-    uint4 w = *reinterpret_cast<const uint4*>(dst + row * P + s);
-    if (grown) {
+  if (grown) {   // earlier codes at the larger scale, whole 16-byte groups
+    const int groups = (lo + 15) / 16;
+    for (int i = tid; i < D * groups; i += kKvThreads) {
+      const int row = i / groups, s = (i - row * groups) * 16;
+      uint4 w = *reinterpret_cast<const uint4*>(vdst + row * P + s);
       w.x = rescale4(w.x, below_mask(s, lo), f);
       w.y = rescale4(w.y, below_mask(s + 4, lo), f);
       w.z = rescale4(w.z, below_mask(s + 8, lo), f);
       w.w = rescale4(w.w, below_mask(s + 12, lo), f);
+      *reinterpret_cast<uint4*>(tile + row * P + s) = w;
     }
-    *reinterpret_cast<uint4*>(tile + row * P + s) = w;
+    __syncthreads();
   }
-  __syncthreads();
-  for (int it = tid; it < items; it += kKvThreads) {
-    float v[8];
-    load(it, v);
-    const int slot = it / G, d0 = (it - slot * G) * 8;
+  each([&](int it, const Pair<W>& q) {
+    uint8_t* at = tile + lo + slot_of(it);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) tile[(d0 + j) * P + lo + slot] = (uint8_t)kv_code(v[j], inv);
-  }
+    for (int j = 0; j < W; ++j) {
+      at[(q.a + j) * P] = (uint8_t)kv_code(q.x[j], inv);
+      at[(q.b + j) * P] = (uint8_t)kv_code(q.y[j], inv);
+    }
+  });
   __syncthreads();
+  const int s0 = grown ? 0 : c0, nc = c1 - s0;
   for (int i = tid; i < D * nc; i += kKvThreads) {
-    const int row = i / nc, s = (c0 + i - row * nc) * 16;
-    *reinterpret_cast<uint4*>(dst + row * P + s) = *reinterpret_cast<const uint4*>(tile + row * P + s);
+    const int row = i / nc, s = (s0 + i - row * nc) * 16;
+    *reinterpret_cast<uint4*>(vdst + row * P + s) = *reinterpret_cast<const uint4*>(tile + row * P + s);
   }
+}
+
+template <int W, int H>
+const void* append_pick(bool bf16) {
+  return bf16 ? (const void*)kv_append_kernel<true, W, H> : (const void*)kv_append_kernel<false, W, H>;
 }
 
 }  // namespace
@@ -288,12 +388,13 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const KvRows& r,
     return p == nullptr || (((uintptr_t)p & 15u) == 0 && (stride * es) % 16 == 0);
   };
   const size_t es = bf16 ? 2 : 4;
-  const bool vec = a16(r.k, r.k_stride, es) && a16(r.v, r.v_stride, es) && a16(r.q, r.q_stride, es);
+  // groups of 8: 16-byte aligned rows and angles, rotated dims in whole pairs of groups
+  const bool vec = a16(r.k, r.k_stride, es) && a16(r.v, r.v_stride, es) && a16(r.q, r.q_stride, es) &&
+                   r.rot % 16 == 0 && a16(r.cos, 0, 4) && a16(r.sin, 0, 4);
   const int pu = (int)page_units;
-  const void* kern = bf16 ? (vec ? (const void*)kv_append_kernel<true, true>
-                                 : (const void*)kv_append_kernel<true, false>)
-                          : (vec ? (const void*)kv_append_kernel<false, true>
-                                 : (const void*)kv_append_kernel<false, false>);
+  const int rows = b.max_new < c.page ? b.max_new : c.page;   // of one page
+  const bool few = rows * (c.head_dim / 16) <= kKvThreads;
+  const void* kern = !vec ? append_pick<1, 4>(bf16) : few ? append_pick<8, 1>(bf16) : append_pick<8, 2>(bf16);
   void* args[] = {(void*)&c, (void*)&b, (void*)&r, (void*)&pages_per_seq, (void*)&pu,
                   (void*)&q_blocks};
   return hipLaunchKernel(kern, dim3((unsigned)grid), dim3(kKvThreads), args,
