@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libbitnet_mi355x.so")
 
@@ -662,50 +663,80 @@ class BitnetResidual(ctypes.Structure):
 
 
 SIGNATURES["bitnet_kv_append"] = (_I, [ctypes.POINTER(BitnetKvCache),
-                                       ctypes.POINTER(BitnetKvBatch),
-                                       ctypes.POINTER(BitnetKvRows), _P])
+                                       ctypes.POINTER(BitnetKvBatch), _P, _P])
 SIGNATURES["bitnet_attention_workspace_bytes"] = (_SZ, [ctypes.POINTER(BitnetKvCache),
                                                         ctypes.POINTER(BitnetKvBatch), _I])
 SIGNATURES["bitnet_attention"] = (_I, [ctypes.POINTER(BitnetKvCache),
                                        ctypes.POINTER(BitnetKvBatch), _P, _I, _I64, _I,
                                        ctypes.c_float, _I64, _P, _I, _P, _P, _SZ, _P])
-SIGNATURES["bitnet_residual_norm"] = (_I, [ctypes.POINTER(BitnetResidual), _P])
+SIGNATURES["bitnet_residual_norm"] = (_I, [_P, _P])
+
+
+# The same two structs as byte strings: packing one takes a third of the time of
+# filling the ctypes class (tests compare the layouts).
+_ROWS = struct.Struct("@PPPPqqqiiPPqii")
+_RESIDUAL = struct.Struct("@PPPPPPPPPqqqiiiff0q")
 
 
 def _one_device(*ts):
-    """Every tensor (None: absent) on one device: its kernels read them all."""
-    dev = None
+    """The device of every tensor (None: absent): its kernels read them all."""
+    index, first = None, None
     for t in ts:
         if t is None:
             continue
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors lie on {dev} and {t.device}")
-    return dev
+        i = t.get_device()
+        if index is None:
+            index, first = i, t
+        elif i != index or (i < 0 and t.device != first.device):
+            raise ValueError(f"tensors lie on {first.device} and {t.device}")
+    return None if first is None else first.device
+
+
+_codes = {}
+
+
+def _code(dtype, name):
+    """bitnet_dtype of an fp32 or bf16 tensor."""
+    if not _codes:
+        for d in _floats():
+            _codes[d] = _dtype_code(d)
+    code = _codes.get(dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, _floats()))}, got {dtype}")
+    return code
+
+
+def _like(t, shape, dtype, name):
+    """_expect for one dtype, quick where the tensor is as expected."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        _expect(t, shape, dtype, name)
 
 
 class _On:
     """The tensors' device made current (kernels launch on the current device) and
     the stream the call goes to: the caller's, which has to be one of that device, or
     the device's current one.  Tensors that the call allocates belong to that stream."""
+    __slots__ = ("_index", "_guard")
 
     def __init__(self, device, stream):
         import torch
         if stream is not None and stream.device != device:
             raise ValueError(f"the stream is one of {stream.device}, the tensors lie on {device}")
-        self._guard = None
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be CUDA tensors, not {device}")
+        self._index = device.index
         if stream is not None:
             self._guard = torch.cuda.stream(stream)       # its device too
         elif torch.cuda.current_device() != device.index:
             self._guard = torch.cuda.device(device)
-        self._device = device
+        else:
+            self._guard = None
 
     def __enter__(self):
         import torch
         if self._guard is not None:
             self._guard.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream(self._device).cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def __exit__(self, *exc):
         if self._guard is not None:
@@ -783,17 +814,18 @@ class KVBatch:
 def _rows(t, heads, dim, name):
     """t [tokens, heads, dim]: dims and heads adjacent, any distance between tokens.
     Returns that distance in elements."""
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
-        raise ValueError(f"{name}: expected [tokens, {heads or 'heads'}, {dim}], got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != dim:
+        raise ValueError(f"{name}: expected [tokens, {heads or 'heads'}, {dim}], got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    h = t.shape[1]
-    if t.numel() == 0:
+    n, h, _ = shape
+    if t.is_contiguous():
         return h * dim
     st = t.stride()
-    if st[2] != 1 or (h > 1 and st[1] != dim) or (t.shape[0] > 1 and st[0] < h * dim):
+    if st[2] != 1 or (h > 1 and st[1] != dim) or (n > 1 and st[0] < h * dim):
         raise ValueError(f"{name}: a token's heads and dims must lie one after another")
-    return st[0] if t.shape[0] > 1 else h * dim
+    return st[0] if n > 1 else h * dim
 
 
 def bitnet_kv_append(cache, batch, k, v, cos=None, sin=None, interleaved=False, q=None, q_out=None,
@@ -802,42 +834,43 @@ def bitnet_kv_append(cache, batch, k, v, cos=None, sin=None, interleaved=False, 
     positions and appends k and v to the cache.  cos / sin: fp32 [positions, rotary/2]
     (None: no rotation).  Returns the rotated queries (None without q)."""
     import torch
-    dim = cache.head_dim
+    dim, dtype = cache.head_dim, k.dtype
     ks, vs = _rows(k, cache.kv_heads, dim, "k"), _rows(v, cache.kv_heads, dim, "v")
     tokens = k.shape[0]
-    dt = _dtype_code(k.dtype)
-    if v.dtype != k.dtype or v.shape[0] != tokens:
+    dt = _code(dtype, "k")
+    if v.dtype is not dtype or v.shape[0] != tokens:
         raise ValueError("v must match k in tokens and dtype")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
-    rot = positions = 0
+    rot = positions = cp = sp = 0
     if cos is not None:
         if cos.dim() != 2:
             raise ValueError("cos must be [positions, rotary / 2]")
+        _like(cos, cos.shape, torch.float32, "cos")
+        _like(sin, cos.shape, torch.float32, "sin")
         positions, rot = cos.shape[0], 2 * cos.shape[1]
-        _expect(cos, cos.shape, torch.float32, "cos")
-        _expect(sin, cos.shape, torch.float32, "sin")
-    qs = q_heads = 0
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    qs = q_heads = qp = qo = 0
     if q is not None:
         qs = _rows(q, None, dim, "q")
-        if q.dtype != k.dtype or q.shape[0] != tokens:
+        if q.dtype is not dtype or q.shape[0] != tokens:
             raise ValueError("q must match k in tokens and dtype")
-        q_heads = q.shape[1]
+        q_heads, qp = q.shape[1], q.data_ptr()
+        if q_out is not None:
+            _like(q_out, q.shape, dtype, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
     device = _one_device(cache.k, batch.table, k, v, cos, sin, q, q_out)
     with _On(device, stream) as s:
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        if q_out is not None:
-            _expect(q_out, q.shape, q.dtype, "q_out")
-        rows = BitnetKvRows(k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
-                            None if q is None else q_out.data_ptr(), ks, vs, qs, dt, q_heads,
-                            None if cos is None else cos.data_ptr(),
-                            None if sin is None else sin.data_ptr(), positions, rot,
-                            1 if interleaved else 0)
-        _check("bitnet_kv_append", lib().bitnet_kv_append(cache.ref, batch._of(tokens),
-                                                          ctypes.byref(rows), s))
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=dtype, device=device)
+            qo = q_out.data_ptr()
+        rows = _ROWS.pack(k.data_ptr(), v.data_ptr(), qp, qo, ks, vs, qs, dt, q_heads, cp, sp, positions,
+                          rot, 1 if interleaved else 0)
+        status = lib().bitnet_kv_append(cache.ref, batch._of(tokens), rows, s)
+    if status:
+        raise BitnetError("bitnet_kv_append", status)
     return q_out
 
 
@@ -854,29 +887,36 @@ def bitnet_attention(cache, batch, q, scale=None, window=0, out=None, out_dtype=
     import torch
     dim = cache.head_dim
     qs = _rows(q, None, dim, "q")
-    tokens, q_heads = q.shape[0], q.shape[1]
+    tokens, q_heads, _ = q.shape
     if q_heads % cache.kv_heads:
         raise ValueError("q_heads must be a multiple of the cache's kv_heads")
     if out is not None:
-        _expect(out, q.shape, _floats(), "out")
+        if out.dtype is not q.dtype:
+            _expect(out, q.shape, _floats(), "out")
+        _like(out, q.shape, out.dtype, "out")
     if lse is not None:
-        _expect(lse, (tokens, q_heads), torch.float32, "lse")
+        _like(lse, (tokens, q_heads), torch.float32, "lse")
     if workspace is not None:
         _need_cuda(workspace)
     device = _one_device(cache.k, batch.table, q, out, lse, workspace)
     with _On(device, stream) as s:
         if out is None:
             out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=device)
-        b = batch._of(tokens)
-        need = lib().bitnet_attention_workspace_bytes(cache.ref, b, q_heads)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        _check("bitnet_attention", lib().bitnet_attention(
-            cache.ref, b, q.data_ptr(), _dtype_code(q.dtype), qs, q_heads,
-            dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
-            _dtype_code(out.dtype), None if lse is None else lse.data_ptr(),
-            None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), s))
+        b, l = batch._of(tokens), lib()
+        have = wp = 0
+        if workspace is None:
+            have = l.bitnet_attention_workspace_bytes(cache.ref, b, q_heads)
+            if have:
+                workspace = torch.empty(have, dtype=torch.uint8, device=device)
+        else:
+            have = workspace.numel() * workspace.element_size()
+        if have:
+            wp = workspace.data_ptr()
+        status = l.bitnet_attention(cache.ref, b, q.data_ptr(), _code(q.dtype, "q"), qs, q_heads,
+                                    dim ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                                    _code(out.dtype, "out"), 0 if lse is None else lse.data_ptr(), wp, have, s)
+    if status:
+        raise BitnetError("bitnet_attention", status)
     return out
 
 
@@ -889,34 +929,47 @@ def bitnet_residual_norm(y, h, h_out=None, post_weight=None, gate=None, scale=1.
     import torch
     if y.dim() != 2:
         raise ValueError("y must be 2-D [M, K]")
-    m, k = y.shape
-    _expect(y, (m, k), _floats(), "y")
-    _expect(h, (m, k), _floats(), "h")
-    _expect(post_weight, (k,), torch.float32, "post_weight")
-    _expect(pre_weight, (k,), torch.float32, "pre_weight")
-    _expect(u, (m, k), _floats(), "u")
-    gate_stride = 0
+    f32, shape, yd, hd = torch.float32, y.shape, y.dtype, h.dtype
+    m, k = shape
+    y_code, h_code, u_code, gate_stride = _code(yd, "y"), _code(hd, "h"), 0, 0
+    _like(y, shape, yd, "y")
+    _like(h, shape, hd, "h")
+    p1 = p2 = pg = pu = pq = ps = 0
+    if post_weight is not None:
+        _like(post_weight, (k,), f32, "post_weight")
+        p1 = post_weight.data_ptr()
+    if pre_weight is not None:
+        _like(pre_weight, (k,), f32, "pre_weight")
+        p2 = pre_weight.data_ptr()
     if gate is not None:
-        gate_stride = k if gate.dim() == 2 else 0
-        _expect(gate, (m, k) if gate.dim() == 2 else (k,), y.dtype, "gate")
+        rows = gate.dim() == 2
+        _like(gate, shape if rows else (k,), yd, "gate")
+        gate_stride, pg = k if rows else 0, gate.data_ptr()
+    if u is not None:
+        u_code = _code(u.dtype, "u")
+        _like(u, shape, u.dtype, "u")
+        pu = u.data_ptr()
+    if h_out is not None:
+        _like(h_out, shape, hd, "h_out")
+    if x_q is not None:
+        _like(x_q, shape, torch.int8, "x_q")
+    if x_scale is not None:
+        _like(x_scale, (m,), f32, "x_scale")
     if not quantize and (x_q is not None or x_scale is not None):
         raise ValueError("x_q / x_scale with quantize=False")
     device = _one_device(y, h, h_out, post_weight, gate, pre_weight, u, x_q, x_scale)
     with _On(device, stream) as s:
         if h_out is None:
-            h_out = torch.empty((m, k), dtype=h.dtype, device=device)
-        _expect(h_out, (m, k), h.dtype, "h_out")
+            h_out = torch.empty(shape, dtype=hd, device=device)
         if quantize:
             if x_q is None:
-                x_q = torch.empty((m, k), dtype=torch.int8, device=device)
+                x_q = torch.empty(shape, dtype=torch.int8, device=device)
             if x_scale is None:
-                x_scale = torch.empty(m, dtype=torch.float32, device=device)
-            _expect(x_q, (m, k), torch.int8, "x_q")
-            _expect(x_scale, (m,), torch.float32, "x_scale")
-        p = lambda t: None if t is None else t.data_ptr()
-        args = BitnetResidual(p(y), p(h), p(gate), p(h_out), p(u), p(post_weight), p(pre_weight),
-                              p(x_q), p(x_scale), m, k, gate_stride, _dtype_code(y.dtype),
-                              _dtype_code(h.dtype), 0 if u is None else _dtype_code(u.dtype),
-                              scale, eps)
-        _check("bitnet_residual_norm", lib().bitnet_residual_norm(ctypes.byref(args), s))
+                x_scale = torch.empty(m, dtype=f32, device=device)
+            pq, ps = x_q.data_ptr(), x_scale.data_ptr()
+        args = _RESIDUAL.pack(y.data_ptr(), h.data_ptr(), pg, h_out.data_ptr(), pu, p1, p2, pq, ps, m, k,
+                              gate_stride, y_code, h_code, u_code, scale, eps)
+        status = lib().bitnet_residual_norm(args, s)
+    if status:
+        raise BitnetError("bitnet_residual_norm", status)
     return h_out, x_q, x_scale

@@ -145,6 +145,16 @@ def test_residual_nothing_to_do(lib):
     assert lib.bitnet_residual_norm(None, None) == ENULL
 
 
+def test_packed_structs_match_the_header():
+    """The binding packs two structs itself: the same bytes as their ctypes classes."""
+    assert N._ROWS.size == ctypes.sizeof(N.BitnetKvRows)
+    v = (1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14)
+    assert N._ROWS.pack(*v) == bytes(N.BitnetKvRows(*v))
+    assert N._RESIDUAL.size == ctypes.sizeof(N.BitnetResidual)
+    v = (1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 0.5, 0.25)
+    assert N._RESIDUAL.pack(*v) == bytes(N.BitnetResidual(*v))
+
+
 # ---------------------------------------------------------------------------
 # the binding
 # ---------------------------------------------------------------------------
