@@ -27,6 +27,8 @@
 // step's codes are loaded while this one's are used.
 #include "attn_internal.h"
 
+#include <type_traits>
+
 namespace bitnet {
 namespace {
 
@@ -78,6 +80,11 @@ __device__ __forceinline__ float halves_sum(float v) {
 }
 __device__ __forceinline__ float lane_of(float v, int lane) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+
+// A positive finite float, by its bits (this file is compiled without NaN semantics).
+__device__ __forceinline__ bool is_scale(float v) {
+  return __float_as_uint(v) - 1u < 0x7f7fffffu;
 }
 
 // QT / PT: fp16 terms of a query and of a weight.
@@ -168,6 +175,15 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
   auto clamped = [&](int pid) -> int64_t { return (uint32_t)pid < (uint32_t)c.pages ? pid : 0; };
   const int kc_of = tid % (DP / 16), vq = tid & 3;
   auto key_of = [&](int n) -> int { return (tid + n * kThreads) / (DP / 16); };
+  // offsets in a page, for its first 64 slots (a page of 128 adds those of the step)
+  const int64_t head_at = (int64_t)head * P * D, page_bytes = (int64_t)c.kv_heads * P * D;
+  int koff[NL], voff[NL];
+#pragma unroll
+  for (int n = 0; n < NL; ++n) {
+    // dims past the head read dim 0: their queries are 0
+    koff[n] = (key_of(n) & (P - 1)) * D + (kc_of * 16 < D ? kc_of * 16 : 0);
+    voff[n] = min((tid >> 2) + 64 * n, D - 1) * P + ((vq * 16) & (P - 1));
+  }
   int pk[NL], pv;   // pages of the next load
   auto find = [&](int step) {
 #pragma unroll
@@ -176,18 +192,13 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
   };
   uint4 kr[NL], vr[NL];
   auto load = [&](int step) {
-#pragma unroll
-    for (int n = 0; n < NL; ++n) {
-      const int key = step * kStep + key_of(n);
-      const int d0 = kc_of * 16 < D ? kc_of * 16 : 0;   // dims past the head: their queries are 0
-      kr[n] = *reinterpret_cast<const uint4*>(
-          c.k + ((clamped(pk[n]) * c.kv_heads + head) * P + (key & (P - 1))) * D + d0);
-    }
-    const int8_t* vp = c.v + (clamped(pv) * c.kv_heads + head) * P * D +
-                       ((step * kStep + vq * 16) & (P - 1));
+    const int at = (step * kStep) & (P - 1);
 #pragma unroll
     for (int n = 0; n < NL; ++n)
-      vr[n] = *reinterpret_cast<const uint4*>(vp + min((tid >> 2) + 64 * n, D - 1) * P);
+      kr[n] = *reinterpret_cast<const uint4*>(c.k + head_at + at * D + clamped(pk[n]) * page_bytes + koff[n]);
+    const int8_t* vp = c.v + head_at + at + clamped(pv) * page_bytes;
+#pragma unroll
+    for (int n = 0; n < NL; ++n) vr[n] = *reinterpret_cast<const uint4*>(vp + voff[n]);
   };
   auto stage = [&](uint8_t* buf) {
 #pragma unroll
@@ -211,14 +222,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
     }
   };
 
-  // scales of a step's four groups of 16 keys, in lanes 0 .. 3 of every wave
-  int gp;   // page of the step after the one whose scales are at hand
+  // scales of a step's four groups of 16 keys, in lanes 0 .. 3 of every wave: loaded a
+  // step ahead, looked at when they are used
+  int gp, gp_next;   // pages of this step's groups, and of the next one's
   float dk, dv;
   auto scales = [&](int pid) {
     const int64_t at = clamped(pid) * c.kv_heads + head;
-    dk = (uint32_t)pid < (uint32_t)c.pages ? c.k_scale[at] : -1.0f;   // -1: no keys there
+    dk = c.k_scale[at];
     dv = c.v_scale[at];
-    if (!(dv > 0.0f && dv < INFINITY)) dv = 1.0f;   // a page that no visible key is in
   };
 
   const int first = tile.step0 + s_lo, end = tile.step0 + s_hi;
@@ -232,27 +243,16 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
   // row of a 32-key tile that the lane's operand reads
   const int krow = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
 
-  if (first < end) {
-    find(first);
-    load(first);
-    gp = page_of(first * kStep + (lane & 3) * 16);
+  // One step from buffer B.  Loads run ahead without a test for the end: past it they
+  // read the sequence's last page again.
+  auto body = [&](auto B, int step) {   // B: 0 or 1, a constant where the loop is unrolled
+    const uint8_t* buf = lds + B * kBuf;
+    // no page: scale -1; a scale that no visible key can have (another page's memory): 1
+    const float dk_now = (uint32_t)gp < (uint32_t)c.pages ? dk : -1.0f;
+    const float dv_now = is_scale(dv) ? dv : 1.0f;
+    gp = gp_next;
     scales(gp);
-    stage(lds);
-    if (first + 1 < end) {
-      find(first + 1);
-      load(first + 1);
-      gp = page_of((first + 1) * kStep + (lane & 3) * 16);
-      if (first + 2 < end) find(first + 2);
-    }
-  }
-  lds_barrier();
-  for (int step = first; step < end; ++step) {
-    uint8_t* buf = lds + ((step - first) & 1) * kBuf;
-    const float dk_now = dk, dv_now = dv;
-    if (step + 1 < end) {
-      scales(gp);
-      if (step + 2 < end) gp = page_of((step + 2) * kStep + (lane & 3) * 16);
-    }
+    gp_next = page_of((step + 2) * kStep + (lane & 3) * 16);
     const int key0 = step * kStep;
     // some column of the wave sees some key of this step
     const bool any = wave * 32 < tile.nc && key0 <= pos_hi && key0 + kStep - 1 >= from_lo;
@@ -273,21 +273,17 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
         }
       }
     }
-    if (step + 1 < end) {
-      stage(lds + ((step - first + 1) & 1) * kBuf);
-      if (step + 2 < end) {
-        load(step + 2);
-        if (step + 3 < end) find(step + 3);
-      }
-    }
+    stage(lds + (1 - B) * kBuf);
+    load(step + 2);
+    find(step + 3);
     if (any) {
-      const float lv = __builtin_amdgcn_logf(dv_now), rdv = 1.0f / dv_now;
+      const float lv = __builtin_amdgcn_logf(dv_now), rdv = __builtin_amdgcn_rcpf(dv_now);
       float ck[4], lg[4], rg[4];
       bool there[4], hole = false;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const float k = lane_of(dk_now, g);
-        there[g] = k > 0.0f;
+        there[g] = is_scale(k);
         hole = hole || !there[g];
         ck[g] = fmaxf(qscale * k, 1e-38f);   // above 0: unseen keys' -inf stays -inf
         lg[g] = lane_of(lv, g);
@@ -359,6 +355,29 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
       }
     }
     lds_barrier();
+  };
+
+  if (first < end) {
+    find(first);
+    load(first);
+    gp = page_of(first * kStep + (lane & 3) * 16);
+    scales(gp);
+    stage(lds);
+    find(first + 1);
+    load(first + 1);
+    gp_next = page_of((first + 1) * kStep + (lane & 3) * 16);
+    find(first + 2);
+    lds_barrier();
+    if constexpr (DP <= 128 && QT == 1) {   // the buffers' offsets in the instructions
+      for (int step = first;;) {
+        body(std::integral_constant<int, 0>{}, step);
+        if (++step >= end) break;
+        body(std::integral_constant<int, 1>{}, step);
+        if (++step >= end) break;
+      }
+    } else {   // (the registers do not suffice for that)
+      for (int step = first; step < end; ++step) body((step - first) & 1, step);
+    }
   }
 
   l = halves_sum(l);
