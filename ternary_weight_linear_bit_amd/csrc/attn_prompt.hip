@@ -37,11 +37,12 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256, kStep = kAttnStep, kCols = 128;
-// Byte offset of 16-byte group `at` of a key's row in LDS.
+// Byte offset of 16-byte group `at` of a key's row in LDS.  Eight lanes at a time read
+// one group of keys b, b + 8 (b = 4 c .. 4 c + 3), or write groups 0, 2, .. 14 of one key:
+// both fall on eight different eighths of 128 bytes (32 banks).
 template <int DP>
 __device__ __forceinline__ int k_group(int key, int at) {
-  const int f = DP == 64 ? key >> 1 : key;   // two 128-byte rows span the banks
-  return key * DP * 2 + ((at ^ f) & (DP / 8 - 1)) * 16;
+  return key * DP * 2 + (((at ^ (at >> 3)) ^ (key ^ ((key >> 1) & 4))) & (DP / 8 - 1)) * 16;
 }
 __device__ __forceinline__ int v_group(int dim, int at) {
   return dim * kStep * 2 + ((at ^ dim) & 7) * 16;
@@ -257,20 +258,17 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
     // some column of the wave sees some key of this step
     const bool any = wave * 32 < tile.nc && key0 <= pos_hi && key0 + kStep - 1 >= from_lo;
     v16f s[2];
-    if (any) {
 #pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
+    for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) s[kt][j] = 0.0f;
-        const int key = kt * 32 + krow;
+      for (int j = 0; j < 16; ++j) s[kt][j] = 0.0f;
+      const int key = kt * 32 + krow;
 #pragma unroll
-        for (int kc = 0; kc < KC; ++kc) {
-          const v8h kk = *reinterpret_cast<const v8h*>(
-              buf + k_group<DP>(key, 2 * kc + h));
+      for (int kc = 0; kc < KC; ++kc) {
+        const v8h kk = *reinterpret_cast<const v8h*>(buf + k_group<DP>(key, 2 * kc + h));
 #pragma unroll
-          for (int n = 0; n < QT; ++n)
-            s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, q[n][kc], s[kt], 0, 0, 0);
-        }
+        for (int n = 0; n < QT; ++n)
+          s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, q[n][kc], s[kt], 0, 0, 0);
       }
     }
     stage(lds + (1 - B) * kBuf);
