@@ -17,7 +17,7 @@
 //     and out two terms.  m follows the running maximum only when it grows by more
 //     than 2^8, so that the accumulators are seldom rescaled; p stays below 2^15.
 //   * Sums over keys and the softmax sum are fp32 (the latter of the unrounded p, over
-//     each page's dv).
+//     each page's dv: of the rounded ones, two a dot instruction, lse lost 2^-12).
 // Products: S[key][column] = K Q^T in 32 x 32 tiles, where row r of a tile reads key
 // 16 (r / 16) + 8 (r / 4 % 2) + 4 (r / 8 % 2) + r % 4: a lane's 16 results are then keys
 // 8 h .. 8 h + 7 and 16 + 8 h .. of its column (h = lane / 32), the operands of
@@ -72,7 +72,7 @@ __device__ __forceinline__ void h2_rest(uint32_t h, float& a, float& b) {
 __device__ __forceinline__ float halves_max(float v) {
   const uint32_t u = __float_as_uint(v);
   auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-  return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  return __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
 __device__ __forceinline__ float halves_sum(float v) {
   const uint32_t u = __float_as_uint(v);
@@ -168,36 +168,40 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
     }
   }
 
-  // Codes of a step: thread t stages 16 dims of keys t / (DP / 16) + .., and 16 keys of
-  // dims t / 4 + ..
+  // Pages of a step's four groups of 16 keys: group lane % 4 in each lane.  An id
+  // outside the cache reads page 0; its keys are not seen.
   const int last = max(tile.sp.len - 1, 0);
   const int32_t* table = b.table + (int64_t)seq * b.width;
-  auto page_of = [&](int key) -> int { return table[min(key, last) >> plan.page_shift]; };
-  auto clamped = [&](int pid) -> int64_t { return (uint32_t)pid < (uint32_t)c.pages ? pid : 0; };
+  auto page_of = [&](int step) -> int {
+    return table[min(step * kStep + (lane & 3) * 16, last) >> plan.page_shift];
+  };
+  auto clamped = [&](int pid) -> uint32_t { return (uint32_t)pid < (uint32_t)c.pages ? pid : 0; };
+
+  // Codes of a step: thread t stages 16 dims of the keys key_of(n), and 16 keys (group
+  // t % 4) of dims t / 4 + 64 n.  A wave's keys of one n lie in one group.
   const int kc_of = tid % (DP / 16), vq = tid & 3;
   auto key_of = [&](int n) -> int { return (tid + n * kThreads) / (DP / 16); };
+  auto group_of = [&](int n) -> int { return (wave * 64 + n * kThreads) / (DP / 16) / 16; };
+  const uint32_t page_bytes = (uint32_t)c.kv_heads * P * D;   // below 2^31
+  const int8_t *k_head = c.k + (int64_t)head * P * D, *v_head = c.v + (int64_t)head * P * D;
   // offsets in a page, for its first 64 slots (a page of 128 adds those of the step)
-  const int64_t head_at = (int64_t)head * P * D, page_bytes = (int64_t)c.kv_heads * P * D;
-  int koff[NL], voff[NL];
+  uint32_t koff[NL], voff[NL];
 #pragma unroll
   for (int n = 0; n < NL; ++n) {
     // dims past the head read dim 0: their queries are 0
     koff[n] = (key_of(n) & (P - 1)) * D + (kc_of * 16 < D ? kc_of * 16 : 0);
     voff[n] = min((tid >> 2) + 64 * n, D - 1) * P + ((vq * 16) & (P - 1));
   }
-  int pk[NL], pv;   // pages of the next load
-  auto find = [&](int step) {
-#pragma unroll
-    for (int n = 0; n < NL; ++n) pk[n] = page_of(step * kStep + key_of(n));
-    pv = page_of(step * kStep + vq * 16);
-  };
   uint4 kr[NL], vr[NL];
-  auto load = [&](int step) {
+  auto load = [&](int step, int pid) {
     const int at = (step * kStep) & (P - 1);
+    const uint32_t page = clamped(pid);
 #pragma unroll
-    for (int n = 0; n < NL; ++n)
-      kr[n] = *reinterpret_cast<const uint4*>(c.k + head_at + at * D + clamped(pk[n]) * page_bytes + koff[n]);
-    const int8_t* vp = c.v + head_at + at + clamped(pv) * page_bytes;
+    for (int n = 0; n < NL; ++n) {
+      const uint32_t pk = __builtin_amdgcn_readlane(page, group_of(n));
+      kr[n] = *reinterpret_cast<const uint4*>(k_head + ((uint64_t)pk * page_bytes + at * D) + koff[n]);
+    }
+    const int8_t* vp = v_head + ((uint64_t)page * page_bytes + at);
 #pragma unroll
     for (int n = 0; n < NL; ++n) vr[n] = *reinterpret_cast<const uint4*>(vp + voff[n]);
   };
@@ -223,12 +227,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
     }
   };
 
-  // scales of a step's four groups of 16 keys, in lanes 0 .. 3 of every wave: loaded a
-  // step ahead, looked at when they are used
-  int gp, gp_next;   // pages of this step's groups, and of the next one's
+  // scales of a step's groups: loaded a step ahead, looked at when they are used
+  int g0, g1, g2;   // pages of this step, the next, the one after
   float dk, dv;
   auto scales = [&](int pid) {
-    const int64_t at = clamped(pid) * c.kv_heads + head;
+    const uint64_t at = (uint64_t)clamped(pid) * (uint32_t)c.kv_heads + head;
     dk = c.k_scale[at];
     dv = c.v_scale[at];
   };
@@ -249,11 +252,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
   auto body = [&](auto B, int step) {   // B: 0 or 1, a constant where the loop is unrolled
     const uint8_t* buf = lds + B * kBuf;
     // no page: scale -1; a scale that no visible key can have (another page's memory): 1
-    const float dk_now = (uint32_t)gp < (uint32_t)c.pages ? dk : -1.0f;
+    const float dk_now = (uint32_t)g0 < (uint32_t)c.pages ? dk : -1.0f;
     const float dv_now = is_scale(dv) ? dv : 1.0f;
-    gp = gp_next;
-    scales(gp);
-    gp_next = page_of((step + 2) * kStep + (lane & 3) * 16);
+    scales(g1);
+    g0 = g1;
+    g1 = g2;
     const int key0 = step * kStep;
     // some column of the wave sees some key of this step
     const bool any = wave * 32 < tile.nc && key0 <= pos_hi && key0 + kStep - 1 >= from_lo;
@@ -272,8 +275,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
       }
     }
     stage(lds + (1 - B) * kBuf);
-    load(step + 2);
-    find(step + 3);
+    g2 = page_of(step + 3);   // before the codes: the next step waits for it, not for them
+    load(step + 2, g1);
     if (any) {
       const float lv = __builtin_amdgcn_logf(dv_now), rdv = __builtin_amdgcn_rcpf(dv_now);
       float ck[4], lg[4], rg[4];
@@ -304,12 +307,12 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
       for (int g = 0; g < 4; ++g) {
         float t = s[g >> 1][8 * (g & 1)];
 #pragma unroll
-        for (int j = 1; j < 8; ++j) t = fmaxf(t, s[g >> 1][8 * (g & 1) + j]);
-        mx = fmaxf(mx, __builtin_fmaf(t, ck[g], lg[g]));
+        for (int j = 1; j < 8; ++j) t = __builtin_fmaxf(t, s[g >> 1][8 * (g & 1) + j]);
+        mx = __builtin_fmaxf(mx, __builtin_fmaf(t, ck[g], lg[g]));
       }
       mx = halves_max(mx);
       if (__builtin_amdgcn_ballot_w64(mx > m + kSlack)) {
-        const float to = fmaxf(m, mx);
+        const float to = __builtin_fmaxf(m, mx);
         const float alpha = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
         m = to;
         l *= alpha;
@@ -356,15 +359,13 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
   };
 
   if (first < end) {
-    find(first);
-    load(first);
-    gp = page_of(first * kStep + (lane & 3) * 16);
-    scales(gp);
+    g0 = page_of(first);
+    g1 = page_of(first + 1);
+    g2 = page_of(first + 2);
+    load(first, g0);
+    scales(g0);
     stage(lds);
-    find(first + 1);
-    load(first + 1);
-    gp_next = page_of((first + 1) * kStep + (lane & 3) * 16);
-    find(first + 2);
+    load(first + 1, g1);
     lds_barrier();
     if constexpr (DP <= 128 && QT == 1) {   // the buffers' offsets in the instructions
       for (int step = first;;) {
