@@ -36,7 +36,7 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-constexpr int kThreads = 256, kStep = kAttnStep, kCols = 128;
+constexpr int kStep = kAttnStep;
 // Byte offset of 16-byte group `at` of a key's row in LDS.  Eight lanes at a time read
 // one group of keys b, b + 8 (b = 4 c .. 4 c + 3), or write groups 0, 2, .. 14 of one key:
 // both fall on eight different eighths of 128 bytes (32 banks).
@@ -88,12 +88,13 @@ __device__ __forceinline__ bool is_scale(float v) {
   return __float_as_uint(v) - 1u < 0x7f7fffffu;
 }
 
-// QT / PT: fp16 terms of a query and of a weight.
-template <int DP, int QT, int PT, bool QB, bool OB>
-__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kernel(
+// NW: waves (32 columns each).  QT / PT: fp16 terms of a query and of a weight.
+template <int DP, int NW, int QT, int PT, bool QB, bool OB>
+__global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel(
     const KvCache c, const KvBatch b, const AttnArgs a, const AttnPlan plan,
     float* __restrict__ part) {
-  constexpr int KC = DP / 16, DT = DP / 32, NL = DP / 64;   // NL: 16-code loads of K (and of V) a thread
+  constexpr int kThreads = 64 * NW, kCols = 32 * NW;
+  constexpr int KC = DP / 16, DT = DP / 32, NL = DP / (16 * NW);   // NL: 16-code loads of K (and V) a thread
   constexpr int kKBytes = kStep * DP * 2, kBuf = 2 * kKBytes;
   extern __shared__ uint4 lds4[];
   uint8_t* lds = reinterpret_cast<uint8_t*>(lds4);
@@ -178,9 +179,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
   auto clamped = [&](int pid) -> uint32_t { return (uint32_t)pid < (uint32_t)c.pages ? pid : 0; };
 
   // Codes of a step: thread t stages 16 dims of the keys key_of(n), and 16 keys (group
-  // t % 4) of dims t / 4 + 64 n.  A wave's keys of one n lie in one group.
+  // t % 4) of dims dim_of(n).  A wave's keys of one n lie in one group.
   const int kc_of = tid % (DP / 16), vq = tid & 3;
   auto key_of = [&](int n) -> int { return (tid + n * kThreads) / (DP / 16); };
+  auto dim_of = [&](int n) -> int { return (tid + n * kThreads) >> 2; };
   auto group_of = [&](int n) -> int { return (wave * 64 + n * kThreads) / (DP / 16) / 16; };
   const uint32_t page_bytes = (uint32_t)c.kv_heads * P * D;   // below 2^31
   const int8_t *k_head = c.k + (int64_t)head * P * D, *v_head = c.v + (int64_t)head * P * D;
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
   for (int n = 0; n < NL; ++n) {
     // dims past the head read dim 0: their queries are 0
     koff[n] = (key_of(n) & (P - 1)) * D + (kc_of * 16 < D ? kc_of * 16 : 0);
-    voff[n] = min((tid >> 2) + 64 * n, D - 1) * P + ((vq * 16) & (P - 1));
+    voff[n] = min(dim_of(n), D - 1) * P + ((vq * 16) & (P - 1));
   }
   uint4 kr[NL], vr[NL];
   auto load = [&](int step, int pid) {
@@ -216,7 +218,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
         codes_to_h4(kw[j], x + 2 * j);
         codes_to_h4(vw[j], y + 2 * j);
       }
-      const int key = key_of(n), dim = (tid >> 2) + 64 * n;
+      const int key = key_of(n), dim = dim_of(n);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         *reinterpret_cast<uint4*>(buf + k_group<DP>(key, 2 * kc_of + j)) =
@@ -421,26 +423,44 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_prompt_kerne
 
 template <int DP>
 const void* pick_prompt(bool qb, bool ob) {
-  return qb ? (ob ? (const void*)attn_prompt_kernel<DP, 1, 1, true, true>
-                  : (const void*)attn_prompt_kernel<DP, 1, 1, true, false>)
-            : (ob ? (const void*)attn_prompt_kernel<DP, 2, 1, false, true>
-                  : (const void*)attn_prompt_kernel<DP, 2, 2, false, false>);
+  return qb ? (ob ? (const void*)attn_prompt_kernel<DP, 4, 1, 1, true, true>
+                  : (const void*)attn_prompt_kernel<DP, 4, 1, 1, true, false>)
+            : (ob ? (const void*)attn_prompt_kernel<DP, 4, 2, 1, false, true>
+                  : (const void*)attn_prompt_kernel<DP, 4, 2, 2, false, false>);
+}
+
+constexpr int kTileCols = 128, kWideCols = 256;
+
+int64_t tiles_of(const KvCache& c, const KvBatch& b, int q_heads, int cols) {
+  const int64_t all = (int64_t)b.max_new * (q_heads / c.kv_heads);
+  return (int64_t)b.seqs * c.kv_heads * ((all + cols - 1) / cols);
 }
 
 }  // namespace
 
 AttnPlan attn_prompt_plan(const KvCache& c, const KvBatch& b, int q_heads) {
-  return attn_plan(c, b, q_heads, kCols, 512, 8);
+  return attn_plan(c, b, q_heads, kTileCols, 512, 8);
 }
 
 hipError_t launch_attn_prompt(const KvCache& c, const KvBatch& b, const AttnArgs& a,
-                              const AttnPlan& p, bool q_bf16, bool out_bf16, void* workspace,
+                              const AttnPlan& plan, bool q_bf16, bool out_bf16, void* workspace,
                               hipStream_t s) {
-  const int64_t grid = (int64_t)b.seqs * c.kv_heads * p.tiles * p.splits;
-  if (grid > 2147483647) return hipErrorInvalidValue;
+  AttnPlan p = plan;
   float* part = static_cast<float*>(workspace);
   const int dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
-  const void* kern = dp == 64 ? pick_prompt<64>(q_bf16, out_bf16)
+  // Eight waves share a step's conversion between 256 columns: bf16 queries of 65 to 128
+  // dims with a workgroup for every compute unit (8192 tokens of 32 heads: 604 -> 576 us).
+  // Fewer take four waves, whose workgroups are twice as many (and split the keys).
+  const bool wide = dp == 128 && q_bf16 && tiles_of(c, b, a.q_heads, kWideCols) >= 256;
+  if (wide) {
+    p = attn_plan(c, b, a.q_heads, kWideCols, 1, 8);
+    p.splits = 1;
+  }
+  const int64_t grid = (int64_t)b.seqs * c.kv_heads * p.tiles * p.splits;
+  if (grid > 2147483647) return hipErrorInvalidValue;
+  const void* kern = wide ? (out_bf16 ? (const void*)attn_prompt_kernel<128, 8, 1, 1, true, true>
+                                      : (const void*)attn_prompt_kernel<128, 8, 1, 1, true, false>)
+                     : dp == 64 ? pick_prompt<64>(q_bf16, out_bf16)
                      : dp == 128 ? pick_prompt<128>(q_bf16, out_bf16) : pick_prompt<256>(q_bf16, out_bf16);
   const size_t lds = (size_t)2 * 2 * kStep * dp * 2;   // two buffers of K and V in fp16
   if (lds > 65536) {
@@ -448,7 +468,7 @@ hipError_t launch_attn_prompt(const KvCache& c, const KvBatch& b, const AttnArgs
     if (e != hipSuccess) return e;
   }
   void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&p, (void*)&part};
-  const hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(kThreads), args, lds, s);
+  const hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(p.cols * 2), args, lds, s);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_attn_join(c, b, a, p, 1.0f, out_bf16, part, s);
 }
