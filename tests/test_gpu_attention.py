@@ -102,6 +102,16 @@ def test_prompts(heads, q_heads, dim, page, dt):
     run(heads, q_heads, dim, page, [200, 1, 65, 129, 0, 64], [200, 77, 65, 300, 5, 191], dt, seed=page + dim)
 
 
+@pytest.mark.parametrize("dim", [128, 80])
+@pytest.mark.parametrize("page,out_dt", [(16, "bf16"), (128, "f32")])
+def test_wide_prompts(dim, page, out_dt):
+    """Enough bf16 columns for the workgroups of 256: whole, partly and barely filled, with
+    step counts on every residue of the buffers, and windows."""
+    news, lens = [130, 1, 40, 5], [130, 450, 300, 70]
+    run(64, 128, dim, page, news, lens, "bf16", out_dt, seed=dim)
+    run(86, 86, dim, page, [257, 20, 1], [257, 220, 129], "bf16", out_dt, seed=dim, window=65)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("window", [1, 2, 16, 63, 64, 65, 200, 10 ** 9])
 def test_windows(dt, window):
