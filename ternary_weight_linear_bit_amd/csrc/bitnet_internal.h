@@ -544,7 +544,6 @@ struct KvRows {
   int rot;                   // rotated dims (0: none)
   int neighbours;            // pairs (2i, 2i + 1) instead of (i, i + rot / 2)
 };
-constexpr int kKvQRows = 4;  // rows of queries that one workgroup rotates
 hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const KvRows& r, bool bf16,
                             hipStream_t s);
 

@@ -264,10 +264,36 @@ __global__ __launch_bounds__(NT) void residual_kernel(const ResidualArgs p, int 
   }
 }
 
+// Threads of a workgroup.  Rows of up to 4096 fit one or two groups a thread; one each
+// for few tokens, whose time is the chain of the sums (2560 wide: 4.1 -> 3.8 us), and
+// small workgroups for small rows (4096 x 640: 15.2 -> 10.3 us).  Longer rows take more
+// threads (2048 x 8192, fp32 stream: 57.6 -> 48.6 us; one token of 14336: 9.9 -> 6.1),
+// but sixteen waves leave a compute unit one workgroup, so that many tokens rather read
+// part of h' again (2048 x 10240, bf16: 59.6 with 1024 threads, 47.6 with 512).
 template <bool YB, bool HB>
-const void* residual_pick(bool vec) {
-  return vec ? (const void*)residual_kernel<YB, HB, 8, 256, 2>
-             : (const void*)residual_kernel<YB, HB, 1, 256, 8>;
+const void* residual_pick(bool vec, int64_t K, int64_t M, int* threads) {
+  if (!vec) {
+    *threads = 256;
+    return (const void*)residual_kernel<YB, HB, 1, 256, 8>;
+  }
+  if (K <= 1024) {
+    *threads = 128;
+    return (const void*)residual_kernel<YB, HB, 8, 128, 1>;
+  }
+  if (K <= 4096 && M > 64) {
+    *threads = 256;
+    return (const void*)residual_kernel<YB, HB, 8, 256, 2>;
+  }
+  if (K <= 4096) {
+    *threads = 512;
+    return (const void*)residual_kernel<YB, HB, 8, 512, 1>;
+  }
+  if (K <= 8192 || M > 256) {
+    *threads = 512;
+    return (const void*)residual_kernel<YB, HB, 8, 512, 2>;
+  }
+  *threads = 1024;
+  return (const void*)residual_kernel<YB, HB, 8, 1024, 2>;
 }
 
 }  // namespace
@@ -278,11 +304,14 @@ hipError_t launch_residual(const ResidualArgs& a, bool y_bf16, bool h_bf16, bool
   const bool vec = a.K % 8 == 0 && al(a.y, 16) && al(a.h, 16) && al(a.gate, 16) && al(a.h_out, 16) &&
                    al(a.u, 16) && al(a.post, 16) && al(a.pre, 16) && al(a.xq, 8) &&
                    a.gate_stride % 8 == 0;
-  const void* kern = y_bf16 ? (h_bf16 ? residual_pick<true, true>(vec) : residual_pick<true, false>(vec))
-                            : (h_bf16 ? residual_pick<false, true>(vec) : residual_pick<false, false>(vec));
+  int threads;
+  const void* kern = y_bf16 ? (h_bf16 ? residual_pick<true, true>(vec, a.K, M, &threads)
+                                      : residual_pick<true, false>(vec, a.K, M, &threads))
+                            : (h_bf16 ? residual_pick<false, true>(vec, a.K, M, &threads)
+                                      : residual_pick<false, false>(vec, a.K, M, &threads));
   const int ub = u_bf16 ? 1 : 0;
   void* args[] = {(void*)&a, (void*)&ub};
-  return hipLaunchKernel(kern, dim3((unsigned)M), dim3(256), args, 0, s);
+  return hipLaunchKernel(kern, dim3((unsigned)M), dim3((unsigned)threads), args, 0, s);
 }
 
 }  // namespace bitnet
