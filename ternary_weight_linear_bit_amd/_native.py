@@ -680,15 +680,14 @@ _RESIDUAL = struct.Struct("@PPPPPPPPPqqqiiiff0q")
 
 def _one_device(*ts):
     """The device of every tensor (None: absent): its kernels read them all."""
-    index, first = None, None
+    first = None
     for t in ts:
-        if t is None:
-            continue
-        i = t.get_device()
-        if index is None:
-            index, first = i, t
-        elif i != index or (i < 0 and t.device != first.device):
-            raise ValueError(f"tensors lie on {first.device} and {t.device}")
+        if t is not None:
+            i = t.get_device()
+            if first is None:
+                index, first = i, t
+            elif i != index or (i < 0 and t.device != first.device):
+                raise ValueError(f"tensors lie on {first.device} and {t.device}")
     return None if first is None else first.device
 
 
@@ -707,8 +706,9 @@ def _code(dtype, name):
 
 
 def _like(t, shape, dtype, name):
-    """_expect for one dtype, quick where the tensor is as expected."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+    """_expect for one dtype, quick where the tensor is as expected (that it lies on the
+    GPU is seen by _one_device and _On)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         _expect(t, shape, dtype, name)
 
 
@@ -720,17 +720,17 @@ class _On:
 
     def __init__(self, device, stream):
         import torch
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is one of {stream.device}, the tensors lie on {device}")
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be CUDA tensors, not {device}")
-        self._index = device.index
         if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is one of {stream.device}, the tensors lie on {device}")
             self._guard = torch.cuda.stream(stream)       # its device too
-        elif torch.cuda.current_device() != device.index:
+        elif device.type != "cuda":
+            raise ValueError(f"tensors must be CUDA tensors, not {device}")
+        elif torch._C._cuda_getDevice() != device.index:
             self._guard = torch.cuda.device(device)
         else:
             self._guard = None
+        self._index = device.index
 
     def __enter__(self):
         import torch
@@ -960,12 +960,12 @@ def bitnet_residual_norm(y, h, h_out=None, post_weight=None, gate=None, scale=1.
     device = _one_device(y, h, h_out, post_weight, gate, pre_weight, u, x_q, x_scale)
     with _On(device, stream) as s:
         if h_out is None:
-            h_out = torch.empty(shape, dtype=hd, device=device)
+            h_out = torch.empty_like(h)
         if quantize:
             if x_q is None:
-                x_q = torch.empty(shape, dtype=torch.int8, device=device)
+                x_q = torch.empty_like(y, dtype=torch.int8)
             if x_scale is None:
-                x_scale = torch.empty(m, dtype=f32, device=device)
+                x_scale = y.new_empty(m, dtype=f32)
             pq, ps = x_q.data_ptr(), x_scale.data_ptr()
         args = _RESIDUAL.pack(y.data_ptr(), h.data_ptr(), pg, h_out.data_ptr(), pu, p1, p2, pq, ps, m, k,
                               gate_stride, y_code, h_code, u_code, scale, eps)
