@@ -29,15 +29,15 @@
 // row column c and quarter g (lanes 16 g ..) ends up with the 16 consecutive keys
 // 16 g .. 16 g + 15: exactly the operand of O[dim][row] = V^T P^T, whose other side
 // is 16 consecutive bytes of the cache's value rows.  Weights never leave their lane.
-// Columns are (row, query head of the group) pairs, 16 a workgroup.  The four waves
-// of a workgroup take every fourth step and are joined in LDS; the keys of a
-// sequence are split over workgroups (attn_splits) and joined by a second kernel.
+// Columns are (row, query head of the group) pairs, 16 a workgroup.  The NW waves of a
+// workgroup take every NW-th step and are joined in LDS; the keys of a sequence are
+// split over workgroups (attn_part) and joined by a second kernel.
 #include "attn_internal.h"
 
 namespace bitnet {
 namespace {
 
-constexpr int kThreads = 256, kWaves = 4, kStep = kAttnStep, kCols = 16;
+constexpr int kWaves = 4, kManyWaves = 8, kStep = kAttnStep, kCols = 16;
 
 // Fixed point of a digit count.
 template <int ND>
@@ -95,13 +95,14 @@ __device__ __forceinline__ float rows_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-template <int DP, int ND, bool QB, bool OB>
-__global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kernel(
+template <int DP, int NW, int ND, bool QB, bool OB>
+__global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel(
     const KvCache c, const KvBatch b, const AttnArgs a, const AttnPlan plan,
     float* __restrict__ part) {
-  constexpr int KC = DP / 64, DT = DP / 16, HT = DT < 8 ? DT : 8;   // dims joined at a time: 16 HT
-  __shared__ float sm[kWaves][kCols], sl[kWaves][kCols];
-  __shared__ float so[kWaves][kCols][16 * HT + 4];
+  constexpr int kThreads = 64 * NW;
+  constexpr int KC = DP / 64, DT = DP / 16, HT = DT < 32 / NW ? DT : 32 / NW;   // 16 HT dims joined at a time
+  __shared__ float sm[NW][kCols], sl[NW][kCols];
+  __shared__ float so[NW][kCols][16 * HT + 4];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 15, g = lane >> 4;
   int unit = blockIdx.x;
   const int split = unit % plan.splits;
@@ -196,7 +197,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
     for (int i = 0; i < 4; ++i) o[dt][i] = 0.0f;
 
   const int s_begin = tile.step0 + s_lo + wave, s_end = tile.step0 + s_hi;
-  int pid_v = 0, pid_k1 = 0, pid_v1 = 0;   // this step's, the next one's
+  // pages of this step, of the next and of the one after: an id is loaded ahead of the
+  // codes of the step before its own, so that no wait for it waits for them
+  int pid_v = 0, pid_k1 = 0, pid_v1 = 0, pid_k2 = 0, pid_v2 = 0;
   float dk = 0.0f, dv = 1.0f;
   auto scales = [&](int pid) {
     const int64_t at = (int64_t)((uint32_t)pid < (uint32_t)c.pages ? pid : 0) * c.kv_heads + head;
@@ -206,14 +209,14 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
   if (s_begin < s_end) {
     const int pk = page_of(s_begin, col >> 2);
     pid_v = page_of(s_begin, g);
-    pid_k1 = page_of(s_begin + kWaves, col >> 2);
-    pid_v1 = page_of(s_begin + kWaves, g);
+    pid_k1 = page_of(s_begin + NW, col >> 2);
+    pid_v1 = page_of(s_begin + NW, g);
     load_k(s_begin, pk);
     scales(pid_v);
     load_v(s_begin, pid_v);
   }
-  for (int step = s_begin; step < s_end; step += kWaves) {
-    const bool more = step + kWaves < s_end;
+  for (int step = s_begin; step < s_end; step += NW) {
+    const bool more = step + NW < s_end;
     float x[4][4];   // the products first, as numbers
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -233,7 +236,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
         x[t][i] = joined<ND>(d);
       }
     }
-    if (more) load_k(step + kWaves, pid_k1);
+    pid_k2 = page_of(step + 2 * NW, col >> 2);
+    pid_v2 = page_of(step + 2 * NW, g);
+    if (more) load_k(step + NW, pid_k1);
 
     // x = log2 e s + log2 dv of the lane's 16 keys; -inf where the row sees none
     const int j0 = step * kStep + g * 16;
@@ -286,10 +291,10 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
       }
     }
     if (more) {
-      load_v(step + kWaves, pid_v1);
+      load_v(step + NW, pid_v1);
       pid_v = pid_v1;
-      pid_k1 = page_of(step + 2 * kWaves, col >> 2);
-      pid_v1 = page_of(step + 2 * kWaves, g);
+      pid_k1 = pid_k2;
+      pid_v1 = pid_v2;
     }
   }
 
@@ -302,9 +307,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
   __syncthreads();
   float top = sm[0][col], total = 0.0f;
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sm[w][col]);
+  for (int w = 1; w < NW; ++w) top = fmaxf(top, sm[w][col]);
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w)
+  for (int w = 0; w < NW; ++w)
     total += sm[w][col] == -INFINITY ? 0.0f : sl[w][col] * __builtin_amdgcn_exp2f(sm[w][col] - top);
   const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
   const int64_t pu = (int64_t)blockIdx.x * plan.part_cols;
@@ -323,7 +328,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
       const int ec = e / (nd / 4), d = (e - ec * (nd / 4)) * 4;
       float4 y = *reinterpret_cast<const float4*>(&so[0][ec][d]);
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) {
+      for (int w = 1; w < NW; ++w) {
         const float4 z = *reinterpret_cast<const float4*>(&so[w][ec][d]);
         y.x += z.x;
         y.y += z.y;
@@ -333,9 +338,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
       if (alone) {
         float et = sm[0][ec], el = 0.0f;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) et = fmaxf(et, sm[w][ec]);
+        for (int w = 1; w < NW; ++w) et = fmaxf(et, sm[w][ec]);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
+        for (int w = 0; w < NW; ++w)
           el += sm[w][ec] == -INFINITY ? 0.0f : sl[w][ec] * __builtin_amdgcn_exp2f(sm[w][ec] - et);
         const float r = el > 0.0f ? 1.0f / (el * Digits<ND>::kTop) : 0.0f;
         const int oc = tile.c0 + ec, orow = oc / group;
@@ -362,22 +367,38 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void attn_decode_kerne
 }
 
 // ND = 3 for fp32 in and out, else 2.
-template <int DP>
+template <int DP, int NW>
 const void* pick_decode(bool qb, bool ob) {
-  return qb ? (ob ? (const void*)attn_decode_kernel<DP, 2, true, true>
-                  : (const void*)attn_decode_kernel<DP, 2, true, false>)
-            : (ob ? (const void*)attn_decode_kernel<DP, 2, false, true>
-                  : (const void*)attn_decode_kernel<DP, 3, false, false>);
+  return qb ? (ob ? (const void*)attn_decode_kernel<DP, NW, 2, true, true>
+                  : (const void*)attn_decode_kernel<DP, NW, 2, true, false>)
+            : (ob ? (const void*)attn_decode_kernel<DP, NW, 2, false, true>
+                  : (const void*)attn_decode_kernel<DP, NW, 3, false, false>);
 }
+template <int NW>
+const void* pick_decode(int dim, bool qb, bool ob) {
+  if constexpr (NW == kWaves)
+    if (dim > 128) return pick_decode<256, NW>(qb, ob);
+  return dim <= 64 ? pick_decode<64, NW>(qb, ob) : pick_decode<128, NW>(qb, ob);
+}
+
+constexpr int64_t kOneLaunch = kManyWaves;   // steps up to which no keys are split
 
 }  // namespace
 
 // Two workgroups per compute unit; no part is shorter than one step a wave.  (Four
 // times as many for batches of uneven lengths: 64 sequences of 1 .. 8191 tokens 131 ->
 // 130 us, but four of 65536 115 -> 175 us: a part's start and end cost about as much as
-// four steps.)
+// four steps.)  Up to eight steps, eight waves a workgroup take them at one step a wave in
+// one launch (300 tokens of 20 heads 9.2 -> 8.4 us with the join; at two steps a wave
+// 9.5 -> 10.2).
 AttnPlan attn_decode_plan(const KvCache& c, const KvBatch& b, int q_heads) {
-  return attn_plan(c, b, q_heads, kCols, 512, kWaves);
+  AttnPlan p = attn_plan(c, b, q_heads, kCols, 512, kWaves);
+  p.waves = kWaves;
+  if (p.splits > 1 && b.max_len <= kOneLaunch * kStep && c.head_dim <= 128) {
+    p.splits = 1;
+    p.waves = kManyWaves;
+  }
+  return p;
 }
 
 hipError_t launch_attn_decode(const KvCache& c, const KvBatch& b, const AttnArgs& a,
@@ -386,11 +407,10 @@ hipError_t launch_attn_decode(const KvCache& c, const KvBatch& b, const AttnArgs
   const int64_t grid = (int64_t)b.seqs * c.kv_heads * p.tiles * p.splits;
   if (grid > 2147483647) return hipErrorInvalidValue;
   float* part = static_cast<float*>(workspace);
-  const int dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
-  const void* kern = dp == 64 ? pick_decode<64>(q_bf16, out_bf16)
-                     : dp == 128 ? pick_decode<128>(q_bf16, out_bf16) : pick_decode<256>(q_bf16, out_bf16);
+  const void* kern = p.waves == kManyWaves ? pick_decode<kManyWaves>(c.head_dim, q_bf16, out_bf16)
+                                           : pick_decode<kWaves>(c.head_dim, q_bf16, out_bf16);
   void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&p, (void*)&part};
-  const hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(kThreads), args, 0, s);
+  const hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(64 * p.waves), args, 0, s);
   if (e != hipSuccess || p.splits == 1) return e;
   const float unit = !q_bf16 && !out_bf16 ? Digits<3>::kTop : Digits<2>::kTop;
   return launch_attn_join(c, b, a, p, unit, out_bf16, part, s);

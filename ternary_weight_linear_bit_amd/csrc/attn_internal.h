@@ -62,6 +62,7 @@ struct AttnPlan {
   int cols, tiles;          // columns a workgroup, tiles of a sequence
   int splits, least;
   int part_cols;            // columns of a tile's partial sums
+  int waves;                // of a workgroup
 };
 // A part of a tile in the workspace: part_cols columns of head_dim + 4 floats: the
 // maximum m (log2), the sum of 2^(x - m) / dv, two unused, and the sums over 2^(x - m) vc
@@ -72,7 +73,7 @@ hipError_t launch_attn_join(const KvCache& c, const KvBatch& b, const AttnArgs& 
 
 inline AttnPlan attn_plan(const KvCache& c, const KvBatch& b, int q_heads, int cols,
                           int workgroups, int least) {
-  AttnPlan p;
+  AttnPlan p{};
   p.group = q_heads / c.kv_heads;
   p.page_shift = 4;
   while ((1 << p.page_shift) < c.page) ++p.page_shift;
