@@ -261,7 +261,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
     g1 = g2;
     const int key0 = step * kStep;
     // some column of the wave sees some key of this step
-    const bool any = wave * 32 < tile.nc && key0 <= pos_hi && key0 + kStep - 1 >= from_lo;
+    const bool any = key0 <= pos_hi && key0 + kStep - 1 >= from_lo;
     v16f s[2];
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
@@ -369,7 +369,15 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
     stage(lds);
     load(first + 1, g1);
     lds_barrier();
-    if constexpr (DP <= 128 && QT == 1) {   // the buffers' offsets in the instructions
+    if (wave * 32 >= tile.nc) {   // no columns: the wave only stages (a sequence of few rows)
+      for (int step = first; step < end; ++step) {
+        g1 = g2;
+        stage(lds + (1 - ((step - first) & 1)) * kBuf);
+        g2 = page_of(step + 3);
+        load(step + 2, g1);
+        lds_barrier();
+      }
+    } else if constexpr (DP <= 128 && QT == 1) {   // the buffers' offsets in the instructions
       for (int step = first;;) {
         body(std::integral_constant<int, 0>{}, step);
         if (++step >= end) break;
