@@ -461,7 +461,8 @@ bitnet_status bitnet_chain_error(const bitnet_chain *chain, int *error);
  *   head_dim  a multiple of 16, 16 to 256.
  *   kv_heads  1 to 65535; pages 1 to 2^31 - 1 (the arrays may pass 4 GiB).
  *   k, v      16-byte aligned; the scales 4-byte aligned.
- * Memory of pages that were never written may hold anything.
+ * Memory of pages that were never written may hold anything; scales of pages that are
+ * read must be positive (bitnet_kv_append writes no others for finite rows).
  */
 typedef struct bitnet_kv_cache {
   int8_t *k;       /* [pages][kv_heads][page][head_dim] */
@@ -480,13 +481,17 @@ typedef struct bitnet_kv_cache {
  * Position j lies in page table[b][j / page], slot j % page.
  *   seqs     1 to 65535 (0: nothing to do).
  *   width    page ids a row of the table holds, width * page <= 2^30.
- *   tokens   rows of the row arrays (rows outside every sequence are left alone).
+ *   tokens   rows of the row arrays, <= 2^30 (rows outside every sequence are left
+ *            alone).
  *   max_new  1 .. tokens: no sequence has more new rows (rows past it are left alone).
  *   max_len  0 .. width * page: no kv_len is larger (a larger one counts as max_len).
  * The contents are not trusted: row numbers are clamped to the batch, a kv_len
  * below 0 counts as 0, and a page id outside the cache is a page without tokens
  * (nothing is written to it, and its keys are not seen).  A row whose position is
  * negative (more new rows than tokens) has no place in the cache and sees no key.
+ * Sequences whose rows overlap (a q_start that goes back) give unspecified results.
+ * A launch covers seqs * max_new rows, most of them idle where one sequence has many
+ * rows and the others few: prompts and single tokens run faster as two batches.
  */
 typedef struct bitnet_kv_batch {
   const int32_t *table;    /* [seqs][width] */
@@ -529,9 +534,10 @@ typedef struct bitnet_kv_rows {
  *   earlier codes c become rne(RN32(c * RN32(d / d'))).
  * All results are bit-exact against that definition.  Rows must be finite (others
  * spoil their own page and head).  Slots past a sequence's last token keep their
- * bytes.  Two sequences of a batch may share pages that the call does not write;
- * a page that it writes must belong to one sequence (otherwise its contents are
- * unspecified).
+ * bytes.  Sequences may share pages that the call does not write; a page that it
+ * writes must appear once in the batch (otherwise its contents are unspecified).
+ * BITNET_ERR_SHAPE where the launch would pass 2^24 workgroups (one a row of queries
+ * and one a page, head, and keys or values).
  */
 bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, const bitnet_kv_batch *batch,
                                const bitnet_kv_rows *rows, hipStream_t stream);
@@ -542,11 +548,16 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, const bitnet_kv_bat
  * written, its own among them.
  *   s_j = softmax_scale * (q . k_j),  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),
  *   lse = m + ln sum_j e^(s_j - m),  m = max_j s_j.
- * A row that sees no key gets zeros and lse = -inf.
+ * A row that sees no key gets zeros and lse = -inf.  Sums are fp32 or exact integers;
+ * with fp32 in and out queries and weights are held to 22 bits or more, else to 11 or
+ * more (a bf16 query exactly).  The same call gives the same bits; another max_len may
+ * split the sums elsewhere.
  *   q        [tokens] rows of [q_heads][head_dim], q_stride elements apart (>= q_heads *
  *            head_dim), fp32 or bf16 (q_dtype), finite; query head h reads kv head
- *            h / (q_heads / kv_heads), q_heads a multiple of kv_heads, <= 65535.
- *   out      [tokens][q_heads][head_dim], contiguous, fp32 or bf16 (out_dtype).
+ *            h / (q_heads / kv_heads), q_heads a multiple of kv_heads, <= 65535;
+ *            max_new * (q_heads / kv_heads) <= 2^30, and at most 2^23 workgroups.
+ *   out      [tokens][q_heads][head_dim], contiguous, 16-byte aligned, fp32 or bf16
+ *            (out_dtype).
  *   lse      [tokens][q_heads] fp32, or NULL.
  *   softmax_scale  finite; window >= 0.
  *   workspace  bitnet_attention_workspace_bytes() bytes of device memory, 16-byte
@@ -574,7 +585,7 @@ size_t bitnet_attention_workspace_bytes(const bitnet_kv_cache *cache,
  *   x_q, x_scale = the codes and scales that bitnet_quantize_acts forms of u.
  * r = RN32(1 / sqrt(RN32(ms + eps))) of the row it scales, ms the exactly rounded
  * mean of squares, as in bitnet_act_prologue.  Bit-exact against that definition.
- *   M, K         M >= 0, K >= 1 (M == 0 is a no-op), M <= 2^31 - 1.
+ *   M, K         M >= 0, K >= 1 (M == 0 is a no-op), M < 2^22, K < 2^31.
  *   y            [M][K] fp32 or bf16 (y_dtype); gate has the same type.
  *   h, h_out     [M][K] fp32 or bf16 (h_dtype); h_out may be h.
  *   gate         NULL, or [M] rows of [K], gate_stride elements apart (0: one row
@@ -582,7 +593,7 @@ size_t bitnet_attention_workspace_bytes(const bitnet_kv_cache *cache,
  *   post_weight, pre_weight  NULL (no norm) or [K] fp32.
  *   u            NULL, or [M][K] fp32 or bf16 (u_dtype; not looked at when u is NULL).
  *   x_q, x_scale both NULL, or [M][K] int8 and [M] fp32.
- *   scale        finite; eps >= 0, finite.
+ *   scale        finite; eps >= 0, finite (with 0 a row of zeros has no norm: undefined).
  * Values must be finite.
  */
 typedef struct bitnet_residual {

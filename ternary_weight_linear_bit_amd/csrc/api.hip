@@ -246,7 +246,7 @@ bitnet_status check_kv_sizes(const bitnet_kv_cache& c, const bitnet_kv_batch& b)
   if (c.head_dim < 16 || c.head_dim > 256 || c.head_dim % 16 != 0) return BITNET_ERR_SHAPE;
   if (c.kv_heads < 1 || c.kv_heads > 65535 || c.pages < 1 || c.pages > kInt32Max)
     return BITNET_ERR_SHAPE;
-  if (b.seqs < 0 || b.seqs > kMaxSeqs || b.tokens < 0 || b.tokens > kInt32Max)
+  if (b.seqs < 0 || b.seqs > kMaxSeqs || b.tokens < 0 || b.tokens > kMaxCached)
     return BITNET_ERR_SHAPE;
   if (b.seqs == 0 || b.tokens == 0) return BITNET_OK;
   if (b.width < 1 || b.width > kMaxCached / c.page || b.max_new < 1 || b.max_new > b.tokens ||
@@ -277,6 +277,12 @@ bitnet::KvBatch kv_batch(const bitnet_kv_batch& b) {
 // q_heads over a cache's kv_heads.
 bool heads_fit(const bitnet_kv_cache& c, int q_heads) {
   return q_heads >= 1 && q_heads <= 65535 && q_heads % c.kv_heads == 0;
+}
+
+// Sizes of an attention call that has something to do.
+bool attention_fits(const bitnet_kv_cache& c, const bitnet_kv_batch& b, int q_heads) {
+  return b.max_new * (q_heads / c.kv_heads) <= kMaxCached &&
+         bitnet::attention_fits(kv_cache(c), kv_batch(b), q_heads);
 }
 
 }  // namespace
@@ -679,6 +685,8 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache* cache, const bitnet_kv_bat
   if (r.k_stride < kv_row || r.v_stride < kv_row || (r.q && r.q_stride < q_row))
     return BITNET_ERR_SHAPE;
   if (r.rotary > 0 && r.positions < b.max_len) return BITNET_ERR_SHAPE;
+  if (bitnet::kv_append_grid(kv_cache(c), kv_batch(b), r.q != nullptr) > bitnet::max_grid(256))
+    return BITNET_ERR_SHAPE;
   st = check_kv_arrays(c, b);
   if (st != BITNET_OK) return st;
   if (!r.k || !r.v || (r.q && !r.q_out) || (r.rotary > 0 && (!r.cos || !r.sin)))
@@ -697,7 +705,8 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache* cache, const bitnet_kv_bat
 size_t bitnet_attention_workspace_bytes(const bitnet_kv_cache* cache, const bitnet_kv_batch* batch,
                                         int q_heads) {
   if (!cache || !batch || check_kv_sizes(*cache, *batch) != BITNET_OK ||
-      !heads_fit(*cache, q_heads) || batch->seqs == 0 || batch->tokens == 0)
+      !heads_fit(*cache, q_heads) || batch->seqs == 0 || batch->tokens == 0 ||
+      !attention_fits(*cache, *batch, q_heads))
     return 0;
   return bitnet::attention_workspace_bytes(kv_cache(*cache), kv_batch(*batch), q_heads);
 }
@@ -715,11 +724,12 @@ bitnet_status bitnet_attention(const bitnet_kv_cache* cache, const bitnet_kv_bat
   if (!valid_dtype(q_dtype) || !valid_dtype(out_dtype)) return BITNET_ERR_DTYPE;
   if (!heads_fit(c, q_heads) || window < 0 || !finite(softmax_scale)) return BITNET_ERR_SHAPE;
   if (b.seqs == 0 || b.tokens == 0) return BITNET_OK;
-  if (q_stride < (int64_t)q_heads * c.head_dim) return BITNET_ERR_SHAPE;
+  if (q_stride < (int64_t)q_heads * c.head_dim || !attention_fits(c, b, q_heads))
+    return BITNET_ERR_SHAPE;
   st = check_kv_arrays(c, b);
   if (st != BITNET_OK) return st;
   if (!q || !out) return BITNET_ERR_NULL;
-  if (!aligned(q, esize(q_dtype)) || !aligned(out, esize(out_dtype)) || !aligned(lse, 4))
+  if (!aligned(q, esize(q_dtype)) || !aligned(out, 16) || !aligned(lse, 4))
     return BITNET_ERR_ALIGN;
   const bitnet::KvCache kc = kv_cache(c);
   const bitnet::KvBatch kb = kv_batch(b);
@@ -739,7 +749,7 @@ bitnet_status bitnet_residual_norm(const bitnet_residual* args, hipStream_t stre
   const bitnet_residual& r = *args;
   if (!valid_dtype(r.y_dtype) || !valid_dtype(r.h_dtype) || (r.u && !valid_dtype(r.u_dtype)))
     return BITNET_ERR_DTYPE;
-  if (r.M < 0 || r.M > kInt32Max || r.K < 1 || r.K > kInt32Max ||
+  if (r.M < 0 || r.M > bitnet::max_grid(1024) || r.K < 1 || r.K > kInt32Max ||
       (r.gate && r.gate_stride != 0 && r.gate_stride < r.K) || !finite(r.scale) ||
       !finite(r.eps) || r.eps < 0.0f)
     return BITNET_ERR_SHAPE;

@@ -85,7 +85,6 @@ hipError_t launch_attn_join(const KvCache& c, const KvBatch& b, const AttnArgs& 
                             const AttnPlan& p, float unit, bool out_bf16, const float* part,
                             hipStream_t s) {
   const int64_t grid = (int64_t)b.seqs * c.kv_heads * p.tiles * p.part_cols;
-  if (grid > 2147483647) return hipErrorInvalidValue;
   void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&p, (void*)&unit, (void*)&part};
   return hipLaunchKernel(out_bf16 ? (const void*)attn_join_kernel<true>
                                   : (const void*)attn_join_kernel<false>,
@@ -95,6 +94,13 @@ hipError_t launch_attn_join(const KvCache& c, const KvBatch& b, const AttnArgs& 
 size_t attention_workspace_bytes(const KvCache& c, const KvBatch& b, int q_heads) {
   return attn_workspace(c, b, many_rows(c, b, q_heads) ? attn_prompt_plan(c, b, q_heads)
                                                        : attn_decode_plan(c, b, q_heads));
+}
+
+bool attention_fits(const KvCache& c, const KvBatch& b, int q_heads) {
+  const AttnPlan p = many_rows(c, b, q_heads) ? attn_prompt_plan(c, b, q_heads)
+                                              : attn_decode_plan(c, b, q_heads);
+  const int64_t tiles = (int64_t)b.seqs * c.kv_heads * p.tiles;
+  return tiles * p.splits <= max_grid(512) && (p.splits == 1 || tiles * p.part_cols <= max_grid(kThreads));
 }
 
 hipError_t launch_attention(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool q_bf16,

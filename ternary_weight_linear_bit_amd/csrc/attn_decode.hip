@@ -405,7 +405,6 @@ hipError_t launch_attn_decode(const KvCache& c, const KvBatch& b, const AttnArgs
                               const AttnPlan& p, bool q_bf16, bool out_bf16, void* workspace,
                               hipStream_t s) {
   const int64_t grid = (int64_t)b.seqs * c.kv_heads * p.tiles * p.splits;
-  if (grid > 2147483647) return hipErrorInvalidValue;
   float* part = static_cast<float*>(workspace);
   const void* kern = p.waves == kManyWaves ? pick_decode<kManyWaves>(c.head_dim, q_bf16, out_bf16)
                                            : pick_decode<kWaves>(c.head_dim, q_bf16, out_bf16);

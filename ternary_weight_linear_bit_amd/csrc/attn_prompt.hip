@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const float k = lane_of(dk_now, g);
-        there[g] = is_scale(k);
+        there[g] = (int)__float_as_uint(k) >= 0;   // by its sign bit
         hole = hole || !there[g];
         ck[g] = fmaxf(qscale * k, 1e-38f);   // above 0: unseen keys' -inf stays -inf
         lg[g] = lane_of(lv, g);
@@ -465,7 +465,6 @@ hipError_t launch_attn_prompt(const KvCache& c, const KvBatch& b, const AttnArgs
     p.splits = 1;
   }
   const int64_t grid = (int64_t)b.seqs * c.kv_heads * p.tiles * p.splits;
-  if (grid > 2147483647) return hipErrorInvalidValue;
   const void* kern = wide ? (out_bf16 ? (const void*)attn_prompt_kernel<128, 8, 1, 1, true, true>
                                       : (const void*)attn_prompt_kernel<128, 8, 1, 1, true, false>)
                      : dp == 64 ? pick_prompt<64>(q_bf16, out_bf16)

@@ -501,6 +501,9 @@ size_t lut_workspace_bytes(int64_t N, int64_t K);
 hipError_t launch_lut(const uint8_t* wp, const float* w_scale, const int8_t* xq,
                       const float* x_scale, int64_t M, int64_t N, int64_t K, void* y,
                       bool y_bf16, int32_t* acc_out, void* workspace, int cus, hipStream_t s);
+// Largest grid of workgroups of t threads: the runtime counts threads in 32 bits.
+constexpr int64_t max_grid(int threads) { return ((int64_t)1 << 32) / threads - 1; }
+
 // Paged 8-bit cache of one layer's keys and values (bitnet_kv_cache, validated).
 struct KvCache {
   int8_t* k;                 // [pages][kv_heads][page][head_dim]
@@ -544,6 +547,8 @@ struct KvRows {
   int rot;                   // rotated dims (0: none)
   int neighbours;            // pairs (2i, 2i + 1) instead of (i, i + rot / 2)
 };
+// Workgroups of the launch.
+int64_t kv_append_grid(const KvCache& c, const KvBatch& b, bool queries);
 hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const KvRows& r, bool bf16,
                             hipStream_t s);
 
@@ -557,6 +562,8 @@ struct AttnArgs {
   float scale;
 };
 size_t attention_workspace_bytes(const KvCache& c, const KvBatch& b, int q_heads);
+// Whether the launches' grids are within the runtime's limits.
+bool attention_fits(const KvCache& c, const KvBatch& b, int q_heads);
 hipError_t launch_attention(const KvCache& c, const KvBatch& b, const AttnArgs& a, bool q_bf16,
                             bool out_bf16, void* workspace, hipStream_t s);
 // Residual join (bitnet_residual, validated).

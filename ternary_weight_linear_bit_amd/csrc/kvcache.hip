@@ -361,14 +361,23 @@ const void* append_pick(bool bf16) {
 
 }  // namespace
 
+namespace {
+int pages_touched(const KvCache& c, const KvBatch& b) { return (b.max_new + c.page - 2) / c.page + 1; }
+int64_t page_workgroups(const KvCache& c, const KvBatch& b) {
+  return (int64_t)b.seqs * pages_touched(c, b) * c.kv_heads * 2;
+}
+}  // namespace
+
+// A row of queries a workgroup (four rows a thread's loop: 170 registers instead of 60, 77
+// instead of 57 us for 1759 fp32 tokens of 64 + 64 + 64 heads).
+int64_t kv_append_grid(const KvCache& c, const KvBatch& b, bool queries) {
+  return page_workgroups(c, b) + (queries ? (int64_t)b.seqs * b.max_new : 0);
+}
+
 hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const KvRows& r, bool bf16,
                             hipStream_t s) {
-  const int pages_per_seq = (b.max_new + c.page - 2) / c.page + 1;
-  const int64_t page_units = (int64_t)b.seqs * pages_per_seq * c.kv_heads * 2;
-  // a row of queries a workgroup (four rows a thread's loop: 170 registers instead of 60,
-  // 77 instead of 57 us for 1759 fp32 tokens of 64 + 64 + 64 heads)
-  const int64_t grid = page_units + (r.q ? (int64_t)b.seqs * b.max_new : 0);
-  if (grid > 2147483647) return hipErrorInvalidValue;
+  const int pages_per_seq = pages_touched(c, b);
+  const int64_t grid = kv_append_grid(c, b, r.q != nullptr);
   const auto a16 = [](const void* p, int64_t stride, size_t es) {
     return p == nullptr || (((uintptr_t)p & 15u) == 0 && (stride * es) % 16 == 0);
   };
@@ -376,7 +385,7 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const KvRows& r,
   // groups of 8: 16-byte aligned rows and angles, rotated dims in whole pairs of groups
   const bool vec = a16(r.k, r.k_stride, es) && a16(r.v, r.v_stride, es) && a16(r.q, r.q_stride, es) &&
                    r.rot % 16 == 0 && a16(r.cos, 0, 4) && a16(r.sin, 0, 4);
-  const int pu = (int)page_units;
+  const int pu = (int)page_workgroups(c, b);
   const int rows = b.max_new < c.page ? b.max_new : c.page;   // of one page
   const bool few = rows * (c.head_dim / 16) <= kKvThreads;
   const void* kern = !vec ? append_pick<1, 4>(bf16) : few ? append_pick<8, 1>(bf16) : append_pick<8, 2>(bf16);

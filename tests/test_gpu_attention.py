@@ -130,6 +130,7 @@ def test_sharp_and_flat_weights(dt):
     run(2, 8, 128, 64, [1, 1, 70], [700, 129, 200], dt, sharp=0.0)
     run(2, 8, 128, 64, [1, 1, 70], [700, 129, 200], dt, scale=-0.2)
     run(2, 8, 128, 64, [1, 1, 70], [700, 129, 200], dt, sharp=1e-20)
+    run(2, 8, 128, 64, [1, 1, 70], [700, 129, 200], dt, scale=0.0)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -180,6 +181,52 @@ def test_bounds_of_the_batch():
 def test_strided_queries():
     run(2, 4, 64, 16, [3, 1, 90], [40, 5, 100], strided=True)
     run(2, 4, 80, 16, [3, 1, 90], [40, 5, 100], dt="f32", strided=True)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [1, 3])
+def test_unaligned_queries(dt, shift):
+    """Query rows aligned to their elements only."""
+    q_start, kv_len, table, pages = seqs([2, 1, 90], [40, 5, 100], 16)
+    k, v, ks, vs = cache(pages, 2, 16, 80, 3)
+    c = N.KVCache(dev(k), dev(v), dev(ks), dev(vs))
+    q = dev(np.random.default_rng(0).standard_normal((93, 4, 80)).astype(F32)).to(TYPES[dt])
+    flat = torch.zeros(q.numel() + shift, dtype=q.dtype, device=DEV)
+    flat[shift:] = q.reshape(-1)
+    for most in (2, 90):      # both kernels (the rows past max_new are left alone)
+        b = N.KVBatch(dev(table), dev(q_start), dev(kv_len), most, table.shape[1] * 16)
+        outs = [torch.full((93, 4, 80), 7.0, dtype=q.dtype, device=DEV) for _ in range(2)]
+        N.bitnet_attention(c, b, q, out=outs[0])
+        N.bitnet_attention(c, b, flat[shift:].view(93, 4, 80), out=outs[1])
+        assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 128), (256, 32)])
+def test_captured_prompts(dim, page):
+    """Prompts and drafted tokens in a graph, replayed over other lengths and queries with
+    eager calls in between."""
+    q_start, kv_len, table, pages = seqs([70, 3], [90, 200], page, width=32)
+    k, v, ks, vs = cache(pages, 2, page, dim, 3)
+    c = N.KVCache(dev(k), dev(v), dev(ks), dev(vs))
+    qs, ln = dev(q_start), dev(kv_len)
+    b = N.KVBatch(dev(table), qs, ln, 70, 32 * page)
+    q = torch.zeros((73, 4, dim), dtype=torch.bfloat16, device=DEV)
+    few = N.KVBatch(dev(table), dev(np.array([0, 1, 2], np.int32)), ln, 1, 32 * page)
+    N.bitnet_attention(c, b, q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = N.bitnet_attention(c, b, q)
+        one = N.bitnet_attention(c, few, q[:2])
+    for n in range(4):
+        q.normal_()
+        ln.copy_(torch.tensor([90 - 7 * n, 200 - 31 * n], dtype=torch.int32))
+        qs.copy_(torch.tensor([0, 70 - 20 * n, 73 - 20 * n], dtype=torch.int32))
+        out.fill_(7.0)
+        g.replay()
+        want = torch.full_like(out, 7.0)
+        N.bitnet_attention(c, b, q, out=want)
+        assert torch.equal(out, want)
+        assert torch.equal(one, N.bitnet_attention(c, few, q[:2]))
 
 
 def test_shared_pages():

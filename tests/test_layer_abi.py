@@ -90,7 +90,7 @@ def attend(lib, c, b, q=A, q_dtype=0, q_stride=512, q_heads=4, scale=1.0, window
     (dict(q_heads=0), ESHAPE), (dict(q_stride=511), ESHAPE), (dict(window=-1), ESHAPE),
     (dict(scale=float("nan")), ESHAPE), (dict(scale=float("inf")), ESHAPE), (dict(q=None), ENULL),
     (dict(out=None), ENULL), (dict(q=A + 2), EALIGN), (dict(out=A + 2), EALIGN),
-    (dict(out_dtype=1, out=A + 1), EALIGN), (dict(lse=A + 2), EALIGN)])
+    (dict(out_dtype=1, out=A + 1), EALIGN), (dict(out=A + 8), EALIGN), (dict(lse=A + 2), EALIGN)])
 def test_attention_refusals(lib, bad, want):
     assert attend(lib, kv(), batch(), **bad) == want
 
@@ -109,6 +109,18 @@ def test_attention_workspace(lib):
         assert attend(lib, kv(), long, ws=None) == EWS
         assert attend(lib, kv(), long, ws_bytes=need - 1) == EWS
         assert attend(lib, kv(), long, ws=A + 4, ws_bytes=need) == EALIGN
+
+
+def test_launches_beyond_the_runtime(lib):
+    """Sizes whose grids the runtime cannot count are refused, not passed to it."""
+    c, r = kv(page=128), rows(positions=1 << 30)
+    big = batch(seqs=65535, width=1 << 20, tokens=1 << 30, max_new=1 << 20, max_len=1 << 27)
+    assert lib.bitnet_kv_append(ctypes.byref(c), ctypes.byref(big), ctypes.byref(r), None) == ESHAPE
+    assert attend(lib, c, big) == ESHAPE
+    assert lib.bitnet_attention_workspace_bytes(ctypes.byref(c), ctypes.byref(big), 4) == 0
+    wide = batch(seqs=1, tokens=1 << 30, max_new=1 << 30)
+    assert attend(lib, kv(kv_heads=1), wide, q_heads=64, q_stride=64 * 128) == ESHAPE
+    assert lib.bitnet_residual_norm(ctypes.byref(res(M=1 << 22)), None) == ESHAPE
 
 
 def test_nothing_to_do(lib):
