@@ -549,8 +549,8 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, const bitnet_kv_bat
  *   s_j = softmax_scale * (q . k_j),  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),
  *   lse = m + ln sum_j e^(s_j - m),  m = max_j s_j.
  * A row that sees no key gets zeros and lse = -inf.  Sums are fp32 or exact integers;
- * with fp32 in and out queries and weights are held to 22 bits or more, else to 11 or
- * more (a bf16 query exactly).  The same call gives the same bits; another max_len may
+ * queries are held to 22 bits or more, the weights e^(s - m) to 22 with fp32 in and out
+ * and to 11 or more otherwise; lse is summed from unrounded ones.  The same call gives the same bits; another max_len may
  * split the sums elsewhere.
  *   q        [tokens] rows of [q_heads][head_dim], q_stride elements apart (>= q_heads *
  *            head_dim), fp32 or bf16 (q_dtype), finite; query head h reads kv head

@@ -14,9 +14,10 @@
 // operand that is turned into 8-bit digits, a query row (once) and the weights of a
 // step (16 a lane).  A value x with |x| <= X is held as the integer
 // v = rne(x V / X), V = 127 * 256^(ND - 1), in ND signed base-256 digits, each with
-// its own product; the int32 sums are exact.  ND = 2 (bf16 in or out) holds the
-// queries to 2^-16 of their row's largest value and the weights to 2^-16 of the
-// row's largest, finer than bf16's 2^-9 of each; ND = 3 (fp32 in and out) to 2^-24.
+// its own product; the int32 sums are exact.  Queries take 3 digits (2^-24 of their row's
+// largest value; with two the logits of bf16 queries were 2^-16 off, and lse, an fp32
+// output, with them), weights ND = 2 (2^-16 of the row's largest, finer than bf16's 2^-9
+// of each), or 3 for fp32 in and out.
 // Converting the codes to 16-bit floats instead would take 320 vector instructions
 // a lane and step of 64 keys, the digits take about 60.
 //
@@ -38,6 +39,7 @@ namespace bitnet {
 namespace {
 
 constexpr int kWaves = 4, kManyWaves = 8, kStep = kAttnStep, kCols = 16;
+constexpr int kQd = 3;   // digits of a query
 
 // Fixed point of a digit count.
 template <int ND>
@@ -95,6 +97,7 @@ __device__ __forceinline__ float rows_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// NW: waves.  ND: digits of a weight.
 template <int DP, int NW, int ND, bool QB, bool OB>
 __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel(
     const KvCache c, const KvBatch b, const AttnArgs a, const AttnPlan plan,
@@ -127,7 +130,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
   const int from = a.window > 0 ? max(pos - a.window + 1, 0) : 0;   // visible: from .. pos
 
   // queries: digits of dims 64 kc + 16 g .. + 15 of the lane's column
-  v4i qd[ND][KC];
+  v4i qd[kQd][KC];
   float qscale;
   {
     float q[KC][16];
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
     amax = rows_max(amax);
     const float up = amax < 0x1p-64f ? 0x1p64f : 1.0f;   // keeps 1 / amax finite
     const float inv = amax > 0.0f ? 1.0f / (amax * up) : 0.0f;
-    qscale = amax / Digits<ND>::kTop * a.scale * 1.44269504088896340736f;
+    qscale = amax / Digits<kQd>::kTop * a.scale * 1.44269504088896340736f;
 #pragma unroll
     for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
@@ -151,10 +154,10 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
         float x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(__fmul_rn(q[kc][4 * w + j], up), inv);
-        uint32_t d[ND];
-        digits4<ND>(x, d);
+        uint32_t d[kQd];
+        digits4<kQd>(x, d);
 #pragma unroll
-        for (int n = 0; n < ND; ++n) qd[n][kc][w] = (int)d[n];
+        for (int n = 0; n < kQd; ++n) qd[n][kc][w] = (int)d[n];
       }
   }
 
@@ -220,9 +223,9 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
     float x[4][4];   // the products first, as numbers
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      v4i s[ND];
+      v4i s[kQd];
 #pragma unroll
-      for (int n = 0; n < ND; ++n) {
+      for (int n = 0; n < kQd; ++n) {
         s[n] = (v4i){0, 0, 0, 0};
 #pragma unroll
         for (int kc = 0; kc < KC; ++kc)
@@ -230,10 +233,10 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        int d[ND];
+        int d[kQd];
 #pragma unroll
-        for (int n = 0; n < ND; ++n) d[n] = s[n][i];
-        x[t][i] = joined<ND>(d);
+        for (int n = 0; n < kQd; ++n) d[n] = s[n][i];
+        x[t][i] = joined<kQd>(d);
       }
     }
     pid_k2 = page_of(step + 2 * NW, col >> 2);
@@ -366,7 +369,6 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
   }
 }
 
-// ND = 3 for fp32 in and out, else 2.
 template <int DP, int NW>
 const void* pick_decode(bool qb, bool ob) {
   return qb ? (ob ? (const void*)attn_decode_kernel<DP, NW, 2, true, true>

@@ -40,17 +40,18 @@ def tables(positions, rot):
 def attention_bounds(out, lse, absv, flat, top, reach, q, keys, exact_io):
     """How far the kernel's out and lse may be from the float64 ones, elementwise.
 
-    The queries enter the products with an error of at most 2^-b of the row's largest
-    |q| (b = 15.9: two 8-bit digits, 127 * 256 steps a side; fp32 in or out: 22), which
-    moves a logit by at most reach * max|q| * 2^-b.  Weights are kept to 2^-b of the
-    row's largest (w = p dv), or, for bf16, rounded to 11 bits each (2^-11 of sum w|v|).
-    Fp32 arithmetic: a logit within 2^-21 of the largest |s| (a few roundings), exp
-    within 2^-20, sums over `keys` keys within (keys / 16 + 32) 2^-24 of sum w|v|.  A
-    logit error e moves every weight by a factor within exp(2e) after the division.
-    bf16 outputs are rounded: 2^-8 of the value (half a step)."""
+    The queries enter the products with an error of at most 2^-22 of the row's largest
+    |q| (bf16 ones exactly, where they are not below 2^-14 of it), which moves a logit by
+    at most reach * max|q| * 2^-22.  Weights w = p dv are kept to 2^-b of the row's
+    largest (b = 15.9: two 8-bit digits, 127 * 256 steps; fp32 in and out: 22), or, for
+    bf16, rounded to 11 bits each (2^-11 of sum w|v|).  Fp32 arithmetic: a logit within
+    2^-21 of the largest |s| (a few roundings), exp within 2^-20, sums over `keys` keys
+    within (keys / 16 + 32) 2^-24 of sum w|v|.  A logit error e moves every weight by a
+    factor within exp(2e) after the division.  lse has the logits' errors and the sum's,
+    whatever the output's type.  bf16 outputs are rounded: 2^-8 of the value (half a step)."""
     b = 22.0 if exact_io else 15.9
     amax = np.abs(q).max(-1)
-    e = reach * amax * 2.0 ** -b + top * 2.0 ** -21 + 2.0 ** -20
+    e = reach * amax * 2.0 ** -22 + top * 2.0 ** -21 + 2.0 ** -20
     rel = np.expm1(2 * e) + (keys / 16 + 32) * 2.0 ** -24
     tol = rel[..., None] * absv + flat * 2.0 ** -b     # flat: summed over the visible keys
     if not exact_io:
@@ -58,5 +59,5 @@ def attention_bounds(out, lse, absv, flat, top, reach, q, keys, exact_io):
     else:
         tol = tol + 2.0 ** -24 * np.abs(out)
     tol_lse = np.where(np.isfinite(lse), e + (keys / 16 + 32) * 2.0 ** -24
-                       + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0)) + 2.0 ** -21, 0)
+                       + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0)), 0)
     return tol + 1e-30, tol_lse
