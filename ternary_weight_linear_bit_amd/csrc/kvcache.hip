@@ -34,25 +34,32 @@ constexpr int kKvThreads = 256;
 template <int W>
 using vec = float __attribute__((ext_vector_type(W)));
 
-// W consecutive elements from element i; W = 8: the address is 16-byte aligned.
+// W consecutive elements from element i, aligned to the element (the hardware takes
+// 16-byte loads at any element's alignment).
 template <bool BF16, int W>
 __device__ __forceinline__ vec<W> kv_load(const void* x, int64_t i) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   vec<W> v;
   if constexpr (W == 1) {
     v[0] = BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(x)[i])
                 : reinterpret_cast<const float*>(x)[i];
   } else if constexpr (BF16) {
-    const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + i);
-    const uint32_t d[4] = {a.x, a.y, a.z, a.w};
+    u32x4 d;
+    __builtin_memcpy(&d, reinterpret_cast<const uint16_t*>(x) + i, 16);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = __uint_as_float(d[j] << 16);
       v[2 * j + 1] = __uint_as_float(d[j] & 0xffff0000u);
     }
   } else {
-    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + i);
-    const float4 a = p[0], b = p[1];
-    v = (vec<8>){a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    u32x4 a, b;
+    __builtin_memcpy(&a, reinterpret_cast<const float*>(x) + i, 16);
+    __builtin_memcpy(&b, reinterpret_cast<const float*>(x) + i + 4, 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __uint_as_float(a[j]);
+      v[j + 4] = __uint_as_float(b[j]);
+    }
   }
   return v;
 }
@@ -177,8 +184,7 @@ __device__ __forceinline__ void store_row(void* out, int64_t i, vec<W> v) {
   }
 }
 
-// W: dims a group (8, or 1 where rows, angles or the number of rotated dims do not
-// allow 16-byte groups).  H: pairs that a thread keeps; a page with more reads its rows again.
+// W: dims a group (8, or 1 where the rotated dims are no whole pairs of groups).  H: pairs that a thread keeps; a page with more reads its rows again.
 template <bool BF16, int W, int H>
 __global__ __launch_bounds__(kKvThreads) void kv_append_kernel(const KvCache c, const KvBatch b,
                                                                const KvRows r, int pages_per_seq,
@@ -378,17 +384,11 @@ hipError_t launch_kv_append(const KvCache& c, const KvBatch& b, const KvRows& r,
                             hipStream_t s) {
   const int pages_per_seq = pages_touched(c, b);
   const int64_t grid = kv_append_grid(c, b, r.q != nullptr);
-  const auto a16 = [](const void* p, int64_t stride, size_t es) {
-    return p == nullptr || (((uintptr_t)p & 15u) == 0 && (stride * es) % 16 == 0);
-  };
-  const size_t es = bf16 ? 2 : 4;
-  // groups of 8: 16-byte aligned rows and angles, rotated dims in whole pairs of groups
-  const bool vec = a16(r.k, r.k_stride, es) && a16(r.v, r.v_stride, es) && a16(r.q, r.q_stride, es) &&
-                   r.rot % 16 == 0 && a16(r.cos, 0, 4) && a16(r.sin, 0, 4);
+  const bool groups = r.rot % 16 == 0;   // whole pairs of groups rotate
   const int pu = (int)page_workgroups(c, b);
   const int rows = b.max_new < c.page ? b.max_new : c.page;   // of one page
   const bool few = rows * (c.head_dim / 16) <= kKvThreads;
-  const void* kern = !vec ? append_pick<1, 4>(bf16) : few ? append_pick<8, 1>(bf16) : append_pick<8, 2>(bf16);
+  const void* kern = !groups ? append_pick<1, 4>(bf16) : few ? append_pick<8, 1>(bf16) : append_pick<8, 2>(bf16);
   void* args[] = {(void*)&c, (void*)&b, (void*)&r, (void*)&pages_per_seq, (void*)&pu};
   return hipLaunchKernel(kern, dim3((unsigned)grid), dim3(kKvThreads), args,
                          (size_t)c.page * c.head_dim, s);

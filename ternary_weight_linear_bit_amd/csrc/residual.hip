@@ -13,75 +13,73 @@
 // Bound by memory: y and h are read once, h' and the codes written once.  One
 // workgroup per token; each thread keeps its first H groups of 8 values in
 // registers from the first sum to the last store.  Rows beyond that read h' again
-// (never h, which h_out may replace).
+// (never h, which h_out may replace).  The K % 8 last values of a row go one to a
+// thread.  Groups are loaded and stored whole at any alignment (the hardware takes
+// 16-byte accesses at element alignment): rows of odd lengths have no other path.
 #include "bitnet_internal.h"
+
+#include <type_traits>
 
 namespace bitnet {
 namespace {
 
-template <bool BF16>
-__device__ __forceinline__ float rs_load1(const void* x, int64_t i) {
-  if (BF16) return bf16_bits_to_float(reinterpret_cast<const uint16_t*>(x)[i]);
-  return reinterpret_cast<const float*>(x)[i];
-}
-template <bool BF16>
-__device__ __forceinline__ void rs_store1(void* x, int64_t i, float v) {
-  if (BF16)
-    reinterpret_cast<uint16_t*>(x)[i] = float_to_bf16_rne(v);
-  else
-    reinterpret_cast<float*>(x)[i] = v;
-}
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// W consecutive elements (8 from a 16-byte aligned address, or 1).
+// W consecutive elements (8 or 1), aligned to the element.
 template <bool BF16, int W>
 __device__ __forceinline__ void rs_load(const void* x, int64_t i, float v[W]) {
-  if (W == 1) {
-    v[0] = rs_load1<BF16>(x, i);
-  } else if (BF16) {
-    const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x) + i);
-    const uint32_t d[4] = {a.x, a.y, a.z, a.w};
+  if constexpr (W == 1) {
+    v[0] = BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t*>(x)[i])
+                : reinterpret_cast<const float*>(x)[i];
+  } else if constexpr (BF16) {
+    u32x4 d;
+    __builtin_memcpy(&d, reinterpret_cast<const uint16_t*>(x) + i, 16);
 #pragma unroll
-    for (int j = 0; j < W / 2; ++j) {
+    for (int j = 0; j < 4; ++j) {
       v[2 * j] = __uint_as_float(d[j] << 16);
       v[2 * j + 1] = __uint_as_float(d[j] & 0xffff0000u);
     }
   } else {
+    u32x4 d[2];
+    __builtin_memcpy(&d[0], reinterpret_cast<const float*>(x) + i, 16);
+    __builtin_memcpy(&d[1], reinterpret_cast<const float*>(x) + i + 4, 16);
 #pragma unroll
-    for (int h = 0; h < W / 4; ++h) {
-      const float4 a = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(x) + i)[h];
-      v[4 * h] = a.x;
-      v[4 * h + 1] = a.y;
-      v[4 * h + 2] = a.z;
-      v[4 * h + 3] = a.w;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(d[j / 4][j % 4]);
   }
 }
 // Rounds v to the type, stores it, and leaves the stored values in v.
 template <bool BF16, int W>
 __device__ __forceinline__ void rs_store(void* x, int64_t i, float v[W]) {
-  if (W == 1) {
-    rs_store1<BF16>(x, i, v[0]);
-    if (BF16) v[0] = bf16_bits_to_float(float_to_bf16_rne(v[0]));
-  } else if (BF16) {
-    uint32_t w[W / 2 + 1];
-#pragma unroll
-    for (int j = 0; j < W / 2; ++j) {
-      w[j] = bf16x2_rne(v[2 * j], v[2 * j + 1]);
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  if constexpr (W == 1) {
+    if (BF16) {
+      const uint16_t r = float_to_bf16_rne(v[0]);
+      reinterpret_cast<uint16_t*>(x)[i] = r;
+      v[0] = bf16_bits_to_float(r);
+    } else {
+      reinterpret_cast<float*>(x)[i] = v[0];
     }
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(x) + i) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(x) + i);
+  } else if constexpr (BF16) {
+    u32x4 d;
 #pragma unroll
-    for (int h = 0; h < W / 4; ++h)
-      p[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+    for (int j = 0; j < 4; ++j) {
+      d[j] = bf16x2_rne(v[2 * j], v[2 * j + 1]);
+      v[2 * j] = __uint_as_float(d[j] << 16);
+      v[2 * j + 1] = __uint_as_float(d[j] & 0xffff0000u);
+    }
+    __builtin_memcpy(reinterpret_cast<uint16_t*>(x) + i, &d, 16);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 d = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                       __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])};
+      __builtin_memcpy(reinterpret_cast<float*>(x) + i + 4 * h, &d, 16);
+    }
   }
 }
 
-// YB / HB: bf16 y (and gate), bf16 stream.  W: elements a group (8 or 1).  NT
-// threads, H groups held by each.
-template <bool YB, bool HB, int W, int NT, int H>
+// YB / HB: bf16 y (and gate), bf16 stream.  NT threads, H groups of 8 held by each.
+template <bool YB, bool HB, int NT, int H>
 __global__ __launch_bounds__(NT) void residual_kernel(const ResidualArgs p, int u_bf16) {
   constexpr int NW = NT / 64;
   __shared__ float wmax[NW];
@@ -89,9 +87,13 @@ __global__ __launch_bounds__(NT) void residual_kernel(const ResidualArgs p, int 
   __shared__ unsigned long long limbs[kSqLimbs];
   __shared__ uint32_t sqwork[kSqWork];
   __shared__ float sh_ms;
+  using Eight = std::integral_constant<int, 8>;
+  using One = std::integral_constant<int, 1>;
   const int64_t m = blockIdx.x, K = p.K, at = m * K;
-  const int64_t n = K / W;   // groups of the row (K is a multiple of W)
+  const int64_t n = K / 8;   // groups of the row
   const int tid = threadIdx.x;
+  const int64_t last = n * 8 + tid;   // the thread's value behind them
+  const bool one = last < K;
 
   // r of the values that each(f) visits; every thread calls it
   auto norm_factor = [&](double ss, auto each) -> float {
@@ -115,14 +117,18 @@ __global__ __launch_bounds__(NT) void residual_kernel(const ResidualArgs p, int 
     return rms_factor_of_mean(ms, p.eps);
   };
 
-  float y[H][W], v[H][W];
+  float y[H][8], v[H][8], y1[1], v1[1];
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int64_t g = tid + (int64_t)h * NT;
     if (g < n) {
-      rs_load<YB, W>(p.y, at + g * W, y[h]);
-      rs_load<HB, W>(p.h, at + g * W, v[h]);
+      rs_load<YB, 8>(p.y, at + g * 8, y[h]);
+      rs_load<HB, 8>(p.h, at + g * 8, v[h]);
     }
+  }
+  if (one) {
+    rs_load<YB, 1>(p.y, at + last, y1);
+    rs_load<HB, 1>(p.h, at + last, v1);
   }
   float r1 = 1.0f;
   if (p.post) {
@@ -132,23 +138,25 @@ __global__ __launch_bounds__(NT) void residual_kernel(const ResidualArgs p, int 
       for (int h = 0; h < H; ++h)
         if (tid + (int64_t)h * NT < n)
 #pragma unroll
-          for (int j = 0; j < W; ++j) f(y[h][j]);
+          for (int j = 0; j < 8; ++j) f(y[h][j]);
       for (int64_t g = tid + (int64_t)H * NT; g < n; g += NT) {
-        float a[W];
-        rs_load<YB, W>(p.y, at + g * W, a);
+        float a[8];
+        rs_load<YB, 8>(p.y, at + g * 8, a);
 #pragma unroll
-        for (int j = 0; j < W; ++j) f(a[j]);
+        for (int j = 0; j < 8; ++j) f(a[j]);
       }
+      if (one) f(y1[0]);
     };
     each_y([&](float a) { ss += (double)a * (double)a; });
     r1 = norm_factor(ss, each_y);
   }
 
-  // h' of group g from its y and h, stored; the stored values stay in x
-  auto join = [&](int64_t g, const float* yy, float* x) {
+  // h' of the W values from element k on, from their y and h; the stored values stay in x
+  auto join = [&](auto w8, int64_t k, const float* yy, float* x) {
+    constexpr int W = decltype(w8)::value;
     float w[W], gt[W];
-    if (p.post) rs_load<false, W>(p.post, g * W, w);
-    if (p.gate) rs_load<YB, W>(p.gate, m * p.gate_stride + g * W, gt);
+    if (p.post) rs_load<false, W>(p.post, k, w);
+    if (p.gate) rs_load<YB, W>(p.gate, m * p.gate_stride + k, gt);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       float z = yy[j];
@@ -156,73 +164,73 @@ __global__ __launch_bounds__(NT) void residual_kernel(const ResidualArgs p, int 
       if (p.gate) z = __fmul_rn(z, gt[j]);
       x[j] = __fadd_rn(x[j], __fmul_rn(z, p.scale));
     }
-    rs_store<HB, W>(p.h_out, at + g * W, x);
+    rs_store<HB, W>(p.h_out, at + k, x);
   };
   double ss = 0.0;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int64_t g = tid + (int64_t)h * NT;
     if (g < n) {
-      join(g, y[h], v[h]);
+      join(Eight{}, g * 8, y[h], v[h]);
 #pragma unroll
-      for (int j = 0; j < W; ++j) ss += (double)v[h][j] * (double)v[h][j];
+      for (int j = 0; j < 8; ++j) ss += (double)v[h][j] * (double)v[h][j];
     }
   }
   for (int64_t g = tid + (int64_t)H * NT; g < n; g += NT) {
-    float a[W], x[W];
-    rs_load<YB, W>(p.y, at + g * W, a);
-    rs_load<HB, W>(p.h, at + g * W, x);
-    join(g, a, x);
+    float a[8], x[8];
+    rs_load<YB, 8>(p.y, at + g * 8, a);
+    rs_load<HB, 8>(p.h, at + g * 8, x);
+    join(Eight{}, g * 8, a, x);
 #pragma unroll
-    for (int j = 0; j < W; ++j) ss += (double)x[j] * (double)x[j];
+    for (int j = 0; j < 8; ++j) ss += (double)x[j] * (double)x[j];
+  }
+  if (one) {
+    join(One{}, last, y1, v1);
+    ss += (double)v1[0] * (double)v1[0];
   }
   if (!p.u && !p.xq) return;
 
-  // visits the thread's groups of h' (from registers, then from h_out: its own stores)
-  auto each_group = [&](auto f) {
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int64_t g = tid + (int64_t)h * NT;
-      if (g < n) f(g, v[h]);
-    }
-    for (int64_t g = tid + (int64_t)H * NT; g < n; g += NT) {
-      float x[W];
-      rs_load<HB, W>(p.h_out, at + g * W, x);
-      f(g, x);
-    }
-  };
   float r2 = 1.0f;
   if (p.pre)
-    r2 = norm_factor(ss, [&](auto f) {
-      each_group([&](int64_t, const float* x) {
+    r2 = norm_factor(ss, [&](auto f) {   // h' from registers, then from the thread's own stores
 #pragma unroll
-        for (int j = 0; j < W; ++j) f(x[j]);
-      });
+      for (int h = 0; h < H; ++h)
+        if (tid + (int64_t)h * NT < n)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f(v[h][j]);
+      for (int64_t g = tid + (int64_t)H * NT; g < n; g += NT) {
+        float x[8];
+        rs_load<HB, 8>(p.h_out, at + g * 8, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f(x[j]);
+      }
+      if (one) f(v1[0]);
     });
-  auto normed = [&](int64_t g, const float* x, float* u) {
-    float w[W];
-    if (p.pre) rs_load<false, W>(p.pre, g * W, w);
+  // u of W values of h'; returns their largest magnitude
+  auto normed = [&](auto w8, int64_t k, float* x) -> float {
+    constexpr int W = decltype(w8)::value;
+    float w[W], a = 0.0f;
+    if (p.pre) rs_load<false, W>(p.pre, k, w);
 #pragma unroll
-    for (int j = 0; j < W; ++j) u[j] = p.pre ? norm_value(x[j], r2, w[j]) : x[j];
+    for (int j = 0; j < W; ++j) {
+      if (p.pre) x[j] = norm_value(x[j], r2, w[j]);
+      a = fmaxf(a, fabsf(x[j]));
+    }
+    return a;
   };
-  // u of the held groups replaces h' in v
+  // u of the held values replaces h'
   float a = 0.0f;
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int64_t g = tid + (int64_t)h * NT;
-    if (g < n) {
-      normed(g, v[h], v[h]);
-#pragma unroll
-      for (int j = 0; j < W; ++j) a = fmaxf(a, fabsf(v[h][j]));
-    }
+    if (g < n) a = fmaxf(a, normed(Eight{}, g * 8, v[h]));
   }
   for (int64_t g = tid + (int64_t)H * NT; g < n; g += NT) {
-    float x[W];
-    rs_load<HB, W>(p.h_out, at + g * W, x);
-    normed(g, x, x);
-#pragma unroll
-    for (int j = 0; j < W; ++j) a = fmaxf(a, fabsf(x[j]));
+    float x[8];
+    rs_load<HB, 8>(p.h_out, at + g * 8, x);
+    a = fmaxf(a, normed(Eight{}, g * 8, x));
   }
+  if (one) a = fmaxf(a, normed(One{}, last, v1));
   float s = 0.0f;
   if (p.xq) {
     a = wave_max(a);
@@ -234,34 +242,35 @@ __global__ __launch_bounds__(NT) void residual_kernel(const ResidualArgs p, int 
     s = kQb / astar;
     if (tid == 0) p.xs[m] = astar / kQb;
   }
-  auto finish = [&](int64_t g, float* u) {
+  auto finish = [&](auto w8, int64_t k, float* u) {
+    constexpr int W = decltype(w8)::value;
     if (p.xq) {
-      if (W == 1) {
-        const float q = rintf(__fmul_rn(u[0], s));
-        p.xq[at + g] = (int8_t)(int)fminf(fmaxf(q, -128.0f), 127.0f);
+      if constexpr (W == 1) {
+        p.xq[at + k] = (int8_t)(uint8_t)rne_bits(u[0], s);
       } else {
-        *reinterpret_cast<uint2*>(p.xq + at + g * W) =
-            make_uint2(quant4(u, s), quant4(u + 4 % W, s));
+        const u32x2 q = {quant4(u, s), quant4(u + 4, s)};
+        __builtin_memcpy(p.xq + at + k, &q, 8);
       }
     }
     if (p.u) {
       if (u_bf16)
-        rs_store<true, W>(p.u, at + g * W, u);
+        rs_store<true, W>(p.u, at + k, u);
       else
-        rs_store<false, W>(p.u, at + g * W, u);
+        rs_store<false, W>(p.u, at + k, u);
     }
   };
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int64_t g = tid + (int64_t)h * NT;
-    if (g < n) finish(g, v[h]);
+    if (g < n) finish(Eight{}, g * 8, v[h]);
   }
   for (int64_t g = tid + (int64_t)H * NT; g < n; g += NT) {
-    float x[W];
-    rs_load<HB, W>(p.h_out, at + g * W, x);
-    normed(g, x, x);
-    finish(g, x);
+    float x[8];
+    rs_load<HB, 8>(p.h_out, at + g * 8, x);
+    normed(Eight{}, g * 8, x);
+    finish(Eight{}, g * 8, x);
   }
+  if (one) finish(One{}, last, v1);
 }
 
 // Threads of a workgroup.  Rows of up to 4096 fit one or two groups a thread; one each
@@ -271,44 +280,36 @@ __global__ __launch_bounds__(NT) void residual_kernel(const ResidualArgs p, int 
 // but sixteen waves leave a compute unit one workgroup, so that many tokens rather read
 // part of h' again (2048 x 10240, bf16: 59.6 with 1024 threads, 47.6 with 512).
 template <bool YB, bool HB>
-const void* residual_pick(bool vec, int64_t K, int64_t M, int* threads) {
-  if (!vec) {
-    *threads = 256;
-    return (const void*)residual_kernel<YB, HB, 1, 256, 8>;
-  }
+const void* residual_pick(int64_t K, int64_t M, int* threads) {
   if (K <= 1024) {
     *threads = 128;
-    return (const void*)residual_kernel<YB, HB, 8, 128, 1>;
+    return (const void*)residual_kernel<YB, HB, 128, 1>;
   }
   if (K <= 4096 && M > 64) {
     *threads = 256;
-    return (const void*)residual_kernel<YB, HB, 8, 256, 2>;
+    return (const void*)residual_kernel<YB, HB, 256, 2>;
   }
   if (K <= 4096) {
     *threads = 512;
-    return (const void*)residual_kernel<YB, HB, 8, 512, 1>;
+    return (const void*)residual_kernel<YB, HB, 512, 1>;
   }
   if (K <= 8192 || M > 256) {
     *threads = 512;
-    return (const void*)residual_kernel<YB, HB, 8, 512, 2>;
+    return (const void*)residual_kernel<YB, HB, 512, 2>;
   }
   *threads = 1024;
-  return (const void*)residual_kernel<YB, HB, 8, 1024, 2>;
+  return (const void*)residual_kernel<YB, HB, 1024, 2>;
 }
 
 }  // namespace
 
 hipError_t launch_residual(const ResidualArgs& a, bool y_bf16, bool h_bf16, bool u_bf16, int64_t M,
                            hipStream_t s) {
-  const auto al = [](const void* p, uintptr_t b) { return ((uintptr_t)p & (b - 1)) == 0; };
-  const bool vec = a.K % 8 == 0 && al(a.y, 16) && al(a.h, 16) && al(a.gate, 16) && al(a.h_out, 16) &&
-                   al(a.u, 16) && al(a.post, 16) && al(a.pre, 16) && al(a.xq, 8) &&
-                   a.gate_stride % 8 == 0;
   int threads;
-  const void* kern = y_bf16 ? (h_bf16 ? residual_pick<true, true>(vec, a.K, M, &threads)
-                                      : residual_pick<true, false>(vec, a.K, M, &threads))
-                            : (h_bf16 ? residual_pick<false, true>(vec, a.K, M, &threads)
-                                      : residual_pick<false, false>(vec, a.K, M, &threads));
+  const void* kern = y_bf16 ? (h_bf16 ? residual_pick<true, true>(a.K, M, &threads)
+                                      : residual_pick<true, false>(a.K, M, &threads))
+                            : (h_bf16 ? residual_pick<false, true>(a.K, M, &threads)
+                                      : residual_pick<false, false>(a.K, M, &threads));
   const int ub = u_bf16 ? 1 : 0;
   void* args[] = {(void*)&a, (void*)&ub};
   return hipLaunchKernel(kern, dim3((unsigned)M), dim3((unsigned)threads), args, 0, s);
