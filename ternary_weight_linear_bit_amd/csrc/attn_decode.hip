@@ -9,7 +9,10 @@
 // A row without keys gives zeros and lse = -inf; a page id outside the cache holds
 // no keys.
 //
-// Bound by memory: every visible code is read once.  The codes go from memory to
+// Bound by memory: every visible code is read once (64 sequences of 1 .. 8191 tokens, 32
+// heads on 8, 128 dims: 131 us, 4.5 TB/s; four of 65536, fp32: 110 us, 4.8 TB/s; a large
+// copy reaches 4.75).  Small calls are bound by one step's latency and two launches (one
+// sequence of 2049 tokens: 10.8 us).  Non-temporal loads were 7-10% slower.  The codes go from memory to
 // the int8 matrix cores as they are, with no conversion and no LDS: it is the other
 // operand that is turned into 8-bit digits, a query row (once) and the weights of a
 // step (16 a lane).  A value x with |x| <= X is held as the integer

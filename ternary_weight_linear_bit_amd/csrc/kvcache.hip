@@ -21,9 +21,10 @@
 // groups of W dims that rotate into each other (so that queries can be rotated in
 // place); it stays in registers from the maximum to the codes.
 //
-// Prompts are bound by memory, single tokens by the chain of dependent loads (row
-// numbers and length; page id, row, angles; scale and earlier codes): each link's
-// loads are issued together.
+// Prompts are bound by memory (4096 bf16 tokens of 20 + 5 + 5 heads: 13.4 us, 4.5 TB/s;
+// 1759 fp32 tokens of 64 + 64 + 64 heads in seven sequences: 54.6 us, 3.7 TB/s), single
+// tokens by the chain of dependent loads (row numbers and length; page id, row, angles;
+// scale and earlier codes; 3.7 us in a graph): each link's loads are issued together.
 #include "bitnet_internal.h"
 
 namespace bitnet {

@@ -10,7 +10,9 @@
 // (the same functions as the activation prologue's norm), so every result is
 // independent of the order of the sums.
 //
-// Bound by memory: y and h are read once, h' and the codes written once.  One
+// Bound by memory: y and h are read once, h' and the codes written once (4093 x 4096,
+// bf16 block, fp32 stream, both norms: 41-43 us, 4.3-4.5 TB/s; one token of 2560: 3.7 us
+// in a graph, the chain of two sums and a maximum).  One
 // workgroup per token; each thread keeps its first H groups of 8 values in
 // registers from the first sum to the last store.  Rows beyond that read h' again
 // (never h, which h_out may replace).  The K % 8 last values of a row go one to a
