@@ -6,7 +6,7 @@ stack, one token (M = 1) streamed through 96 layers of {q, k, v, o: 8192->8192,
 gate, up: 8192->28672, down: 28672->8192} with fp32 activations between layers
 and the per-token int8 activation quantisation fused into every layer (23.35 GB
 of packed weights per token, resident in HBM).  Chain per layer: q, k, v from
-the layer input (one launch); o from q (attention is out of scope); gate and up
+the layer input (one launch); o from q (the linear layers alone); gate and up
 from o (one launch); down from up; down is the next layer's input: 4 launches per
 layer, 384 per token, replayed from a HIP graph.  Weights are synthetic
 N(0, 0.02^2), seeded, ternarised on the GPU by the library.
@@ -124,8 +124,8 @@ def build_stack(torch, N, I, layer_shapes, layers, replicas, fmt="2bit"):
 
 def chain_fn(torch, N, layers_mats, h0, bufs, norms=None, eps=1e-5, fmt="2bit"):
     """Enqueue one step (M tokens) through every layer; returns the number of
-    launches.  Plain chain: q, k, v from the layer input; o from q (attention is
-    out of scope); gate and up from o; down from up.  Full layer (``norms``): an
+    launches.  Plain chain: q, k, v from the layer input; o from q (the linear
+    layers alone); gate and up from o; down from up.  Full layer (``norms``): an
     RMS norm in front of q/k/v and of gate/up, the sub-layer norm in front of o
     and of down, and down consumes ReLU(gate)^2 * up (the layer's neighbours as
     the BitNet b1.58 2B4T architecture names them), all fused into the launches."""

@@ -2,6 +2,7 @@
 // Every check runs before the first HIP call, so a rejected call enqueues nothing.
 #include "bitnet_mi355x.h"
 #include "bitnet_internal.h"
+#include "layer_internal.h"
 
 #include <string.h>
 

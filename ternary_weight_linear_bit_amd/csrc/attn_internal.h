@@ -2,7 +2,7 @@
 // splits the keys of a sequence over workgroups.
 #pragma once
 
-#include "bitnet_internal.h"
+#include "layer_internal.h"
 
 namespace bitnet {
 

@@ -22,10 +22,10 @@
 // place); it stays in registers from the maximum to the codes.
 //
 // Prompts are bound by memory (4096 bf16 tokens of 20 + 5 + 5 heads: 13.4 us, 4.5 TB/s;
-// 1759 fp32 tokens of 64 + 64 + 64 heads in seven sequences: 54.6 us, 3.7 TB/s), single
+// 1374 fp32 tokens of 64 + 64 + 64 heads in seven sequences: 54.6 us, 3.7 TB/s), single
 // tokens by the chain of dependent loads (row numbers and length; page id, row, angles;
 // scale and earlier codes; 3.7 us in a graph): each link's loads are issued together.
-#include "bitnet_internal.h"
+#include "layer_internal.h"
 
 namespace bitnet {
 namespace {
@@ -376,7 +376,7 @@ int64_t page_workgroups(const KvCache& c, const KvBatch& b) {
 }  // namespace
 
 // A row of queries a workgroup (four rows a thread's loop: 170 registers instead of 60, 77
-// instead of 57 us for 1759 fp32 tokens of 64 + 64 + 64 heads).
+// instead of 57 us for 1374 fp32 tokens of 64 + 64 + 64 heads).
 int64_t kv_append_grid(const KvCache& c, const KvBatch& b, bool queries) {
   return page_workgroups(c, b) + (queries ? (int64_t)b.seqs * b.max_new : 0);
 }

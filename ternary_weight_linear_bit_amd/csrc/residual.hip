@@ -18,7 +18,7 @@
 // (never h, which h_out may replace).  The K % 8 last values of a row go one to a
 // thread.  Groups are loaded and stored whole at any alignment (the hardware takes
 // 16-byte accesses at element alignment): rows of odd lengths have no other path.
-#include "bitnet_internal.h"
+#include "layer_internal.h"
 
 #include <type_traits>
 
