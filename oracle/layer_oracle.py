@@ -145,28 +145,34 @@ def attention(k, v, k_scale, v_scale, table, q_start, kv_len, q, scale, window=0
     for b, (s0, n, first, ln) in enumerate(spans(q_start, kv_len, T, max_new, max_len)):
         for h in range(heads):
             kc, vc, dk, dv, ok = gather(k, v, k_scale, v_scale, table[b], h, ln)
-            for i in range(min(n, max_new)):
-                pos = first + i
-                lo = max(0, pos - window + 1) if window else 0
-                at = np.arange(lo, pos + 1)
-                at = at[ok[at]] if len(at) else at
-                for g in range(h * group, (h + 1) * group):
-                    t = s0 + i
-                    if len(at) == 0:
-                        out[t, g], lse[t, g] = 0.0, -np.inf
-                        continue
-                    s = scale * dk[at] * (kc[at] @ q[t, g].astype(np.float64))
-                    m = s.max()
-                    p = np.exp(s - m)
-                    total = p.sum()
-                    w = p * dv[at]
-                    out[t, g] = (w @ vc[at]) / total
-                    lse[t, g] = m + np.log(total)
-                    if detail:
-                        absv[t, g] = (w @ np.abs(vc[at])) / total
-                        flat[t, g] = w.max() * np.abs(vc[at]).sum(0) / total
-                        top[t, g] = np.abs(s).max()
-                        reach[t, g] = (abs(scale) * dk[at] * np.abs(kc[at]).sum(1)).max()
+            rows = min(n, max_new)
+            if rows == 0:
+                continue
+            pos = first + np.arange(rows)[:, None]
+            j = np.arange(ln)[None, :]
+            seen = ok[None, :] & (j <= pos)
+            if window:
+                seen &= j > pos - window
+            some = seen.any(1)
+            t = slice(s0, s0 + rows)
+            for g in range(h * group, (h + 1) * group):
+                out[t, g], lse[t, g] = 0.0, -np.inf
+                if not some.any():
+                    continue
+                with np.errstate(invalid="ignore", over="ignore"):   # scales of pages nobody sees
+                    s = scale * dk * (q[t, g].astype(np.float64) @ kc.T)
+                s = np.where(seen, s, -np.inf)
+                m = np.where(some, s.max(1), 0.0)[:, None]
+                w = np.exp(s - m)
+                total = np.where(some, w.sum(1), 1.0)[:, None]
+                lse[t, g] = np.where(some, (m + np.log(total))[:, 0], -np.inf)
+                w = np.where(seen, w * np.where(seen.any(0), dv, 0.0), 0.0)
+                out[t, g] = (w @ vc) / total
+                if detail:
+                    absv[t, g] = (w @ np.abs(vc)) / total
+                    flat[t, g] = w.max(1)[:, None] * (seen @ np.abs(vc)) / total
+                    top[t, g] = np.where(seen, np.abs(s), 0.0).max(1)
+                    reach[t, g] = np.where(seen, abs(scale) * dk * np.abs(kc).sum(1), 0.0).max(1)
     return (out, lse, absv, flat, top, reach) if detail else (out, lse)
 
 

@@ -96,14 +96,18 @@ int join_cols(const KvCache& c, const AttnPlan& p, int ways) {
   return p.cols > 16 && at_once < 16 ? 16 : at_once;
 }
 
-// Columns (rows x query heads of a kv head) from which the prompt kernel is taken.  32
-// sequences of 1000 tokens, 8 kv heads: 32 columns 25.6 us with the decode kernel, 31.1
-// with this one; 48 columns 36.6 and 32.0; 64 columns 43.8 and 31.9.  Few sequences and
-// heads do not fill the chip with its workgroups: one of 4096 tokens takes 15.8 and 23.5
-// us with 64 columns, 26.0 and 30.3 with 256.
+// Whether a call takes the prompt kernel.  cols: rows x query heads of a kv head.  Its
+// workgroups of 128 columns have to fill half of the chip (us, decode and prompt kernel, 32
+// heads on 8, bf16: one prompt of 256 tokens 10.4 and 15.2, of 512 23.9 and 21.2, of 1024
+// 50.8 and 48.2; 256 rows behind 3840 tokens 52 and 63, 512 behind 3584 94 and 68).  From 48
+// columns on it is also taken where the cache passes the L2s, since the decode kernel reads
+// it for every 16 columns (8 sequences of 4096 tokens, 12 rows each: 47 and 36; 64 heads
+// of their own, 64 rows behind 4032: 52 and 39).
 bool many_rows(const KvCache& c, const KvBatch& b, int q_heads) {
+  const int64_t pairs = (int64_t)b.seqs * c.kv_heads;
   const int64_t cols = (int64_t)b.max_new * (q_heads / c.kv_heads);
-  return cols >= ((int64_t)b.seqs * c.kv_heads >= 32 ? 48 : 512);
+  return pairs * cols >= 128 * 128 ||
+         (cols >= 48 && pairs * b.max_len >= (int64_t)(64 << 20) / (2 * c.head_dim));
 }
 
 }  // namespace

@@ -80,7 +80,7 @@ __device__ __forceinline__ void digits4(const float x[4], uint32_t out[ND]) {
 // The number that ND int32 digit sums stand for.
 template <int ND>
 __device__ __forceinline__ float joined(const int d[ND]) {
-  const float t = (float)((d[0] << 8) + d[1]);   // |digit sum| < 2^22: exact in int32
+  const float t = (float)(d[0] * 256 + d[1]);   // |digit sum| < 2^22: exact in int32
   return ND == 2 ? t : __builtin_fmaf(t, 256.0f, (float)d[ND - 1]);
 }
 

@@ -102,6 +102,20 @@ def test_prompts(heads, q_heads, dim, page, dt):
     run(heads, q_heads, dim, page, [200, 1, 65, 129, 0, 64], [200, 77, 65, 300, 5, 191], dt, seed=page + dim)
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("dt,out_dt", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("dim,window", [(64, 0), (80, 100), (128, 0), (256, 70), (48, 1)])
+def test_many_rows(dim, page, dt, out_dt, window):
+    """Prompts of the size that the prompt kernel takes, rows without keys and missing pages
+    among them."""
+    def edit(table, q_start, kv_len, ks, vs):
+        table[1, 1] = -1
+        kv_len[3] = 30                                   # 40 rows of 30 tokens
+    run(16, 32, dim, page, [257, 65, 1, 40, 130], [300, 200, 250, 40, 130], dt, out_dt, window=window,
+        seed=dim, edit=edit)
+    run(8, 24, dim, page, [257, 1, 90], [700, 650, 400], dt, out_dt, window=window, seed=dim + 1)
+
+
 @pytest.mark.parametrize("dim", [128, 80])
 @pytest.mark.parametrize("page,out_dt", [(16, "bf16"), (128, "f32")])
 def test_wide_prompts(dim, page, out_dt):
@@ -123,64 +137,76 @@ def test_mixed_types(dt, out_dt):
     run(2, 8, 128, 64, [1, 90, 4], [500, 130, 20], dt, out_dt)
 
 
+# few heads: the decode kernel; many: the prompt kernel
+BOTH = pytest.mark.parametrize("heads,q_heads", [(2, 4), (96, 192)])
+
+
+@BOTH
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_sharp_and_flat_weights(dt):
+def test_sharp_and_flat_weights(dt, heads, q_heads):
     """Logits far apart (one key takes all), equal ones, and a negative scale."""
-    run(2, 8, 128, 64, [1, 1, 70], [700, 129, 200], dt, sharp=30.0)
-    run(2, 8, 128, 64, [1, 1, 70], [700, 129, 200], dt, sharp=0.0)
-    run(2, 8, 128, 64, [1, 1, 70], [700, 129, 200], dt, scale=-0.2)
-    run(2, 8, 128, 64, [1, 1, 70], [700, 129, 200], dt, sharp=1e-20)
-    run(2, 8, 128, 64, [1, 1, 70], [700, 129, 200], dt, scale=0.0)
+    run(heads, q_heads, 128, 64, [1, 1, 70], [300, 129, 200], dt, sharp=30.0)
+    run(heads, q_heads, 128, 64, [1, 1, 70], [300, 129, 200], dt, sharp=0.0)
+    run(heads, q_heads, 128, 64, [1, 1, 70], [300, 129, 200], dt, scale=-0.2)
+    run(heads, q_heads, 128, 64, [1, 1, 70], [300, 129, 200], dt, sharp=1e-20)
+    run(heads, q_heads, 128, 64, [1, 1, 70], [300, 129, 200], dt, scale=0.0)
 
 
+@BOTH
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_large_queries(dt):
+def test_large_queries(dt, heads, q_heads):
     """Queries near the type's end do not overflow on the way (their logits stay finite)."""
-    run(1, 2, 64, 16, [1, 40], [90, 77], dt, sharp=1e30, scale=1e-31)
+    run(heads, q_heads, 64, 16, [1, 60], [90, 77], dt, sharp=1e30, scale=1e-31)
 
 
+@BOTH
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_page_scales_far_apart(dt):
+def test_page_scales_far_apart(dt, heads, q_heads):
     """Pages whose scales differ by many orders: a tiny one beside a large one."""
     def edit(table, q_start, kv_len, ks, vs):
         rng = np.random.default_rng(1)
         vs *= np.exp(rng.normal(0, 6, vs.shape)).astype(F32)
         ks *= np.exp(rng.normal(0, 1, ks.shape)).astype(F32)
-    run(2, 4, 64, 16, [1, 3, 100], [300, 50, 150], dt, edit=edit)
+    run(heads, q_heads, 64, 16, [1, 3, 100], [300, 50, 150], dt, edit=edit)
 
 
+@BOTH
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_rows_without_keys(dt):
+def test_rows_without_keys(dt, heads, q_heads):
     """More rows than tokens, no tokens at all, and rows behind the batch."""
-    run(2, 4, 64, 16, [5, 1, 80, 3], [3, 0, 20, 3], dt, tail=6)
+    run(heads, q_heads, 64, 16, [5, 1, 80, 3], [3, 0, 20, 3], dt, tail=6)
 
 
+@BOTH
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_bad_pages_are_not_seen(dt):
+def test_bad_pages_are_not_seen(dt, heads, q_heads):
     def edit(table, q_start, kv_len, ks, vs):
         table[0, 1], table[0, 3] = -1, 1 << 30
         table[1, 0] = 10 ** 9                            # a sequence whose only page is missing
         table[2, :2] = -7
-    run(2, 4, 64, 16, [1, 1, 90, 3], [100, 9, 120, 40], dt, edit=edit)
-    run(2, 4, 64, 64, [1, 1, 90, 3], [300, 9, 190, 40], dt, edit=edit)
+    run(heads, q_heads, 64, 16, [1, 1, 90, 3], [100, 9, 120, 40], dt, edit=edit)
+    run(heads, q_heads, 64, 64, [1, 1, 90, 3], [300, 9, 190, 40], dt, edit=edit)
 
 
-def test_bad_rows_and_lengths():
+@BOTH
+def test_bad_rows_and_lengths(heads, q_heads):
     def edit(table, q_start, kv_len, ks, vs):
         q_start[:] = [-4, 30, 1 << 30, 20]
         kv_len[:] = [40, -5, 1 << 30]
-    run(2, 4, 64, 16, [30, 1, 16], [40, 5, 16], edit=edit, max_new=30)
+    run(heads, q_heads, 64, 16, [30, 1, 16], [40, 5, 16], edit=edit, max_new=30)
 
 
-def test_bounds_of_the_batch():
+@BOTH
+def test_bounds_of_the_batch(heads, q_heads):
     """Rows past max_new are left alone, tokens past max_len are not there."""
-    run(2, 4, 64, 16, [30, 1, 16], [40, 5, 16], max_new=9)
-    run(2, 4, 64, 16, [3, 1, 16], [40, 5, 16], max_len=20)
+    run(heads, q_heads, 64, 16, [50, 1, 16], [60, 5, 16], max_new=29)
+    run(heads, q_heads, 64, 16, [3, 1, 36], [40, 5, 36], max_len=30)
 
 
-def test_strided_queries():
-    run(2, 4, 64, 16, [3, 1, 90], [40, 5, 100], strided=True)
-    run(2, 4, 80, 16, [3, 1, 90], [40, 5, 100], dt="f32", strided=True)
+@BOTH
+def test_strided_queries(heads, q_heads):
+    run(heads, q_heads, 64, 16, [3, 1, 90], [40, 5, 100], strided=True)
+    run(heads, q_heads, 80, 16, [3, 1, 90], [40, 5, 100], dt="f32", strided=True)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -188,16 +214,16 @@ def test_strided_queries():
 def test_unaligned_queries(dt, shift):
     """Query rows aligned to their elements only."""
     q_start, kv_len, table, pages = seqs([2, 1, 90], [40, 5, 100], 16)
-    k, v, ks, vs = cache(pages, 2, 16, 80, 3)
+    k, v, ks, vs = cache(pages, 16, 16, 80, 3)
     c = N.KVCache(dev(k), dev(v), dev(ks), dev(vs))
-    q = dev(np.random.default_rng(0).standard_normal((93, 4, 80)).astype(F32)).to(TYPES[dt])
+    q = dev(np.random.default_rng(0).standard_normal((93, 64, 80)).astype(F32)).to(TYPES[dt])
     flat = torch.zeros(q.numel() + shift, dtype=q.dtype, device=DEV)
     flat[shift:] = q.reshape(-1)
     for most in (2, 90):      # both kernels (the rows past max_new are left alone)
         b = N.KVBatch(dev(table), dev(q_start), dev(kv_len), most, table.shape[1] * 16)
-        outs = [torch.full((93, 4, 80), 7.0, dtype=q.dtype, device=DEV) for _ in range(2)]
+        outs = [torch.full((93, 64, 80), 7.0, dtype=q.dtype, device=DEV) for _ in range(2)]
         N.bitnet_attention(c, b, q, out=outs[0])
-        N.bitnet_attention(c, b, flat[shift:].view(93, 4, 80), out=outs[1])
+        N.bitnet_attention(c, b, flat[shift:].view(93, 64, 80), out=outs[1])
         assert torch.equal(outs[0], outs[1])
 
 
@@ -206,11 +232,11 @@ def test_captured_prompts(dim, page):
     """Prompts and drafted tokens in a graph, replayed over other lengths and queries with
     eager calls in between."""
     q_start, kv_len, table, pages = seqs([70, 3], [90, 200], page, width=32)
-    k, v, ks, vs = cache(pages, 2, page, dim, 3)
+    k, v, ks, vs = cache(pages, 32, page, dim, 3)
     c = N.KVCache(dev(k), dev(v), dev(ks), dev(vs))
     qs, ln = dev(q_start), dev(kv_len)
     b = N.KVBatch(dev(table), qs, ln, 70, 32 * page)
-    q = torch.zeros((73, 4, dim), dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros((73, 128, dim), dtype=torch.bfloat16, device=DEV)
     few = N.KVBatch(dev(table), dev(np.array([0, 1, 2], np.int32)), ln, 1, 32 * page)
     N.bitnet_attention(c, b, q)
     g = torch.cuda.CUDAGraph()
@@ -229,11 +255,12 @@ def test_captured_prompts(dim, page):
         assert torch.equal(one, N.bitnet_attention(c, few, q[:2]))
 
 
-def test_shared_pages():
+@BOTH
+def test_shared_pages(heads, q_heads):
     """Two sequences on one prefix."""
     def edit(table, q_start, kv_len, ks, vs):
         table[1, :2] = table[0, :2]
-    run(2, 4, 64, 16, [1, 4, 1], [40, 60, 16], edit=edit)
+    run(heads, q_heads, 64, 16, [1, 44, 1], [40, 60, 16], edit=edit)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -267,10 +294,11 @@ def test_repeats_are_identical():
     k, v, ks, vs = cache(pages, 2, 16, 128, 3)
     c = N.KVCache(dev(k), dev(v), dev(ks), dev(vs))
     b = N.KVBatch(dev(table), dev(q_start), dev(kv_len), 70, 9008)
-    q = dev(np.random.default_rng(0).standard_normal((74, 8, 128)).astype(F32))
-    first = host(N.bitnet_attention(c, b, q))
-    for _ in range(3):
-        np.testing.assert_array_equal(host(N.bitnet_attention(c, b, q)), first)
+    for heads in (8, 96):                             # both kernels
+        q = dev(np.random.default_rng(0).standard_normal((74, heads, 128)).astype(F32))
+        first = host(N.bitnet_attention(c, b, q))
+        for _ in range(3):
+            np.testing.assert_array_equal(host(N.bitnet_attention(c, b, q)), first)
 
 
 def test_cache_beyond_4_gib():
@@ -285,11 +313,13 @@ def test_cache_beyond_4_gib():
     for name in ("k", "v", "k_scale", "v_scale"):
         getattr(big, name)[pages - 1] = getattr(small, name)[0]
         getattr(big, name)[7] = getattr(small, name)[1]
-    n, ln = dev(np.array([0, 1, 41], np.int32)), dev(np.array([200, 256], np.int32))
-    q = dev(np.random.default_rng(0).standard_normal((41, 16, dim)).astype(F32))
+    n, ln = dev(np.array([0, 1, 71], np.int32)), dev(np.array([200, 256], np.int32))
+    q = dev(np.random.default_rng(0).standard_normal((71, 128, dim)).astype(F32))
     t0, t1 = np.array([[0, 1], [0, 1]], np.int32), np.array([[pages - 1, 7]] * 2, np.int32)
-    want = host(N.bitnet_attention(small, N.KVBatch(dev(t0), n, ln, 40, 256), q))
-    got = host(N.bitnet_attention(big, N.KVBatch(dev(t1), n, ln, 40, 256), q))
-    np.testing.assert_array_equal(got, want)
+    for most in (70, 1):                              # both kernels
+        out = [torch.zeros_like(q) for _ in range(2)]
+        N.bitnet_attention(small, N.KVBatch(dev(t0), n, ln, most, 256), q, out=out[0])
+        N.bitnet_attention(big, N.KVBatch(dev(t1), n, ln, most, 256), q, out=out[1])
+        assert torch.equal(*out) and bool(out[0][0].any())
     del big
     torch.cuda.empty_cache()
