@@ -743,7 +743,17 @@ class _On:
             self._guard.__exit__(*exc)
 
 
-class KVCache:
+class _Fixed:
+    """Attributes are set once: the C struct is made from them, and an assignment after
+    that would change nothing."""
+
+    def __setattr__(self, name, value):
+        if name[0] != "_" and name in self.__dict__:
+            raise AttributeError(f"{name} is fixed: make a new {type(self).__name__}")
+        object.__setattr__(self, name, value)
+
+
+class KVCache(_Fixed):
     """Paged 8-bit cache of one layer: int8 k [pages, kv_heads, page, head_dim] and
     v [pages, kv_heads, head_dim, page], fp32 scales [pages, kv_heads].  Holds the
     tensors and the C struct; sizes are fixed, contents are the caller's."""
@@ -778,11 +788,12 @@ class KVCache:
                        torch.empty((pages, kv_heads), dtype=torch.float32, device=device))
 
 
-class KVBatch:
+class KVBatch(_Fixed):
     """Ragged batch over a paged cache: int32 table [seqs, width] of page ids, q_start
     [seqs + 1] (rows of each sequence's new tokens), kv_len [seqs] (cached tokens with
     the new ones).  max_new and max_len bound what q_start and kv_len say; the arrays'
-    contents may change between calls (and between replays of a captured graph)."""
+    contents may change between calls (and between replays of a captured graph), the
+    attributes may not."""
 
     def __init__(self, table, q_start, kv_len, max_new, max_len):
         import torch

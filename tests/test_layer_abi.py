@@ -287,3 +287,17 @@ def test_binding_rejects_other_devices():
         N._On(torch.device("cuda", 0), Stream())
     with pytest.raises(ValueError):                  # host memory is no argument of a kernel
         N.bitnet_residual_norm(z(4, 8), z(4, 8))
+
+
+@pytest.mark.parametrize("name", ["KVCache", "KVBatch"])
+def test_attributes_are_fixed(name):
+    # the C struct is made once, so an assignment could only be ignored
+    c = getattr(N, name)
+    x = c.__new__(c)
+    x.max_len = x.k = 1
+    for a in ("max_len", "k"):
+        with pytest.raises(AttributeError, match="fixed"):
+            setattr(x, a, 2)
+        assert getattr(x, a) == 1
+    x._struct = (1, None)
+    x._struct = (2, None)
