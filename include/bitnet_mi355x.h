@@ -549,9 +549,11 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, const bitnet_kv_bat
  *   s_j = softmax_scale * (q . k_j),  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),
  *   lse = m + ln sum_j e^(s_j - m),  m = max_j s_j.
  * A row that sees no key gets zeros and lse = -inf.  Sums are fp32 or exact integers;
- * queries are held to 22 bits or more, the weights e^(s - m) to 22 with fp32 in and out
- * and to 11 or more otherwise; lse is summed from unrounded ones.  The same call gives the same bits; another max_len may
- * split the sums elsewhere.
+ * queries are held to 22 bits or more of their row's largest; each weight e^(s - m), times its
+ * page's value scale, to 22 bits of itself with fp32 in and out and to 11 or more otherwise,
+ * those below 2^-48 of the row's largest excepted, which may count as 0 in out; lse is summed
+ * from unrounded ones.  The same call gives the same bits; another max_len may split the sums
+ * elsewhere.
  *   q        [tokens] rows of [q_heads][head_dim], q_stride elements apart (>= q_heads *
  *            head_dim), fp32 or bf16 (q_dtype), finite; query head h reads kv head
  *            h / (q_heads / kv_heads), q_heads a multiple of kv_heads, <= 65535;

@@ -14,8 +14,7 @@ constexpr int kThreads = 256;
 template <bool OB>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(const KvCache c, const KvBatch b,
                                                              const AttnArgs a,
-                                                             const AttnPlan plan, int ways,
-                                                             int cols, float unit,
+                                                             const AttnPlan plan, int ways, int cols,
                                                              const float* __restrict__ part) {
   __shared__ float4 sy[kThreads];
   __shared__ float2 sml[kThreads];
@@ -68,7 +67,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(const KvCache c, co
       }
     }
     if (way > 0 || !on) continue;
-    const float r = l > 0.0f ? 1.0f / (l * unit) : 0.0f;
+    const float r = l > 0.0f ? 1.0f / l : 0.0f;
     const int oc = tile.c0 + col, row = oc / plan.group;
     const int64_t at =
         (tile.sp.s0 + row) * (int64_t)a.q_heads + head * plan.group + (oc - row * plan.group);
@@ -113,12 +112,12 @@ bool many_rows(const KvCache& c, const KvBatch& b, int q_heads) {
 }  // namespace
 
 hipError_t launch_attn_join(const KvCache& c, const KvBatch& b, const AttnArgs& a,
-                            const AttnPlan& p, float unit, bool out_bf16, const float* part,
+                            const AttnPlan& p, bool out_bf16, const float* part,
                             hipStream_t s) {
   int ways = join_ways(c, p), cols = join_cols(c, p, ways);
   const int64_t grid = (int64_t)b.seqs * c.kv_heads * p.tiles * ((p.part_cols + cols - 1) / cols);
   void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&p, (void*)&ways, (void*)&cols,
-                  (void*)&unit, (void*)&part};
+                  (void*)&part};
   return hipLaunchKernel(out_bf16 ? (const void*)attn_join_kernel<true>
                                   : (const void*)attn_join_kernel<false>,
                          dim3((unsigned)grid), dim3(kThreads), args, 0, s);

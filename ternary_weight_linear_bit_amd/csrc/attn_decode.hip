@@ -10,19 +10,24 @@
 // no keys.
 //
 // Bound by memory: every visible code is read once (64 sequences of 1 .. 8191 tokens, 32
-// heads on 8, 128 dims: 131 us, 4.5 TB/s; four of 65536, fp32: 110 us, 4.8 TB/s; a large
+// heads on 8, 128 dims: 137 us, 4.3 TB/s; four of 65536, fp32: 108 us, 4.8 TB/s; a large
 // copy reaches 4.75).  Small calls are bound by one step's latency and two launches (one
-// sequence of 2049 tokens: 10.8 us).  Non-temporal loads were 7-10% slower.  The codes go from memory to
-// the int8 matrix cores as they are, with no conversion and no LDS: it is the other
-// operand that is turned into 8-bit digits, a query row (once) and the weights of a
-// step (16 a lane).  A value x with |x| <= X is held as the integer
-// v = rne(x V / X), V = 127 * 256^(ND - 1), in ND signed base-256 digits, each with
-// its own product; the int32 sums are exact.  Queries take 3 digits (2^-24 of their row's
-// largest value; with two the logits of bf16 queries were 2^-16 off, and lse, an fp32
-// output, with them), weights ND = 2 (2^-16 of the row's largest, finer than bf16's 2^-9
-// of each), or 3 for fp32 in and out.
+// sequence of 2049 tokens: 10.8 us).  Non-temporal loads were 7-10% slower.  The codes go from
+// memory to the int8 matrix cores as they are, with no conversion and no LDS: it is the other
+// operand that is turned into 8-bit digits, a query row (once) and the weights of a step (16 a
+// lane), each digit with its own product; the int32 sums are exact.
+//   * Queries x with |x| <= X: v = rne(x V / X), V = 127 * 256^2, in three signed base-256
+//     digits (2^-24 of their row's largest value; with two the logits of bf16 queries were
+//     2^-16 off, and lse, an fp32 output, with them).
+//   * Weights: 2^14 of them is the power of two above the step's largest, and a pass takes two
+//     digits of what the passes before left, 15 more bits each, until every weight of the
+//     wave's step is within 2^-11 of itself (2^-22 with fp32 in and out) or below 2^-48 of the
+//     row's largest.  Two passes are common (three in fp32); each further one costs 5% where
+//     sequences are uneven and nothing where memory is busy.  A fixed point against the row's
+//     largest weight, in one pass, ran 64 sequences in 131 us and lost what is 2^-16 of it: of
+//     a row whose first key has 95% of the weight, and no value, a third of the output.
 // Converting the codes to 16-bit floats instead would take 320 vector instructions
-// a lane and step of 64 keys, the digits take about 60.
+// a lane and step of 64 keys, the digits of a pass take about 50.
 //
 // The page's scale dv joins the exponent: x_j = log2 e s_j + log2 dv, weights
 // 2^(x_j - max x), so that the weights' fixed-point range fits the largest product
@@ -38,17 +43,17 @@
 // split over workgroups (attn_part) and joined by a second kernel.
 #include "attn_internal.h"
 
+#include <type_traits>
+
 namespace bitnet {
 namespace {
 
 constexpr int kWaves = 4, kManyWaves = 8, kStep = kAttnStep, kCols = 16;
-constexpr int kQd = 3;   // digits of a query
-
-// Fixed point of a digit count.
-template <int ND>
-struct Digits {
-  static constexpr float kTop = ND == 2 ? 32512.0f : 8323072.0f;   // 127 * 256^(ND - 1)
-};
+constexpr int kQd = 3;                 // digits of a query
+constexpr float kQTop = 8323072.0f;    // 127 * 256^2: a query row's largest value
+constexpr float kLift = 14.0f;         // weights of a step: at most 2^14, two digits
+constexpr float kPass = 0x1p-15f;      // unit of a pass over that of the pass before
+constexpr float kRound = kRneMagic + 128.0f;
 
 // Byte K of four dwords, a first.
 template <int K>
@@ -59,29 +64,38 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
   return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
 }
 
-// Digits (most significant first) of four values x >= -1, <= 1 times kTop.  With
-// u = v + 0x80 (ND 2) or v + 0x8080 (ND 3) byte j of u is digit j, its top bit
-// flipped for all but the highest.
-template <int ND>
-__device__ __forceinline__ void digits4(const float x[4], uint32_t out[ND]) {
+// Three digits (most significant first) of four values x >= -1, <= 1 times kQTop.  With
+// u = v + 0x8080 byte j of u is digit j, its top bit flipped for all but the highest.
+__device__ __forceinline__ void query_digits(const float x[4], uint32_t out[kQd]) {
   uint32_t u[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (ND == 2)   // one addition rounds to nearest even and adds 0x80 (see rne_bits)
-      u[j] = __float_as_uint(__fadd_rn(__fmul_rn(x[j], Digits<2>::kTop), kRneMagic + 128.0f));
-    else
-      u[j] = (uint32_t)((int)rintf(__fmul_rn(x[j], Digits<3>::kTop)) + 0x8080);
-  }
-  out[ND - 1] = bytes4<0>(u[0], u[1], u[2], u[3]) ^ 0x80808080u;
-  out[ND - 2] = bytes4<1>(u[0], u[1], u[2], u[3]) ^ (ND == 3 ? 0x80808080u : 0u);
-  if (ND == 3) out[0] = bytes4<2>(u[0], u[1], u[2], u[3]);
+  for (int j = 0; j < 4; ++j) u[j] = (uint32_t)((int)rintf(__fmul_rn(x[j], kQTop)) + 0x8080);
+  out[2] = bytes4<0>(u[0], u[1], u[2], u[3]) ^ 0x80808080u;
+  out[1] = bytes4<1>(u[0], u[1], u[2], u[3]) ^ 0x80808080u;
+  out[0] = bytes4<2>(u[0], u[1], u[2], u[3]);
+}
+// Two digits of four values |y| <= 2^14 `unit` in units: adding kRound units rounds to
+// nearest even and leaves the integer, and 0x80, in the float's low bits (see rne_bits).
+__device__ __forceinline__ void weight_digits(const float y[4], float unit, uint32_t out[2]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) u[j] = __float_as_uint(__fadd_rn(y[j], kRound * unit));
+  out[1] = bytes4<0>(u[0], u[1], u[2], u[3]) ^ 0x80808080u;
+  out[0] = bytes4<1>(u[0], u[1], u[2], u[3]);
+}
+// What that rounding leaves of a value, at most half a unit: both differences are exact.
+__device__ __forceinline__ float weight_rest(float y, float unit) {
+  return __fsub_rn(y, __fsub_rn(__fadd_rn(y, kRound * unit), kRound * unit));
+}
+// 2^n of a whole n <= 126, exactly; 0 far below.  (A larger n only meets sums of 0.)
+__device__ __forceinline__ float power_of_2(float n) {
+  return __builtin_amdgcn_ldexpf(1.0f, (int)fminf(fmaxf(n, -200.0f), 126.0f));
 }
 
-// The number that ND int32 digit sums stand for.
-template <int ND>
-__device__ __forceinline__ float joined(const int d[ND]) {
+// The number that a product's int32 digit sums stand for.
+__device__ __forceinline__ float joined(const int d[kQd]) {
   const float t = (float)(d[0] * 256 + d[1]);   // |digit sum| < 2^22: exact in int32
-  return ND == 2 ? t : __builtin_fmaf(t, 256.0f, (float)d[ND - 1]);
+  return __builtin_fmaf(t, 256.0f, (float)d[2]);
 }
 
 // max / sum over the four 16-lane rows of the wave (lanes with equal lane % 16)
@@ -100,8 +114,8 @@ __device__ __forceinline__ float rows_sum(float v) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// NW: waves.  ND: digits of a weight.
-template <int DP, int NW, int ND, bool QB, bool OB>
+// NW: waves.  B: bits that each weight keeps.
+template <int DP, int NW, int B, bool QB, bool OB>
 __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel(
     const KvCache c, const KvBatch b, const AttnArgs a, const AttnPlan plan,
     float* __restrict__ part) {
@@ -149,7 +163,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
     amax = rows_max(amax);
     const float up = amax < 0x1p-64f ? 0x1p64f : 1.0f;   // keeps 1 / amax finite
     const float inv = amax > 0.0f ? 1.0f / (amax * up) : 0.0f;
-    qscale = amax / Digits<kQd>::kTop * a.scale * 1.44269504088896340736f;
+    qscale = amax / kQTop * a.scale * 1.44269504088896340736f;
 #pragma unroll
     for (int kc = 0; kc < KC; ++kc)
 #pragma unroll
@@ -158,7 +172,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(__fmul_rn(q[kc][4 * w + j], up), inv);
         uint32_t d[kQd];
-        digits4<kQd>(x, d);
+        query_digits(x, d);
 #pragma unroll
         for (int n = 0; n < kQd; ++n) qd[n][kc][w] = (int)d[n];
       }
@@ -195,7 +209,8 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
       vr[dt] = *reinterpret_cast<const v4i*>(at + min(16 * dt + col, D - 1) * P);
   };
 
-  float m = -INFINITY, l = 0.0f;
+  // m: the largest x so far.  l, o: over 2^r, a whole number.
+  float m = -INFINITY, r = 0.0f, l = 0.0f;
   float o[DT][4];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
@@ -239,7 +254,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
         int d[kQd];
 #pragma unroll
         for (int n = 0; n < kQd; ++n) d[n] = s[n][i];
-        x[t][i] = joined<kQd>(d);
+        x[t][i] = joined(d);
       }
     }
     pid_k2 = page_of(step + 2 * NW, col >> 2);
@@ -261,40 +276,60 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
         x[t][i] = 4 * t + i <= hi && 4 * t + i >= lo ? y : -INFINITY;
         mx = fmaxf(mx, x[t][i]);
       }
-    mx = fmaxf(rows_max(mx), m);
-    const float ref = mx == -INFINITY ? 0.0f : mx;
-    const float alpha = __builtin_amdgcn_exp2f(m - ref);
-    m = mx;
+    mx = rows_max(mx);
+    m = fmaxf(m, mx);
+    const float rest = ceilf(m) - kReach;   // weights below 2^rest may be lost
+    const float to = mx == -INFINITY ? r : fmaxf(ceilf(mx), rest) - kLift;
+    const float alpha = power_of_2(r - to), floor = fmaxf(power_of_2(rest - to), 0x1p-126f);
+    r = to;
     float sum = 0.0f;
-    v4i pd[ND];
+    uint32_t low = 0x7f800000u;   // the least weight from `floor` on, less that: by its bits,
+                                 // as those of negative numbers are larger
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[t][i] = __builtin_amdgcn_exp2f(x[t][i] - ref);
-        sum += x[t][i];
+        const float p = __builtin_amdgcn_exp2f(x[t][i] - r);
+        x[t][i] = p;
+        sum += p;
+        low = min(low, __float_as_uint(p - floor));
       }
-      uint32_t d[ND];
-      digits4<ND>(x[t], d);
-#pragma unroll
-      for (int n = 0; n < ND; ++n) pd[n][t] = (int)d[n];
-    }
     l = __builtin_fmaf(l, alpha, sum * rdv);
     if (more) scales(pid_v1);
 
+    // Two digits of every weight; then, as long as some weight of the wave is not held to
+    // B bits (it is off by at most half of `unit`), two digits of what they left.
+    float unit = 1.0f;
+    auto pass = [&](auto first) {
+      v4i pd[2];
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-      v4i y[ND];
+      for (int t = 0; t < 4; ++t) {
+        uint32_t d[2];
+        if (!first.value)
 #pragma unroll
-      for (int n = 0; n < ND; ++n)
-        y[n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vr[dt], pd[n], (v4i){0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        int d[ND];
-#pragma unroll
-        for (int n = 0; n < ND; ++n) d[n] = y[n][i];
-        o[dt][i] = __builtin_fmaf(o[dt][i], alpha, joined<ND>(d));
+          for (int i = 0; i < 4; ++i) x[t][i] = weight_rest(x[t][i], unit * (1.0f / kPass));
+        weight_digits(x[t], unit, d);
+        pd[0][t] = (int)d[0];
+        pd[1][t] = (int)d[1];
       }
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        v4i y[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          y[n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vr[dt], pd[n], (v4i){0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float s = (float)(y[0][i] * 256 + y[1][i]);   // |digit sum| < 2^21: exact in int32
+          o[dt][i] = first.value ? __builtin_fmaf(o[dt][i], alpha, s) : __builtin_fmaf(s, unit, o[dt][i]);
+        }
+      }
+    };
+    pass(std::true_type{});
+    const float least = __uint_as_float(low) + floor;   // at least 2^-34 of the reference
+    while (__builtin_amdgcn_ballot_w64(least < unit * (1 << (B - 1)))) {
+      unit *= kPass;
+      pass(std::false_type{});
     }
     if (more) {
       load_v(step + NW, pid_v1);
@@ -305,7 +340,9 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
   }
 
   // join the waves: each scales its sums to the common maximum
-  l = rows_sum(l);
+  m = ceilf(m);
+  const float back = m == -INFINITY ? 0.0f : power_of_2(r - m);   // to sums over 2^m
+  l = rows_sum(l) * back;
   if (g == 0) {
     sm[wave][col] = m;
     sl[wave][col] = l;
@@ -317,7 +354,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
 #pragma unroll
   for (int w = 0; w < NW; ++w)
     total += sm[w][col] == -INFINITY ? 0.0f : sl[w][col] * __builtin_amdgcn_exp2f(sm[w][col] - top);
-  const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+  const float f = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - top) * back;
   const int64_t pu = (int64_t)blockIdx.x * plan.part_cols;
 #pragma unroll
   for (int h0 = 0; h0 < DT; h0 += HT) {
@@ -348,16 +385,16 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
 #pragma unroll
         for (int w = 0; w < NW; ++w)
           el += sm[w][ec] == -INFINITY ? 0.0f : sl[w][ec] * __builtin_amdgcn_exp2f(sm[w][ec] - et);
-        const float r = el > 0.0f ? 1.0f / (el * Digits<ND>::kTop) : 0.0f;
+        const float rl = el > 0.0f ? 1.0f / el : 0.0f;
         const int oc = tile.c0 + ec, orow = oc / group;
         const int64_t at = ((tile.sp.s0 + orow) * a.q_heads + head * group + (oc - orow * group)) * D +
                            16 * h0 + d;
         if (OB)
           *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
-              make_uint2(bf16x2_rne(y.x * r, y.y * r), bf16x2_rne(y.z * r, y.w * r));
+              make_uint2(bf16x2_rne(y.x * rl, y.y * rl), bf16x2_rne(y.z * rl, y.w * rl));
         else
           *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) =
-              make_float4(y.x * r, y.y * r, y.z * r, y.w * r);
+              make_float4(y.x * rl, y.y * rl, y.z * rl, y.w * rl);
       } else {
         *reinterpret_cast<float4*>(part + (pu + ec) * (D + 4) + 4 + 16 * h0 + d) = y;
       }
@@ -374,10 +411,10 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
 
 template <int DP, int NW>
 const void* pick_decode(bool qb, bool ob) {
-  return qb ? (ob ? (const void*)attn_decode_kernel<DP, NW, 2, true, true>
-                  : (const void*)attn_decode_kernel<DP, NW, 2, true, false>)
-            : (ob ? (const void*)attn_decode_kernel<DP, NW, 2, false, true>
-                  : (const void*)attn_decode_kernel<DP, NW, 3, false, false>);
+  return qb ? (ob ? (const void*)attn_decode_kernel<DP, NW, 11, true, true>
+                  : (const void*)attn_decode_kernel<DP, NW, 11, true, false>)
+            : (ob ? (const void*)attn_decode_kernel<DP, NW, 11, false, true>
+                  : (const void*)attn_decode_kernel<DP, NW, 22, false, false>);
 }
 template <int NW>
 const void* pick_decode(int dim, bool qb, bool ob) {
@@ -416,8 +453,7 @@ hipError_t launch_attn_decode(const KvCache& c, const KvBatch& b, const AttnArgs
   void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&p, (void*)&part};
   const hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(64 * p.waves), args, 0, s);
   if (e != hipSuccess || p.splits == 1) return e;
-  const float unit = !q_bf16 && !out_bf16 ? Digits<3>::kTop : Digits<2>::kTop;
-  return launch_attn_join(c, b, a, p, unit, out_bf16, part, s);
+  return launch_attn_join(c, b, a, p, out_bf16, part, s);
 }
 
 }  // namespace bitnet

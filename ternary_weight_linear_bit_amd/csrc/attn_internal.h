@@ -7,6 +7,10 @@
 namespace bitnet {
 
 constexpr int kAttnStep = 64;   // keys of one step
+// Weights e^(s - m) dv below 2^-kReach of their row's largest may count as 0 in the output: a
+// row's sums then stay in fp32's range whatever they are taken over, and 2^24 such weights are
+// less than half of fp32's last bit of the row's.
+constexpr float kReach = 48.0f;
 
 // Columns [c0, c0 + nc) of a sequence's (row, query head of the group) pairs, rows
 // outermost, and the 64-key steps that those rows see.
@@ -65,10 +69,9 @@ struct AttnPlan {
   int waves;                // of a workgroup
 };
 // A part of a tile in the workspace: part_cols columns of head_dim + 4 floats: the
-// maximum m (log2), the sum of 2^(x - m) / dv, two unused, and the sums over 2^(x - m) vc
-// times `unit`.
+// maximum m (log2), the sum of 2^(x - m) / dv, two unused, and the sums over 2^(x - m) vc.
 hipError_t launch_attn_join(const KvCache& c, const KvBatch& b, const AttnArgs& a,
-                            const AttnPlan& p, float unit, bool out_bf16, const float* part,
+                            const AttnPlan& p, bool out_bf16, const float* part,
                             hipStream_t s);
 
 inline AttnPlan attn_plan(const KvCache& c, const KvBatch& b, int q_heads, int cols,

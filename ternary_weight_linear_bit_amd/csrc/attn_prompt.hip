@@ -486,7 +486,7 @@ hipError_t launch_attn_prompt(const KvCache& c, const KvBatch& b, const AttnArgs
   void* args[] = {(void*)&c, (void*)&b, (void*)&a, (void*)&p, (void*)&part};
   const hipError_t e = hipLaunchKernel(kern, dim3((unsigned)grid), dim3(p.cols * 2), args, lds, s);
   if (e != hipSuccess || p.splits == 1) return e;
-  return launch_attn_join(c, b, a, p, 1.0f, out_bf16, part, s);
+  return launch_attn_join(c, b, a, p, out_bf16, part, s);
 }
 
 }  // namespace bitnet
