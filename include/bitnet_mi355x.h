@@ -551,7 +551,8 @@ bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, const bitnet_kv_bat
  * A row that sees no key gets zeros and lse = -inf.  Sums are fp32 or exact integers;
  * queries are held to 22 bits or more of their row's largest; each weight e^(s - m), times its
  * page's value scale, to 22 bits of itself with fp32 in and out and to 11 or more otherwise,
- * those below 2^-48 of the row's largest excepted, which may count as 0 in out; lse is summed
+ * those below 2^-48 of the row's largest excepted, which may count as 0 in out, and what moves
+ * no element of out by more than 2^-24 of the row's largest for each 64 keys; lse is summed
  * from unrounded ones.  The same call gives the same bits; another max_len may split the sums
  * elsewhere.
  *   q        [tokens] rows of [q_heads][head_dim], q_stride elements apart (>= q_heads *

@@ -3,8 +3,8 @@
 // attn_decode.hip.
 //
 // Bound by the vector and matrix instructions together: 8192 tokens of 32 heads on 8, 128
-// dims, bf16, take 566-600 us (916-971 TFLOP/s; a library product of bf16 matrices reaches
-// 1208 on this card), with vector instructions in 55% of the cycles and matrix ones in 42%.
+// dims, bf16, take 590-603 us (912-932 TFLOP/s; a library product of bf16 matrices reaches
+// 1208 on this card), with vector instructions in 55% of the cycles and matrix ones in 40%.
 // Random data draw the clock down: zeros run 17% faster.  Staging a step deeper behind half
 // the barriers, raised wave priority around the products, issue-order hints, values read a
 // group ahead and the two key tiles' products in turn all measured within 2%.
@@ -18,9 +18,15 @@
 //   * Queries: scaled by a power of two to a largest value in [2^10, 2^11), then fp16
 //     (bf16 queries fit exactly); fp32 queries take two fp16 terms (22 bits).
 //   * Weights p = 2^(x - m + 7), x = log2 e s + log2 dv (the page's scale joins the
-//     exponent), rounded to fp16 (2^-12 of each, finer than bf16's 2^-9); for fp32 in
-//     and out two terms.  m follows the running maximum only when it grows by more
-//     than 2^8, so that the accumulators are seldom rescaled; p stays below 2^15.
+//     exponent), rounded to fp16 (within 2^-11 of each, finer than bf16's 2^-8); for fp32 in
+//     and out p = 2^(x - m + 14) in two terms (2^-22).  m follows the largest x of the steps
+//     when that lies more than 2^8 apart, so that the accumulators are seldom rescaled and a
+//     row whose large weight is met early keeps the small ones that come after it; p stays
+//     below 2^15.  Weights that are too small for fp16 beside the largest of their own step
+//     are seen by the least of the rounded ones; where the row's sums are so small that it
+//     matters, what rounding left of them is added in a second round of the step's products
+//     (Weights, below).  With m as the running maximum alone such rows lost what is below
+//     2^-32 of the largest weight, and 8192 tokens took 2-4% less.
 //   * Sums over keys and the softmax sum are fp32 (the latter of the unrounded p, over
 //     each page's dv: of the rounded ones, two a dot instruction, lse lost 2^-12).
 // Products: S[key][column] = K Q^T in 32 x 32 tiles, where row r of a tile reads key
@@ -56,7 +62,19 @@ __device__ __forceinline__ int v_group(int dim, int at) {
   const int f = ((dim >> 1) & 3) | ((dim >> 2) & 4);
   return dim * kStep * 2 + ((at ^ f) & 7) * 16;
 }
-constexpr float kLift = 7.0f, kSlack = 8.0f;   // p <= 2^(kLift + kSlack)
+
+// Weights of PT fp16 terms: p = 2^(x - m + kLift), at most 2^15, which keep 11 PT bits from
+// kHeld on.  m is set anew where a step's largest x lies more than kSlack above or kSink
+// below it.
+template <int PT>
+struct Weights {
+  static constexpr float kLift = PT == 1 ? 7.0f : 14.0f, kSlack = 15.0f - kLift, kSink = 8.0f;
+  static constexpr float kHeld = PT == 1 ? 0x1p-14f : 0x1p-3f;
+  static constexpr float kUp = PT == 1 ? 0x1p29f : 0x1p33f;   // the second round's, over those
+};
+// A smaller weight lacks at most 2^-25, and a sum over a step's 64 keys, codes up to 127, at
+// most 2^-12: less than 2^-24 of the row's largest sum where that is kSums or more.
+constexpr float kSums = 0x1p12f;
 
 // Four codes as fp16 pairs.
 __device__ __forceinline__ void codes_to_h4(uint32_t w, uint32_t out[2]) {
@@ -99,7 +117,7 @@ __device__ __forceinline__ bool is_scale(float v) {
 
 // NW: waves (32 columns each).  QT / PT: fp16 terms of a query and of a weight.
 template <int DP, int NW, int QT, int PT, bool QB, bool OB>
-__global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel(
+__global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : DP == 128 ? 2 : 1) void attn_prompt_kernel(
     const KvCache c, const KvBatch b, const AttnArgs a, const AttnPlan plan,
     float* __restrict__ part) {
   constexpr int kThreads = 64 * NW, kCols = 32 * NW;
@@ -248,7 +266,9 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
   };
 
   const int first = tile.step0 + s_lo, end = tile.step0 + s_hi;
-  float m = -INFINITY, l = 0.0f;
+  using Wt = Weights<PT>;
+  float m = -INFINITY, l = 0.0f;   // l, o: over 2^(m - kLift)
+  float most = -INFINITY;          // the largest x so far
   v16f o[DT];
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
@@ -257,6 +277,55 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
 
   // row of a 32-key tile that the lane's operand reads
   const int krow = 16 * (col >> 4) + 8 * ((col >> 2) & 1) + 4 * ((col >> 3) & 1) + (col & 3);
+
+  // logits of a step's 32-key tile kt, over qscale and their keys' scales.  slow: with few
+  // values in flight (off the loop's common path, whose registers count)
+  auto logits = [&](const uint8_t* buf, int kt, v16f& t, bool slow = false) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) t[j] = 0.0f;
+    const int key = kt * 32 + krow;
+#pragma unroll
+    for (int kc = 0; kc < KC; ++kc) {
+      const v8h kk = *reinterpret_cast<const v8h*>(buf + k_group<DP>(key, 2 * kc + h));
+#pragma unroll
+      for (int n = 0; n < QT; ++n)
+        t = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, q[n][kc], t, 0, 0, 0);
+      if (slow) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // fp16 terms of weights; see(w): pairs of the first ones
+  auto terms = [&](float p[8], v8h pf[PT], auto see) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < PT; ++n) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = h2_of(p[2 * j], p[2 * j + 1]);
+        if (n == 0) see(w[j]);
+        if (n + 1 < PT) h2_rest(w[j], p[2 * j], p[2 * j + 1]);
+      }
+      const uint4 u = make_uint4(w[0], w[1], w[2], w[3]);
+      pf[n] = __builtin_bit_cast(v8h, u);
+    }
+  };
+  // the terms of a step's group g join the sums
+  auto join = [&](const uint8_t* buf, int g, const v8h pf[PT], bool slow = false) __attribute__((always_inline)) {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      const int dim = 32 * dt + col;
+      const v8h vv = *reinterpret_cast<const v8h*>(buf + kKBytes + v_group(dim, 2 * g + h));
+#pragma unroll
+      for (int n = 0; n < PT; ++n)
+        o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, pf[n], o[dt], 0, 0, 0);
+      if (slow) __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto times = [&](float f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[dt][j] *= f;
+  };
 
   // One step from buffer B.  Loads run ahead without a test for the end: past it they
   // read the sequence's last page again.
@@ -272,19 +341,8 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
     // some column of the wave sees some key of this step
     const bool any = key0 <= pos_hi && key0 + kStep - 1 >= from_lo;
     v16f s[2];
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[kt][j] = 0.0f;
-      const int key = kt * 32 + krow;
-#pragma unroll
-      for (int kc = 0; kc < KC; ++kc) {
-        const v8h kk = *reinterpret_cast<const v8h*>(buf + k_group<DP>(key, 2 * kc + h));
-#pragma unroll
-        for (int n = 0; n < QT; ++n)
-          s[kt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kk, q[n][kc], s[kt], 0, 0, 0);
-      }
-    }
+    logits(buf, 0, s[0]);
+    logits(buf, 1, s[1]);
     stage(lds + (1 - B) * kBuf);
     g2 = page_of(step + 3);   // before the codes: the next step waits for it, not for them
     load(step + 2, g1);
@@ -302,7 +360,8 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
         rg[g] = lane_of(rdv, g);
       }
       // group g holds s[g / 2][8 (g % 2) + j], j = 0 .. 7: key 16 g + 8 h + j
-      if (hole || key0 + kStep - 1 > pos_lo || key0 < from_hi) {
+      const bool whole = !hole && key0 + kStep - 1 <= pos_lo && key0 >= from_hi;
+      if (!whole) {
         const int hi = pos - key0 - 8 * h, lo = from - key0 - 8 * h;
 #pragma unroll
         for (int g = 0; g < 4; ++g)
@@ -322,17 +381,16 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
         mx = __builtin_fmaxf(mx, __builtin_fmaf(t, ck[g], lg[g]));
       }
       mx = halves_max(mx);
-      if (__builtin_amdgcn_ballot_w64(mx > m + kSlack)) {
-        const float to = __builtin_fmaxf(m, mx);
+      most = __builtin_fmaxf(most, mx);
+      const float to = mx == -INFINITY ? m : __builtin_fmaxf(mx, most - kReach);
+      if (__builtin_amdgcn_ballot_w64((to > m + Wt::kSlack) | (to < m - Wt::kSink))) {
         const float alpha = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
         m = to;
         l *= alpha;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[dt][j] *= alpha;
+        times(alpha);
       }
-      const float ref = m == -INFINITY ? 0.0f : m - kLift;
+      const float ref = m == -INFINITY ? 0.0f : m - Wt::kLift;
+      v2h least = {(_Float16)65504.0f, (_Float16)65504.0f};   // of the weights
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         float p[8], sum = 0.0f;
@@ -344,26 +402,58 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
         }
         l = __builtin_fmaf(sum, rg[g], l);
         v8h pf[PT];
+        terms(p, pf, [&](uint32_t w) {
+          least = __builtin_elementwise_minimum(least, __builtin_bit_cast(v2h, w));
+        });
+        join(buf, g, pf);
+      }
+      // Weights below kHeld (or unseen, where the step is not whole): whether it matters what
+      // they lack
+      bool small = !whole | (least[0] < (_Float16)Wt::kHeld) | (least[1] < (_Float16)Wt::kHeld);
+      if (__builtin_expect(__builtin_amdgcn_ballot_w64(small) != 0, 0)) {
+        float large = 0.0f;
 #pragma unroll
-        for (int n = 0; n < PT; ++n) {
-          uint32_t w[4];
+        for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            w[j] = h2_of(p[2 * j], p[2 * j + 1]);
-            if (n + 1 < PT) h2_rest(w[j], p[2 * j], p[2 * j + 1]);
+          for (int j = 0; j < 16; ++j) large = __builtin_fmaxf(large, __builtin_fabsf(o[dt][j]));
+        small = (halves_max(large) < kSums) & (l > 0.0f);
+      }
+      // The second round: what is lacking, over a reference kUp lower.  It is held to 11 PT
+      // bits or 2^-25 / kUp, as weights down to 2^-kReach of the row's largest (2^(kLift - 48)
+      // and more) need.  (The tiles in a loop, so that registers spill inside it if they have
+      // to; for bf16 heads of 128 dims they suffice unrolled.)
+      if (__builtin_expect(__builtin_amdgcn_ballot_w64(small) != 0, 0)) {
+        times(Wt::kUp);
+#pragma unroll(QT == 1 && DP == 128 ? 2 : 1)
+        for (int kt = 0; kt < 2; ++kt) {
+          const int hi = pos - key0 - 8 * h - 32 * kt, lo = from - key0 - 8 * h - 32 * kt;
+          v16f t;
+          logits(buf, kt, t, true);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float k = lane_of(dk_now, 2 * kt + g), c1 = fmaxf(qscale * k, 1e-38f);
+            const float c0 = lane_of(lv, 2 * kt + g) - ref;
+            const bool on = (int)__float_as_uint(k) >= 0;
+            float p[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(t[8 * g + j], c1, c0));
+              p[j] = (on & (16 * g + j <= hi) & (16 * g + j >= lo) & (x < Wt::kHeld)) ? x : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int n = 0; n < PT; ++n) h2_rest(h2_of(p[2 * j], p[2 * j + 1]), p[2 * j], p[2 * j + 1]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p[j] *= Wt::kUp;
+            v8h pf[PT];
+            terms(p, pf, [](uint32_t) {});
+            join(buf, 2 * kt + g, pf, true);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          const uint4 u = make_uint4(w[0], w[1], w[2], w[3]);
-          pf[n] = __builtin_bit_cast(v8h, u);
         }
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          const int dim = 32 * dt + col;
-          const v8h vv = *reinterpret_cast<const v8h*>(
-              buf + kKBytes + v_group(dim, 2 * g + h));
-#pragma unroll
-          for (int n = 0; n < PT; ++n)
-            o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, pf[n], o[dt], 0, 0, 0);
-        }
+        times(1.0f / Wt::kUp);
       }
     }
     lds_barrier();
@@ -400,7 +490,9 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
 
   l = halves_sum(l);
   if (!live) return;
-  const float top = m - kLift;   // l and o are over 2^(m - kLift)
+  // sums over 2^top, near the largest weight
+  const float top = most - Wt::kLift, back = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m - most);
+  l *= back;
   if (!alone) {
     float* p = part + (((int64_t)(seq * c.kv_heads + head) * plan.tiles + ct) * plan.splits + split) *
                           plan.part_cols * (D + 4) +
@@ -413,11 +505,12 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_prompt_kernel
         const int d = 32 * dt + 8 * w + 4 * h;
         if (d < D)
           *reinterpret_cast<float4*>(p + 4 + d) =
-              make_float4(o[dt][4 * w], o[dt][4 * w + 1], o[dt][4 * w + 2], o[dt][4 * w + 3]);
+              make_float4(o[dt][4 * w] * back, o[dt][4 * w + 1] * back, o[dt][4 * w + 2] * back,
+                          o[dt][4 * w + 3] * back);
       }
     return;
   }
-  const float r = l > 0.0f ? 1.0f / l : 0.0f;
+  const float r = l > 0.0f ? back / l : 0.0f;
   const int64_t at = (t_row * a.q_heads + q_head) * D;
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)

@@ -54,17 +54,17 @@ def paged(kc, vc, page):
     return np.ascontiguousarray(k), np.ascontiguousarray(v)
 
 
-def one_key_a_dim(rng, keys, dim, heads):
-    """Value codes [heads, keys, dim] of which each dim has one key only (127), so that an output
-    is that key's weight; returns them and the key of each dim [heads, dim]."""
+def one_key_a_dim(rng, keys, dim, heads, but=None):
+    """Value codes [heads, keys, dim] of which each dim has one key only (127), none of head h's
+    but[h], so that an output is that key's weight."""
     vc = np.zeros((heads, keys, dim), np.int8)
-    who = np.stack([rng.choice(keys, dim, replace=keys < dim) for _ in range(heads)])
     for h in range(heads):
-        vc[h, who[h], np.arange(dim)] = 127
-    return vc, who
+        some = np.setdiff1d(np.arange(keys), but[h] if but else ())
+        vc[h, rng.choice(some, dim, replace=len(some) < dim), np.arange(dim)] = 127
+    return vc
 
 
-def weight_bounds(out, lse, absv, flat, top, reach, q, keys, exact_io, out_bf16):
+def weight_bounds(out, lse, absv, flat, top, reach, q, keys, exact_io, out_bf16, steps=0):
     """How far out and lse may be from the float64 ones, elementwise, whatever the values are.
 
     A logit is off by at most e (layer_util.attention_bounds: the queries to 2^-22 of their row's
@@ -73,11 +73,14 @@ def weight_bounds(out, lse, absv, flat, top, reach, q, keys, exact_io, out_bf16)
     out: it is off by at most 2^-11 or 2^-22 of itself, and the sum of w v by that share of the
     sum of w |v|.  fp32 sums over `keys` keys: (keys / 16 + 32) 2^-24 of it.  Weights below
     2^-48 of the row's largest may be 0: flat (the largest weight times the sum of |v|)
-    times 2^-48.  The output's type rounds by half a step: 2^-8 (bf16) or 2^-24 of the value."""
+    times 2^-48.  In each of `steps` steps (the prompt kernel) the weights may further lack what
+    moves no sum by more than 2^-24 of the row's largest sum of w |v|.  The output's type rounds
+    by half a step: 2^-8 (bf16) or 2^-24 of the value."""
     e = reach * np.abs(q).max(-1) * 2.0 ** -22 + top * 2.0 ** -21 + 2.0 ** -20
     sums = (keys / 16 + 32) * 2.0 ** -24
     held = 2.0 ** -22 if exact_io else 2.0 ** -11
     err = (np.expm1(2 * e) + sums + held)[..., None] * absv + flat * REACH
+    err = err + (steps * 2.0 ** -24 * absv.max(-1))[..., None]
     half = 2.0 ** -8 if out_bf16 else 2.0 ** -24
     tol_lse = e + sums + 2.0 ** -22 * np.abs(lse)
     return err + half * (np.abs(out) + err) + 1e-30, tol_lse

@@ -1,5 +1,5 @@
-"""The arithmetic of the decode attention kernel's weights, step by step on the CPU, on rows in
-which one key outweighs thousands; and that the bounds of such rows reject what loses the small
+"""The arithmetic of the attention kernels' weights, step by step on the CPU, on rows in which one
+key outweighs thousands; and that the bounds of such rows reject what loses the small
 weights."""
 
 import numpy as np
@@ -116,7 +116,7 @@ def test_each_weight_by_itself(spread, bits):
     """Every dim has the value of one key only: its output is that key's weight."""
     rng = np.random.default_rng(7)
     q, kc, _, dk, dv, scale = peaked(rng, 1, 1, 1, 128, 300, 5, 40, spread=spread)
-    vc, _ = one_key_a_dim(rng, 300, 128, 1)
+    vc = one_key_a_dim(rng, 300, 128, 1)
     row = (q[0, 0], kc[0], vc[0], dk, dv, scale)
     want, tol = bounds_of(row, bits == 22, False)
     got = by_steps(*row, bits)
@@ -145,3 +145,29 @@ def test_bounds_reject_lost_weights(keys, gap):
 def test_floor_is_small():
     """All the weights that may count as 0, of 2^24 keys, are less than half of fp32's last bit."""
     assert REACH * 2 ** 24 <= 2.0 ** -24
+
+
+@pytest.mark.parametrize("terms,lift,held,up", [(1, 7, -14, 29), (2, 14, -3, 33)])
+def test_prompt_terms_hold_small_weights(terms, lift, held, up):
+    """The prompt kernel's fp16 terms of a weight, and of what they lack where it is below
+    2^held: 11 bits a term down to 2^-48 of the largest; without them a sum over 64 keys of codes
+    up to 127 lacks at most 2^-12."""
+    rng = np.random.default_rng(5)
+
+    def split(x):
+        out, rest = np.zeros_like(x), x
+        for _ in range(terms):
+            t = rest.astype(np.float16).astype(F32)
+            out, rest = out + t.astype(np.float64), (rest - t).astype(F32)
+        return out, rest
+    p = np.exp2(rng.uniform(lift - 48, 15, 100000)).astype(F32)
+    first, rest = split(p)
+    assert np.all(np.isfinite(first))
+    np.testing.assert_array_equal(first + rest, p)                # nothing is lost on the way
+    small = p < 2.0 ** held
+    assert np.all(np.abs(rest[~small]) <= 2.0 ** (-11 * terms) * p[~small])
+    assert 64 * 127 * np.abs(rest[small]).max() <= 2.0 ** -12
+    lifted = (rest * F32(2.0 ** up)).astype(F32)
+    second, _ = split(lifted)
+    err = np.abs(first + second * 2.0 ** -up - p)
+    assert np.all(err[small] <= 2.0 ** (-11 * terms) * p[small])

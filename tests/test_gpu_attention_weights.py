@@ -19,7 +19,7 @@ PAIRS = pytest.mark.parametrize("dt,out_dt", [("bf16", "bf16"), ("f32", "f32"), 
 # kv heads, query heads, rows of a sequence, the least stated max_len: 16 columns a workgroup
 # and few heads for the decode kernel; 48 columns and a large cache for the prompt kernel
 DECODE, PROMPT = (2, 6, 2, 0), (32, 32, 50, 16384)
-BOTH = pytest.mark.parametrize("size", [DECODE], ids=["decode"])
+BOTH = pytest.mark.parametrize("size", [DECODE, PROMPT], ids=["decode", "prompt"])
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -29,7 +29,7 @@ def _gpu():
     N.lib()
 
 
-def run(size, dim, page, lens, dt, out_dt, gap, at=0, value=(False, True), spread=1.0, alone=False, window=0,
+def run(size, dim, page, lens, dt, out_dt, gap, at=0, value=(False, True), spread=1.0, alone="", window=0,
         seed=0, rows=None):
     heads, q_heads, new, least = size
     new = rows or new
@@ -38,7 +38,8 @@ def run(size, dim, page, lens, dt, out_dt, gap, at=0, value=(False, True), sprea
     qf = np.concatenate([m[0] for m in made])
     ks, vs, table, first = [], [], np.full((len(lens), max(-(-max(lens) // page), least // page)), -1, np.int32), 0
     for b, m in enumerate(made):
-        vc = one_key_a_dim(rng, lens[b], dim, heads)[0] if alone else m[2]
+        large = [[(at + i) % lens[b] for i in range(q_heads) if i // (q_heads // heads) == h] for h in range(heads)]
+        vc = one_key_a_dim(rng, lens[b], dim, heads, None if alone == "all" else large) if alone else m[2]
         k, v = paged(m[1], vc, page)
         table[b, :len(k)] = first + rng.permutation(len(k))
         ks.append(np.empty_like(k))
@@ -61,7 +62,8 @@ def run(size, dim, page, lens, dt, out_dt, gap, at=0, value=(False, True), sprea
     want, wl, *detail = L.attention(k, v, dks, dvs, table, q_start, kv_len, qf, scale, window, new, max_len,
                                     detail=True)
     keys = np.repeat(kv_len, new)[:, None].astype(np.float64)
-    tol, tol_l = weight_bounds(want, wl, *detail, qf, keys, dt == "f32" and out_dt == "f32", out_dt == "bf16")
+    tol, tol_l = weight_bounds(want, wl, *detail, qf, keys, dt == "f32" and out_dt == "f32", out_dt == "bf16",
+                               steps=0 if size is DECODE else keys / 64 + 1)
     bad = ~(np.abs(got - want) <= tol)
     assert not bad.any(), (bad.mean(), np.max(np.abs(got - want) / tol), np.argwhere(bad)[:5], got[bad][:5],
                            want[bad][:5], tol[bad][:5])
@@ -104,7 +106,16 @@ def test_window_past_the_key(size, dt):
 def test_each_weight_by_itself(size, dt, out_dt, spread):
     """Every dim has the value of one key only: its output is that key's weight, down to 2^-48 of
     the largest."""
-    run(size, 128, 64, [60, 300], dt, out_dt, 5, at=40, spread=spread, alone=True, seed=int(spread))
+    run(size, 128, 64, [100, 300], dt, out_dt, 5, at=40, spread=spread, alone="all", seed=int(spread))
+
+
+@BOTH
+@PAIRS
+@pytest.mark.parametrize("gap,spread", [(3, 0.5), (9, 0.5), (14, 1.5), (14, 4.0), (22, 0.5), (22, 1.5), (30, 0.5)])
+def test_each_small_weight_by_itself(size, dt, out_dt, gap, spread):
+    """The same, where no dim has a value of the keys that outweigh the others."""
+    run(size, 128, 64, [100, 300], dt, out_dt, gap, at=3, spread=spread, alone="small", seed=gap)
+    run(size, 64, 16, [70, 90], dt, out_dt, gap, at=30, spread=spread, alone="small", seed=gap, window=60)
 
 
 @pytest.mark.parametrize("dt,out_dt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
@@ -118,3 +129,10 @@ def test_long_caches(dt, out_dt, gap):
 def test_one_workgroup_of_eight_waves(dt):
     """Up to 512 keys: a step for each wave."""
     run(DECODE, 128, 64, [512, 300, 65], dt, dt, 14, seed=5)
+
+
+@pytest.mark.parametrize("out_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("gap,alone", [(14, ""), (22, "small")])
+def test_wide_prompts(out_dt, gap, alone):
+    """Enough bf16 columns for workgroups of 256."""
+    run((256, 256, 130, 0), 128, 64, [200], "bf16", out_dt, gap, at=3, alone=alone, seed=gap)
