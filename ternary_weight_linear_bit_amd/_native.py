@@ -696,10 +696,11 @@ _codes = {}
 
 def _code(dtype, name):
     """bitnet_dtype of an fp32 or bf16 tensor."""
-    if not _codes:
-        for d in _floats():
-            _codes[d] = _dtype_code(d)
-    code = _codes.get(dtype)
+    global _codes
+    codes = _codes
+    if not codes:   # made whole before another thread can see it
+        codes = _codes = {d: _dtype_code(d) for d in _floats()}
+    code = codes.get(dtype)
     if code is None:
         raise ValueError(f"{name}: expected {' or '.join(map(str, _floats()))}, got {dtype}")
     return code

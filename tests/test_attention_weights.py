@@ -167,7 +167,6 @@ def test_prompt_terms_hold_small_weights(terms, lift, held, up):
     small = p < 2.0 ** held
     assert np.all(np.abs(rest[~small]) <= 2.0 ** (-11 * terms) * p[~small])
     assert 64 * 127 * np.abs(rest[small]).max() <= 2.0 ** -12
-    lifted = (rest * F32(2.0 ** up)).astype(F32)
-    second, _ = split(lifted)
-    err = np.abs(first + second * 2.0 ** -up - p)
-    assert np.all(err[small] <= 2.0 ** (-11 * terms) * p[small])
+    second, _ = split((rest[small] * F32(2.0 ** up)).astype(F32))
+    err = np.abs(first[small] + second * 2.0 ** -up - p[small])
+    assert np.all(err <= 2.0 ** (-11 * terms) * p[small])

@@ -1,0 +1,34 @@
+"""The binding of the cache, attention and residual calls: threads, and arguments that contradict
+each other."""
+
+import threading
+
+import pytest
+import torch
+
+from ternary_weight_linear_bit_amd import _native as N
+
+
+def test_dtype_codes_are_seen_whole(monkeypatch):
+    """A thread that asks for a dtype's code while another is making the table gets it."""
+    real, half, go = N._dtype_code, threading.Event(), threading.Event()
+
+    def slow(dtype):
+        if threading.current_thread().name == "first" and dtype is torch.bfloat16:
+            half.set()
+            assert go.wait(20)
+        return real(dtype)
+    monkeypatch.setattr(N, "_codes", {})
+    monkeypatch.setattr(N, "_dtype_code", slow)
+    got = []
+    t = threading.Thread(target=lambda: got.append(N._code(torch.float32, "q")), name="first")
+    t.start()
+    try:
+        assert half.wait(20)
+        assert N._code(torch.bfloat16, "q") == N.BITNET_BF16
+    finally:
+        go.set()
+        t.join()
+    assert got == [N.BITNET_F32] and N._code(torch.float32, "q") == N.BITNET_F32
+    with pytest.raises(ValueError, match="q: expected"):
+        N._code(torch.float16, "q")
