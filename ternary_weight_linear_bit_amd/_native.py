@@ -894,8 +894,9 @@ def bitnet_attention_workspace_bytes(cache, batch, tokens, q_heads) -> int:
 def bitnet_attention(cache, batch, q, scale=None, window=0, out=None, out_dtype=None, lse=None,
                      workspace=None, stream=None):
     """Attention of queries q [T, q_heads, D] over the cache -> out [T, q_heads, D]
-    (q's dtype unless out_dtype).  scale: of the products (D**-0.5); window: keys a
-    row sees, itself included (0: all earlier ones); lse: optional fp32 [T, q_heads]."""
+    (q's dtype unless out_dtype or out says another; both must agree).  scale: of the
+    products (D**-0.5); window: keys a row sees, itself included (0: all earlier ones);
+    lse: optional fp32 [T, q_heads]."""
     import torch
     dim = cache.head_dim
     qs = _rows(q, None, dim, "q")
@@ -905,6 +906,8 @@ def bitnet_attention(cache, batch, q, scale=None, window=0, out=None, out_dtype=
     if out is not None:
         if out.dtype is not q.dtype:
             _expect(out, q.shape, _floats(), "out")
+        if out_dtype is not None and out_dtype is not out.dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
         _like(out, q.shape, out.dtype, "out")
     if lse is not None:
         _like(lse, (tokens, q_heads), torch.float32, "lse")

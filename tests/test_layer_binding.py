@@ -8,6 +8,8 @@ import torch
 
 from ternary_weight_linear_bit_amd import _native as N
 
+from test_layer_abi import a_batch, a_cache, cpu, z    # noqa: F401 (cpu: a fixture)
+
 
 def test_dtype_codes_are_seen_whole(monkeypatch):
     """A thread that asks for a dtype's code while another is making the table gets it."""
@@ -32,3 +34,12 @@ def test_dtype_codes_are_seen_whole(monkeypatch):
     assert got == [N.BITNET_F32] and N._code(torch.float32, "q") == N.BITNET_F32
     with pytest.raises(ValueError, match="q: expected"):
         N._code(torch.float16, "q")
+
+
+def test_out_dtype_that_contradicts_out(cpu):   # noqa: F811
+    q = z(4, 4, 32)
+    for out, dtype in ((z(4, 4, 32), torch.bfloat16), (z(4, 4, 32, dtype=torch.bfloat16), torch.float32)):
+        with pytest.raises(ValueError, match="out_dtype"):
+            cpu.bitnet_attention(a_cache(cpu), a_batch(cpu), q, out=out, out_dtype=dtype)
+        with pytest.raises(AssertionError, match="reached the C library"):      # the same one is fine
+            cpu.bitnet_attention(a_cache(cpu), a_batch(cpu), q, out=out, out_dtype=out.dtype)
