@@ -1,6 +1,8 @@
 """The binding of the cache, attention and residual calls: threads, and arguments that contradict
 each other."""
 
+import ctypes
+import os
 import threading
 
 import pytest
@@ -8,7 +10,7 @@ import torch
 
 from ternary_weight_linear_bit_amd import _native as N
 
-from test_layer_abi import a_batch, a_cache, cpu, z    # noqa: F401 (cpu: a fixture)
+from test_layer_abi import A, EALIGN, EWS, a_batch, a_cache, attend, batch, cpu, kv, z  # noqa: F401
 
 
 def test_dtype_codes_are_seen_whole(monkeypatch):
@@ -43,3 +45,21 @@ def test_out_dtype_that_contradicts_out(cpu):   # noqa: F811
             cpu.bitnet_attention(a_cache(cpu), a_batch(cpu), q, out=out, out_dtype=dtype)
         with pytest.raises(AssertionError, match="reached the C library"):      # the same one is fine
             cpu.bitnet_attention(a_cache(cpu), a_batch(cpu), q, out=out, out_dtype=out.dtype)
+
+
+@pytest.mark.parametrize("shape", [
+    dict(seqs=1, width=4096, tokens=1, max_new=1, max_len=200000),          # a token over a long cache
+    dict(seqs=1, width=4096, tokens=200, max_new=200, max_len=200000)],     # a prompt's part over it
+    ids=["decode", "prompt"])
+def test_workspaces_that_do_not_suffice(shape):
+    """Both kernels split the keys of such a call: none, a byte less and a misaligned workspace are
+    refused before anything is launched."""
+    if not os.path.exists(N.LIB_PATH):
+        pytest.skip("libbitnet_mi355x.so not built")
+    lib = N.lib()
+    c, b = kv(), batch(**shape)
+    need = lib.bitnet_attention_workspace_bytes(ctypes.byref(kv(k=None, v=None)), ctypes.byref(b), 4)
+    assert need > 0 and need % ((128 + 4) * 4) == 0      # columns of head_dim + 4 floats
+    assert attend(lib, c, b, ws=None) == EWS
+    assert attend(lib, c, b, ws_bytes=need - 1) == EWS
+    assert attend(lib, c, b, ws=A + 4, ws_bytes=need) == EALIGN
