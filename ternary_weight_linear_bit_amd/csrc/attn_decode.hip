@@ -278,7 +278,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
       }
     mx = rows_max(mx);
     m = fmaxf(m, mx);
-    const float rest = ceilf(m) - kReach;   // weights below 2^rest may be lost
+    const float rest = ceilf(m) - (kReach + 1.0f);   // weights below 2^rest may be lost
     const float to = mx == -INFINITY ? r : fmaxf(ceilf(mx), rest) - kLift;
     const float alpha = power_of_2(r - to), floor = fmaxf(power_of_2(rest - to), 0x1p-126f);
     r = to;
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(64 * NW, DP <= 128 ? 2 : 1) void attn_decode_kernel
       }
     };
     pass(std::true_type{});
-    const float least = __uint_as_float(low) + floor;   // at least 2^-34 of the reference
+    const float least = __uint_as_float(low) + floor;   // at least 2^-35 of the reference
     while (__builtin_amdgcn_ballot_w64(least < unit * (1 << (B - 1)))) {
       unit *= kPass;
       pass(std::false_type{});

@@ -50,12 +50,12 @@ def by_steps(q, kc, vc, dk, dv, scale, bits):
             xs, vs = x[at:at + STEP], vc[at:at + STEP].astype(np.int64)
             mx = xs.max()
             m = max(m, mx)
-            to = max(np.ceil(mx), np.ceil(m) - 48) - F32(LIFT)
+            to = max(np.ceil(mx), np.ceil(m) - 49) - F32(LIFT)
             alpha = F32(2.0 ** float(np.clip(r - to, -200, 126)))
             r = to
             p = np.exp2(xs - to).astype(F32)
             l = F32(l * alpha + F32(p.sum(dtype=F32) * (F32(1) / dv)))
-            floor = F32(2.0 ** float(np.ceil(m) - 48 - r))
+            floor = F32(2.0 ** float(np.ceil(m) - 49 - r))
             low = p[p >= floor].min()
             y, unit, o = p, F32(1), (o * alpha).astype(F32)
             while True:

@@ -136,3 +136,14 @@ def test_one_workgroup_of_eight_waves(dt):
 def test_wide_prompts(out_dt, gap, alone):
     """Enough bf16 columns for workgroups of 256."""
     run((256, 256, 130, 0), 128, 64, [200], "bf16", out_dt, gap, at=3, alone=alone, seed=gap)
+
+
+@pytest.mark.parametrize("size,dim,page,lens,dt,out_dt,at,value,spread,alone,seed", [
+    ((2, 2, 1, 4096), 192, 16, [2362, 84], "f32", "f32", -3, (False,), 2, "small", 324073),
+    ((2, 8, 1, 0), 256, 16, [323, 91], "bf16", "f32", 0, (True,), 8, "all", 308241),
+    ((1, 7, 1, 0), 96, 64, [1286, 558, 141], "f32", "bf16", 0, (False, True), 4, "all", 483414),
+    ((1, 1, 5, 0), 160, 32, [1377, 657], "bf16", "f32", 0, (True,), 2, "all", 898264)])
+def test_smallest_weights_that_count(monkeypatch, size, dim, page, lens, dt, out_dt, at, value, spread, alone, seed):
+    """Outputs that are weights just above 2^-48 of the row's largest."""
+    monkeypatch.setattr(f"{__name__}.DECODE", size)
+    run(size, dim, page, lens, dt, out_dt, 30, at=at, value=value, spread=spread, alone=alone, seed=seed)
