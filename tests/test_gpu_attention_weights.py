@@ -30,7 +30,7 @@ def _gpu():
 
 
 def run(size, dim, page, lens, dt, out_dt, gap, at=0, value=(False, True), spread=1.0, alone="", window=0,
-        seed=0, rows=None):
+        seed=0, rows=None, holes=0.0):
     heads, q_heads, new, least = size
     new = rows or new
     rng = np.random.default_rng(500 + seed)
@@ -46,6 +46,8 @@ def run(size, dim, page, lens, dt, out_dt, gap, at=0, value=(False, True), sprea
         vs.append(np.empty_like(v))
         ks[-1][table[b, :len(k)] - first], vs[-1][table[b, :len(k)] - first] = k, v
         first += len(k)
+    if holes:                                             # pages that are not there
+        table[rng.random(table.shape) < holes] = 1 << 20
     k, v = np.concatenate(ks), np.concatenate(vs)
     dk, dv, scale = made[0][3:]
     dks, dvs = np.full((first, heads), dk, F32), np.full((first, heads), dv, F32)
@@ -61,6 +63,9 @@ def run(size, dim, page, lens, dt, out_dt, gap, at=0, value=(False, True), sprea
     got, gl = host(out.float()), host(lse)
     want, wl, *detail = L.attention(k, v, dks, dvs, table, q_start, kv_len, qf, scale, window, new, max_len,
                                     detail=True)
+    none = np.isneginf(wl)                                # rows whose keys are all missing
+    assert np.all(got[none] == 0) and np.array_equal(np.isneginf(gl), none)
+    wl, gl = np.where(none, 0, wl), np.where(none, 0, gl)
     keys = np.repeat(kv_len, new)[:, None].astype(np.float64)
     tol, tol_l = weight_bounds(want, wl, *detail, qf, keys, dt == "f32" and out_dt == "f32", out_dt == "bf16",
                                steps=0 if size is DECODE else keys / 64 + 1)
@@ -147,3 +152,44 @@ def test_smallest_weights_that_count(monkeypatch, size, dim, page, lens, dt, out
     """Outputs that are weights just above 2^-48 of the row's largest."""
     monkeypatch.setattr(f"{__name__}.DECODE", size)
     run(size, dim, page, lens, dt, out_dt, 30, at=at, value=value, spread=spread, alone=alone, seed=seed)
+
+
+@BOTH
+@pytest.mark.parametrize("dt,out_dt", [("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("gap,alone", [(12, ""), (22, "small")])
+def test_missing_pages(size, dt, out_dt, gap, alone):
+    """Pages that are not there among those with the keys that count, and rows left with none."""
+    run(size, 64, 16, [90, 700], dt, out_dt, gap, at=20, alone=alone, holes=0.3, seed=gap)
+    run(size, 128, 64, [64, 300], dt, out_dt, gap, at=70, alone=alone, holes=0.5, seed=gap + 4, window=90)
+
+
+@pytest.mark.parametrize("size", [DECODE, PROMPT], ids=["decode", "prompt"])
+def test_captured_beside_eager_calls(size):
+    """A graph replayed over rows with and without a dominant key, eager calls in between."""
+    heads, q_heads, new, least = size
+    rng = np.random.default_rng(1)
+    made = [peaked(rng, new, q_heads, heads, 64, 400, gap, 9, (False, True)) for gap in (0, 13, 22)]
+    pages = [paged(m[1], m[2], 16) for m in made]
+    n, width = 25, max(25, least // 16)
+    table = np.full((1, width), -1, np.int32)
+    table[0, :n] = rng.permutation(n)
+    scales = np.full((n, heads), made[0][3], F32), np.full((n, heads), made[0][4], F32)
+    c = N.KVCache(torch.empty((n, heads, 16, 64), dtype=torch.int8, device=DEV),
+                  torch.empty((n, heads, 64, 16), dtype=torch.int8, device=DEV), dev(scales[0]), dev(scales[1]))
+    b = N.KVBatch(dev(table), dev(np.array([0, new], np.int32)), dev(np.array([400], np.int32)), new, width * 16)
+    q = torch.zeros((new, q_heads, 64), dtype=torch.bfloat16, device=DEV)
+    scale = float(made[0][5])
+
+    def fill(i):
+        at = torch.from_numpy(table[0, :n].astype(np.int64)).to(DEV)
+        c.k[at], c.v[at] = dev(pages[i][0]), dev(pages[i][1])
+        q.copy_(dev(made[i][0]))
+    fill(0)
+    N.bitnet_attention(c, b, q, scale=scale)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = N.bitnet_attention(c, b, q, scale=scale)
+    for i in (1, 0, 2, 1, 2):
+        fill(i)
+        g.replay()
+        assert torch.equal(out, N.bitnet_attention(c, b, q, scale=scale)) and bool(out.any())
