@@ -462,7 +462,8 @@ bitnet_status bitnet_chain_error(const bitnet_chain *chain, int *error);
  *   kv_heads  1 to 65535; pages 1 to 2^31 - 1 (the arrays may pass 4 GiB).
  *   k, v      16-byte aligned; the scales 4-byte aligned.
  * Memory of pages that were never written may hold anything; scales of pages that are
- * read must be positive (bitnet_kv_append writes no others for finite rows).
+ * read must be positive, those of values 2^-40 or more (bitnet_kv_append writes none below
+ * 2^-24 for finite rows).
  */
 typedef struct bitnet_kv_cache {
   int8_t *k;       /* [pages][kv_heads][page][head_dim] */

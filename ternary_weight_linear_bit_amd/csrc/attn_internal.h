@@ -8,8 +8,9 @@ namespace bitnet {
 
 constexpr int kAttnStep = 64;   // keys of one step
 // Weights e^(s - m) dv below 2^-kReach of their row's largest may count as 0 in the output: a
-// row's sums then stay in fp32's range whatever they are taken over, and 2^24 such weights are
-// less than half of fp32's last bit of the row's.
+// row's sums (the softmax sum divides by dv, 2^-40 or more) then stay in fp32's range whatever
+// step's reference they are taken over, and 2^24 such weights are less than half of fp32's last
+// bit of the row's.
 constexpr float kReach = 48.0f;
 
 // Columns [c0, c0 + nc) of a sequence's (row, query head of the group) pairs, rows

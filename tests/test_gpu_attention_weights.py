@@ -193,3 +193,17 @@ def test_captured_beside_eager_calls(size):
         fill(i)
         g.replay()
         assert torch.equal(out, N.bitnet_attention(c, b, q, scale=scale)) and bool(out.any())
+
+
+@BOTH
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_least_value_scales(monkeypatch, size, dt):
+    """Values of scale 2^-40 beside a dominant key: neither sum leaves fp32's range."""
+    real = peaked
+
+    def tiny(*a, **kw):
+        q, kc, vc, dk, _, scale = real(*a, **kw)
+        return q, kc, vc, dk, F32(2.0 ** -40), scale
+    monkeypatch.setattr(f"{__name__}.peaked", tiny)
+    for gap in (0, 22, 40):
+        run(size, 64, 16, [300, 1500], dt, "f32", gap, seed=gap)
