@@ -97,11 +97,12 @@ int join_cols(const KvCache& c, const AttnPlan& p, int ways) {
 
 // Whether a call takes the prompt kernel.  cols: rows x query heads of a kv head.  Its
 // workgroups of 128 columns have to fill half of the chip (us, decode and prompt kernel, 32
-// heads on 8, bf16: one prompt of 256 tokens 10.4 and 15.2, of 512 23.9 and 21.2, of 1024
-// 50.8 and 48.2; 256 rows behind 3840 tokens 52 and 63, 512 behind 3584 94 and 68).  From 48
+// heads on 8, bf16: one prompt of 256 tokens 11.2 and 15.8, of 512 26.9 and 21.8, of 1024
+// 61 and 50; 256 rows behind 3840 tokens 62 and 64, 512 behind 3584 109 and 70).  From 48
 // columns on it is also taken where the cache passes the L2s, since the decode kernel reads
-// it for every 16 columns (8 sequences of 4096 tokens, 12 rows each: 47 and 36; 64 heads
-// of their own, 64 rows behind 4032: 52 and 39).
+// it for every 16 columns (12 rows a sequence, 8 sequences of 8192 tokens: 85 and 69, 16 of
+// them: 135 and 92; 8 of 4096: 51 and 53; 64 rows of one of 32768: 113 and 106, 32 rows of
+// one of 65536: 121 and 139; 4 rows of 16 of 8192: 50 and 75).
 bool many_rows(const KvCache& c, const KvBatch& b, int q_heads) {
   const int64_t pairs = (int64_t)b.seqs * c.kv_heads;
   const int64_t cols = (int64_t)b.max_new * (q_heads / c.kv_heads);

@@ -12,7 +12,7 @@
 // Bound by memory: every visible code is read once (64 sequences of 1 .. 8191 tokens, 32
 // heads on 8, 128 dims: 137 us, 4.3 TB/s; four of 65536, fp32: 108 us, 4.8 TB/s; a large
 // copy reaches 4.75).  Small calls are bound by one step's latency and two launches (one
-// sequence of 2049 tokens: 10.8 us).  Non-temporal loads were 7-10% slower.  The codes go from
+// sequence of 2049 tokens: 11.8 us).  Non-temporal loads were 7-10% slower.  The codes go from
 // memory to the int8 matrix cores as they are, with no conversion and no LDS: it is the other
 // operand that is turned into 8-bit digits, a query row (once) and the weights of a step (16 a
 // lane), each digit with its own product; the int32 sums are exact.
@@ -22,10 +22,11 @@
 //   * Weights: 2^14 of them is the power of two above the step's largest, and a pass takes two
 //     digits of what the passes before left, 15 more bits each, until every weight of the
 //     wave's step is within 2^-11 of itself (2^-22 with fp32 in and out) or below 2^-48 of the
-//     row's largest.  Two passes are common (three in fp32); each further one costs 5% where
-//     sequences are uneven and nothing where memory is busy.  A fixed point against the row's
-//     largest weight, in one pass, ran 64 sequences in 131 us and lost what is 2^-16 of it: of
-//     a row whose first key has 95% of the weight, and no value, a third of the output.
+//     row's largest.  Two passes are common (three in fp32).  A fixed point against the row's
+//     largest weight, in one pass, ran 64 sequences in 131 us, and 256 rows behind 3840 tokens
+//     (16 columns a workgroup, bound by vector instructions) in 53 instead of 62, and lost what
+//     is 2^-16 of it: of a row whose first key has 95% of the weight, and no value, a third of
+//     the output.
 // Converting the codes to 16-bit floats instead would take 320 vector instructions
 // a lane and step of 64 keys, the digits of a pass take about 50.
 //
@@ -428,11 +429,11 @@ constexpr int64_t kOneLaunch = kManyWaves;   // steps up to which no keys are sp
 }  // namespace
 
 // Two workgroups per compute unit; no part is shorter than one step a wave.  (Four
-// times as many for batches of uneven lengths: 64 sequences of 1 .. 8191 tokens 131 ->
-// 130 us, but four of 65536 115 -> 175 us: a part's start and end cost about as much as
+// times as many: 64 sequences of uneven lengths up to 8129 tokens 120 -> 112 us, but 63 of
+// 4096 103 -> 112 and four of 65536 112 -> 122: a part's start and end cost about as much as
 // four steps.)  Up to eight steps, eight waves a workgroup take them at one step a wave in
-// one launch (300 tokens of 20 heads 9.2 -> 8.4 us with the join; at two steps a wave
-// 9.5 -> 10.2).
+// one launch (300 tokens of 20 heads, in a graph, 10.5 -> 9.8 us with the join; 1000 tokens at
+// two steps a wave 10.8 -> 14.3).
 AttnPlan attn_decode_plan(const KvCache& c, const KvBatch& b, int q_heads) {
   AttnPlan p = attn_plan(c, b, q_heads, kCols, 512, kWaves);
   p.waves = kWaves;

@@ -3,8 +3,9 @@
 // attn_decode.hip.
 //
 // Bound by the vector and matrix instructions together: 8192 tokens of 32 heads on 8, 128
-// dims, bf16, take 590-603 us (912-932 TFLOP/s; a library product of bf16 matrices reaches
-// 1208 on this card), with vector instructions in 55% of the cycles and matrix ones in 40%.
+// dims, bf16, take 590-628 us, box to box (875-932 TFLOP/s; a library product of bf16 matrices
+// reaches 1208 on this card), with vector instructions in 56% of the cycles and matrix ones
+// in 40%.
 // Random data draw the clock down: zeros run 17% faster.  Staging a step deeper behind half
 // the barriers, raised wave priority around the products, issue-order hints, values read a
 // group ahead and the two key tiles' products in turn all measured within 2%.
@@ -559,7 +560,7 @@ hipError_t launch_attn_prompt(const KvCache& c, const KvBatch& b, const AttnArgs
   float* part = static_cast<float*>(workspace);
   const int dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
   // Eight waves share a step's conversion between 256 columns: bf16 queries of 65 to 128
-  // dims with a workgroup for every compute unit (8192 tokens of 32 heads: 604 -> 576 us).
+  // dims with a workgroup for every compute unit (8192 tokens of 32 heads: 627 -> 599 us).
   // Fewer take four waves, whose workgroups are twice as many (and split the keys).
   const bool wide = dp == 128 && q_bf16 && tiles_of(c, b, a.q_heads, kWideCols) >= 256;
   if (wide) {
