@@ -613,6 +613,124 @@ typedef struct bitnet_residual {
 
 bitnet_status bitnet_residual_norm(const bitnet_residual *args, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * A feed-forward of experts: each token goes through the few of many ternary
+ * matrices that its router chose.  route -> expert_linear (gate and up, with the
+ * activation between them) -> bitnet_quantize_acts -> expert_linear (down, by slot)
+ * -> combine.  (The pages describe dense layers; the products and their rescale are
+ * theirs: dashen-tech, section 3.1.)
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Which rows belong to which expert (device memory, caller-owned).  Pair p = m * topk + j
+ * is choice j of token m; the pairs that have an expert are numbered by expert, then by pair,
+ * and that number is the pair's slot: expert e has the slots [offset[e], offset[e + 1]).
+ *   tokens >= 0, topk 1 to 32, experts 1 to 1024, tokens * topk <= 2^30.
+ *   expert  [tokens][topk] expert of each pair; a number outside 0 .. experts - 1 (-1 where
+ *           bitnet_route found none) is a pair without expert or slot.
+ *   weight  [tokens][topk] fp32.
+ *   offset  [experts + 1]; pair [tokens * topk] pair of each slot, -1 behind the last one;
+ *   slot    [tokens][topk] slot of each pair, -1 for none.
+ * The calls that read a routing do not trust its contents: offsets are clamped to the pairs, and
+ * a slot whose pair, or a pair whose slot, is out of range is left out.
+ */
+typedef struct bitnet_routing {
+  int32_t *expert;
+  float *weight;
+  int32_t *offset, *pair, *slot;
+  int64_t tokens;
+  int topk, experts;
+} bitnet_routing;
+
+/* How bitnet_route weighs a chosen logit x: its softmax among all experts' logits, among the
+ * chosen ones, or 1 / (1 + e^-x). */
+typedef enum bitnet_score { BITNET_SOFTMAX = 0, BITNET_CHOSEN = 1, BITNET_SIGMOID = 2 } bitnet_score;
+
+/*
+ * Each token's topk largest logits, their weights, and the plan of the pairs; fills all arrays of
+ * `routing`.  With logits == NULL `expert` is an input (and `weight` is not touched): the plan alone.
+ *   logits  [tokens] rows of [experts], fp32 or bf16 (dtype, element-aligned), `stride` elements
+ *           apart (>= experts).  Chosen in order of size, ties lowest index first (-0 is 0);
+ *           -inf and NaN are never chosen, and where fewer than topk are left the rest have
+ *           expert -1 and weight 0.
+ *   score, scale   weight = scale * the score, in fp32 (scale finite).  Logits that equal the row's
+ *           largest count e^0, +inf too.
+ *   workspace  bitnet_route_workspace_bytes() bytes, 4-byte aligned; clobbered; calls that overlap
+ *           need one each.  NULL when the size is 0.
+ * Indices are exact, and the same call gives the same bits.
+ */
+bitnet_status bitnet_route(const bitnet_routing *routing, const void *logits, int dtype,
+                           int64_t stride, int score, float scale, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace of bitnet_route for these sizes; 0 for sizes that it refuses. */
+size_t bitnet_route_workspace_bytes(int64_t tokens, int topk, int experts);
+
+/* Activations: none, max(v, 0)^2, v / (1 + e^-v), v * Phi(v) (Phi the standard normal
+ * distribution function). */
+typedef enum bitnet_act {
+  BITNET_ACT_NONE = 0,
+  BITNET_ACT_RELU2 = 1,
+  BITNET_ACT_SILU = 2,
+  BITNET_ACT_GELU = 3
+} bitnet_act;
+
+/*
+ * A ternary product and what follows it:
+ *   v = RN32(float(acc) * RN32(gamma* * d)), acc as in bitnet_ternary_linear;
+ *   v = RN32(v + bias) where there is one;  a = act(v);
+ *   a = RN32(a * u) where there is a second matrix `up`, u as v of it (its own bias);
+ *   a = RN32(a + residual) where there is one;  y = a rounded to y_dtype.
+ * Bit-exact against that definition, but for silu, within 2^-20 of its value, and gelu, within 2^-20
+ * of its value and 2^-24 of |v| together.
+ *   w, up    matrices of [N][K] in the prefill layout (bitnet_repack_prefill), 16-byte aligned;
+ *            up may be NULL.  Experts' matrices lie one behind the other,
+ *            bitnet_prefill_layout_bytes(N, K) bytes each.
+ *   w_scale, up_scale   gamma* [1], of experts [experts].
+ *   bias, up_bias       NULL or fp32 [N], of experts [experts][N].
+ *   x_q, x_scale        [rows][K] int8, 16-byte aligned, and [rows].
+ *   residual  NULL or [rows][N] of y's type; y may be it.
+ *   y         [rows][N] fp32 or bf16, element-aligned; for experts a row for each slot.
+ *   rows      0 to 2^30;  N >= 0;  K % 64 == 0, 64 to BITNET_MAX_K;  N * K < BITNET_MAX_WEIGHTS.
+ *   act       bitnet_act.
+ */
+typedef struct bitnet_product {
+  const uint8_t *w, *up;
+  const float *w_scale, *up_scale;
+  const float *bias, *up_bias;
+  const int8_t *x_q;
+  const float *x_scale;
+  const void *residual;
+  void *y;
+  int64_t rows, N, K;
+  int act, y_dtype;
+} bitnet_product;
+
+/* The product of one matrix (or gate and up) with all rows. */
+bitnet_status bitnet_ternary_linear_act(const bitnet_product *product, hipStream_t stream);
+
+/*
+ * The products of each expert with its slots: y[s] for slot s of expert e is the product of
+ * matrix e with the slot's input row.
+ *   by_slot  0: input row pair[s] / topk (x_q has routing->tokens rows, tokens * K < 2^32);
+ *            1: input row s (x_q has tokens * topk rows).  product->rows has to say the same.
+ *   product  as above, without residual.  Rows of y behind the last slot are left as they are.
+ * Of the routing offset and pair are read (pair with by_slot 0).
+ */
+bitnet_status bitnet_expert_linear(const bitnet_routing *routing, const bitnet_product *product,
+                                   int by_slot, hipStream_t stream);
+
+/*
+ * out[m] = residual[m] + sum over j of weight[m][j] * y[slot[m][j]], j ascending, products and sums
+ * each rounded to fp32 (from 0 without residual), out rounded to its type; pairs without a slot are
+ * left out.  Bit-exact against that definition.
+ *   y         [tokens * topk][K] fp32 or bf16 (y_dtype), element-aligned.
+ *   residual  NULL or [tokens][K] of out's type; out may be it.
+ *   out       [tokens][K] fp32 or bf16 (out_dtype), element-aligned.  K >= 0, K < 2^31.
+ */
+bitnet_status bitnet_combine(const bitnet_routing *routing, const void *y, int y_dtype, int64_t K,
+                             const void *residual, void *out, int out_dtype, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

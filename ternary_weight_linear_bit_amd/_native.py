@@ -988,3 +988,250 @@ def bitnet_residual_norm(y, h, h_out=None, post_weight=None, gate=None, scale=1.
     if status:
         raise BitnetError("bitnet_residual_norm", status)
     return h_out, x_q, x_scale
+
+
+# ---------------------------------------------------------------------------
+# a feed-forward of experts: routing, grouped products, combination
+# ---------------------------------------------------------------------------
+
+class BitnetRouting(ctypes.Structure):
+    """struct bitnet_routing of the public header."""
+    _fields_ = [("expert", _P), ("weight", _P), ("offset", _P), ("pair", _P), ("slot", _P),
+                ("tokens", _I64), ("topk", _I), ("experts", _I)]
+
+
+class BitnetProduct(ctypes.Structure):
+    """struct bitnet_product of the public header."""
+    _fields_ = [("w", _P), ("up", _P), ("w_scale", _P), ("up_scale", _P), ("bias", _P), ("up_bias", _P),
+                ("x_q", _P), ("x_scale", _P), ("residual", _P), ("y", _P), ("rows", _I64), ("N", _I64),
+                ("K", _I64), ("act", _I), ("y_dtype", _I)]
+
+
+SIGNATURES["bitnet_route"] = (_I, [ctypes.POINTER(BitnetRouting), _P, _I, _I64, _I, ctypes.c_float, _P,
+                                   _SZ, _P])
+SIGNATURES["bitnet_route_workspace_bytes"] = (_SZ, [_I64, _I, _I])
+SIGNATURES["bitnet_ternary_linear_act"] = (_I, [_P, _P])
+SIGNATURES["bitnet_expert_linear"] = (_I, [ctypes.POINTER(BitnetRouting), _P, _I, _P])
+SIGNATURES["bitnet_combine"] = (_I, [ctypes.POINTER(BitnetRouting), _P, _I, _I64, _P, _P, _I, _P])
+
+_PRODUCT = struct.Struct("@PPPPPPPPPPqqqii")    # struct bitnet_product as a byte string
+SCORES = {"softmax": 0, "chosen": 1, "sigmoid": 2}
+ACTS = {"none": 0, "relu2": 1, "silu": 2, "gelu": 3}
+
+
+def _named(value, table, name):
+    code = table.get(value)
+    if code is None:
+        raise ValueError(f"{name}: expected one of {', '.join(table)}, got {value!r}")
+    return code
+
+
+class Routing(_Fixed):
+    """Which rows belong to which expert: int32 expert [tokens, topk], fp32 weight [tokens,
+    topk], int32 offset [experts + 1], pair [tokens * topk], slot [tokens, topk].  Holds the
+    tensors and the C struct; sizes are fixed, contents are bitnet_route's or the caller's."""
+
+    def __init__(self, expert, weight, offset, pair, slot):
+        import torch
+        if expert.dim() != 2 or offset.dim() != 1 or offset.shape[0] < 2:
+            raise ValueError("expert must be [tokens, topk] and offset [experts + 1]")
+        tokens, topk = expert.shape
+        _expect(expert, (tokens, topk), torch.int32, "expert")
+        _expect(weight, (tokens, topk), torch.float32, "weight")
+        _expect(offset, (offset.shape[0],), torch.int32, "offset")
+        _expect(pair, (tokens * topk,), torch.int32, "pair")
+        _expect(slot, (tokens, topk), torch.int32, "slot")
+        if topk < 1:
+            raise ValueError("topk must be at least 1")
+        self.device = _one_device(expert, weight, offset, pair, slot)
+        self.expert, self.weight, self.offset, self.pair, self.slot = expert, weight, offset, pair, slot
+        self.tokens, self.topk, self.experts = tokens, topk, offset.shape[0] - 1
+        self.handle = BitnetRouting(expert.data_ptr(), weight.data_ptr(), offset.data_ptr(), pair.data_ptr(),
+                                    slot.data_ptr(), tokens, topk, self.experts)
+        self.ref = ctypes.byref(self.handle)
+
+    @staticmethod
+    def empty(tokens, topk, experts, device="cuda"):
+        """A routing with uninitialised arrays, for bitnet_route to fill."""
+        import torch
+
+        def ints(*shape):
+            return torch.empty(shape, dtype=torch.int32, device=device)
+        return Routing(ints(tokens, topk), torch.empty((tokens, topk), dtype=torch.float32, device=device),
+                       ints(experts + 1), ints(tokens * topk), ints(tokens, topk))
+
+
+class TernaryExperts(_Fixed):
+    """Ternary matrices of equal size, one an expert: uint8 w [experts, *prefill_layout_shape(N, K)]
+    and fp32 scale [experts].  The tensors are kept as they are."""
+
+    def __init__(self, w, scale, n, k):
+        import torch
+        if scale.dim() != 1 or scale.shape[0] < 1:
+            raise ValueError("scale must be [experts]")
+        _expect(w, (scale.shape[0], *prefill_layout_shape(n, k)), torch.uint8, "w")
+        _expect(scale, (scale.shape[0],), torch.float32, "scale")
+        self.device = _one_device(w, scale)
+        self.w, self.scale, self.experts, self.n, self.k = w, scale, scale.shape[0], n, k
+
+    @staticmethod
+    def from_packed(packed, scale, stream=None):
+        """From 2-bit packed matrices [experts, N, K/4] (bitnet_quantize_weights)."""
+        import torch
+        if packed.dim() != 3:
+            raise ValueError("packed must be [experts, N, K/4]")
+        e, n, kb = packed.shape
+        w = torch.empty((e, *prefill_layout_shape(n, 4 * kb)), dtype=torch.uint8, device=packed.device)
+        for i in range(e):
+            bitnet_repack_prefill(packed[i], w[i], stream)
+        return TernaryExperts(w, scale, n, 4 * kb)
+
+
+def bitnet_route_workspace_bytes(tokens, topk, experts) -> int:
+    """Workspace of bitnet_route for these sizes."""
+    return lib().bitnet_route_workspace_bytes(tokens, topk, experts)
+
+
+def bitnet_route(routing, logits=None, score="softmax", scale=1.0, workspace=None, stream=None):
+    """Fills `routing` from router logits [tokens, experts] (fp32 or bf16, any distance between
+    rows): the topk largest of each token, their weights, and the pairs sorted by expert.
+    score: "softmax" (over all experts), "chosen" (over the chosen ones) or "sigmoid".
+    logits=None: routing.expert is given, and only the pairs are sorted.  Returns routing."""
+    import torch
+    code, ptr, dt, stride = _named(score, SCORES, "score"), 0, 0, 0
+    if logits is not None:
+        if logits.shape != (routing.tokens, routing.experts):
+            raise ValueError(f"logits: expected {(routing.tokens, routing.experts)}, got {tuple(logits.shape)}")
+        dt, ptr = _code(logits.dtype, "logits"), logits.data_ptr()
+        st = logits.stride()
+        if (routing.experts > 1 and st[1] != 1) or (routing.tokens > 1 and st[0] < routing.experts):
+            raise ValueError("logits: a token's experts must lie one after another")
+        stride = st[0] if routing.tokens > 1 else routing.experts
+    if workspace is not None:
+        _need_cuda(workspace)
+    device = _one_device(routing.expert, logits, workspace)
+    with _On(device, stream) as s:
+        l = lib()
+        have = wp = 0
+        if workspace is None:
+            have = l.bitnet_route_workspace_bytes(routing.tokens, routing.topk, routing.experts)
+            if have:
+                workspace = torch.empty(have, dtype=torch.uint8, device=device)
+        else:
+            have = workspace.numel() * workspace.element_size()
+        if have:
+            wp = workspace.data_ptr()
+        # (an empty tensor has no address: its plan is that of no tokens)
+        status = l.bitnet_route(routing.ref, ptr, dt, stride, code, scale, wp, have, s)
+    if status:
+        raise BitnetError("bitnet_route", status)
+    return routing
+
+
+def _product(name, w, w_scale, n, k, rows, x_q, x_scale, up, bias, up_bias, act, residual, y, y_dtype, experts, stream,
+             call):
+    """Checks a product's operands, makes y where none is given and calls with the C struct."""
+    import torch
+    f32, many = torch.float32, () if experts is None else (experts,)
+    code = _named(act, ACTS, "act")
+    up_w = up_scale = None
+    if up is not None:
+        up_w, up_scale = up
+    elif up_bias is not None:
+        raise ValueError("up_bias without up")
+    for t, what in ((bias, "bias"), (up_bias, "up_bias")):
+        if t is not None:
+            _like(t, (*many, n), f32, what)
+    if x_q.dim() != 2 or x_q.shape[1] != k:
+        raise ValueError(f"x_q: expected [rows, {k}], got {tuple(x_q.shape)}")
+    _like(x_q, x_q.shape, torch.int8, "x_q")
+    _like(x_scale, x_q.shape[:1], f32, "x_scale")
+    if y is not None:
+        if y_dtype is not None and y_dtype is not y.dtype:
+            raise ValueError(f"y is {y.dtype}, y_dtype {y_dtype}")
+        y_dtype = y.dtype
+        _like(y, (rows, n), y_dtype, "y")
+    y_dtype = y_dtype or (f32 if residual is None else residual.dtype)
+    dt = _code(y_dtype, "y")
+    if residual is not None:
+        _like(residual, (rows, n), y_dtype, "residual")
+    device = _one_device(w, w_scale, up_w, up_scale, bias, up_bias, x_q, x_scale, residual, y)
+    with _On(device, stream) as s:
+        if y is None:
+            y = torch.empty((rows, n), dtype=y_dtype, device=device)
+        args = _PRODUCT.pack(w.data_ptr(), 0 if up is None else up_w.data_ptr(), w_scale.data_ptr(),
+                             0 if up is None else up_scale.data_ptr(), 0 if bias is None else bias.data_ptr(),
+                             0 if up_bias is None else up_bias.data_ptr(), x_q.data_ptr(), x_scale.data_ptr(),
+                             0 if residual is None else residual.data_ptr(), y.data_ptr(), x_q.shape[0], n, k, code, dt)
+        status = call(args, s)
+    if status:
+        raise BitnetError(name, status)
+    return y
+
+
+def bitnet_ternary_linear_act(w_prefill, w_scale, n, x_q, x_scale, up=None, bias=None, up_bias=None, act="none",
+                              residual=None, y=None, y_dtype=None, stream=None):
+    """y = act(x W^T + bias) [* (x U^T + up_bias)] [+ residual] of int8 x_q [M, K]: w_prefill in the
+    prefill layout (prefill_layout_shape(N, K)) with scale [1], up: (matrix, scale) of the same
+    shape, biases fp32 [N], residual [M, N] of y's dtype (y may be it).  act: "none", "relu2",
+    "silu" or "gelu"."""
+    import torch
+    if x_q.dim() != 2:
+        raise ValueError("x_q must be 2-D [M, K]")
+    m, k = x_q.shape
+    for t, what in (((w_prefill, w_scale), "w"), *(() if up is None else ((up, "up"),))):
+        _like(t[0], prefill_layout_shape(n, k), torch.uint8, what)
+        _check_scale(t[1])
+    return _product("bitnet_ternary_linear_act", w_prefill, w_scale, n, k, m, x_q, x_scale, up, bias, up_bias, act,
+                    residual, y, y_dtype, None, stream, lib().bitnet_ternary_linear_act)
+
+
+def bitnet_expert_linear(routing, w, x_q, x_scale, slots=False, up=None, bias=None, up_bias=None, act="none",
+                         y=None, y_dtype=None, stream=None):
+    """Each expert's product with its rows: y [tokens * topk, N], row s for slot s of the routing
+    (rows behind the last slot are left as they are).  w, up: TernaryExperts; x_q: [tokens, K], or
+    with slots=True [tokens * topk, K], a row for each slot; biases fp32 [experts, N]; act as in
+    bitnet_ternary_linear_act."""
+    if w.experts != routing.experts:
+        raise ValueError(f"{w.experts} matrices for {routing.experts} experts")
+    if up is not None and (up.experts, up.n, up.k) != (w.experts, w.n, w.k):
+        raise ValueError("up must have w's sizes")
+    pairs = routing.tokens * routing.topk
+    if x_q.shape[0] != (pairs if slots else routing.tokens):
+        raise ValueError(f"x_q: expected {pairs if slots else routing.tokens} rows, got {x_q.shape[0]}")
+    _one_device(routing.offset, w.w, x_q)
+    f, ref, by_slot = lib().bitnet_expert_linear, routing.ref, 1 if slots else 0
+    return _product("bitnet_expert_linear", w.w, w.scale, w.n, w.k, pairs, x_q, x_scale,
+                    None if up is None else (up.w, up.scale), bias, up_bias, act, None, y, y_dtype, w.experts, stream,
+                    lambda args, s: f(ref, args, by_slot, s))
+
+
+def bitnet_combine(routing, y, residual=None, out=None, out_dtype=None, stream=None):
+    """out[m] = residual[m] + sum_j weight[m, j] * y[slot[m, j]] of the slots' rows y [tokens * topk,
+    K].  residual [tokens, K] has out's dtype (y's unless out, out_dtype or residual says another);
+    out may be it."""
+    import torch
+    pairs = routing.tokens * routing.topk
+    if y.dim() != 2 or y.shape[0] != pairs:
+        raise ValueError(f"y: expected [{pairs}, K], got {tuple(y.shape)}")
+    k, yd = y.shape[1], y.dtype
+    y_code = _code(yd, "y")
+    _like(y, y.shape, yd, "y")
+    if out is not None:
+        if out_dtype is not None and out_dtype is not out.dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        out_dtype = out.dtype
+        _like(out, (routing.tokens, k), out_dtype, "out")
+    out_dtype = out_dtype or (yd if residual is None else residual.dtype)
+    out_code = _code(out_dtype, "out")
+    if residual is not None:
+        _like(residual, (routing.tokens, k), out_dtype, "residual")
+    device = _one_device(routing.slot, y, residual, out)
+    with _On(device, stream) as s:
+        if out is None:
+            out = torch.empty((routing.tokens, k), dtype=out_dtype, device=device)
+        status = lib().bitnet_combine(routing.ref, y.data_ptr(), y_code, k, 0 if residual is None else
+                                      residual.data_ptr(), out.data_ptr(), out_code, s)
+    if status:
+        raise BitnetError("bitnet_combine", status)
+    return out

@@ -3,6 +3,7 @@
 #include "bitnet_mi355x.h"
 #include "bitnet_internal.h"
 #include "layer_internal.h"
+#include "experts_internal.h"
 
 #include <string.h>
 
@@ -284,6 +285,50 @@ bool heads_fit(const bitnet_kv_cache& c, int q_heads) {
 bool attention_fits(const bitnet_kv_cache& c, const bitnet_kv_batch& b, int q_heads) {
   return b.max_new * (q_heads / c.kv_heads) <= kMaxCached &&
          bitnet::attention_fits(kv_cache(c), kv_batch(b), q_heads);
+}
+
+// Limits of a batch of pairs (token, choice).
+constexpr int64_t kMaxPairs = (int64_t)1 << 30;
+
+bool routing_fits(int64_t tokens, int topk, int experts) {
+  return tokens >= 0 && topk >= 1 && topk <= bitnet::kMaxTopk && experts >= 1 &&
+         experts <= bitnet::kMaxExperts && tokens <= kMaxPairs / topk;
+}
+
+bitnet::Routing routing_of(const bitnet_routing& r) {
+  return {r.expert, r.weight, r.offset, r.pair, r.slot, (int)r.tokens, r.topk, r.experts,
+          (int)(r.tokens * r.topk)};
+}
+
+// Sizes of a product with `rows` rows of y; *nothing: there is none to compute.
+bitnet_status check_product(const bitnet_product& p, int64_t rows, bool* nothing) {
+  if (!valid_dtype(p.y_dtype)) return BITNET_ERR_DTYPE;
+  if (rows < 0 || rows > kMaxPairs || p.N < 0 || p.K < 64 || p.K % 64 != 0 || p.K > BITNET_MAX_K ||
+      p.N >= BITNET_MAX_WEIGHTS / p.K || p.N > kInt32Max - 31 || p.act < BITNET_ACT_NONE ||
+      p.act > BITNET_ACT_GELU || (!p.up && (p.up_scale || p.up_bias)))
+    return BITNET_ERR_SHAPE;
+  *nothing = rows == 0 || p.N == 0;
+  if (*nothing) return BITNET_OK;
+  if (!p.w || !p.w_scale || (p.up && !p.up_scale) || !p.x_q || !p.x_scale || !p.y)
+    return BITNET_ERR_NULL;
+  if (!aligned(p.w, 16) || !aligned(p.up, 16) || !aligned(p.x_q, 16) || !aligned(p.w_scale, 4) ||
+      !aligned(p.up_scale, 4) || !aligned(p.bias, 4) || !aligned(p.up_bias, 4) ||
+      !aligned(p.x_scale, 4) || !aligned(p.y, esize(p.y_dtype)) ||
+      !aligned(p.residual, esize(p.y_dtype)))
+    return BITNET_ERR_ALIGN;
+  return BITNET_OK;
+}
+
+bitnet_status run_product(const bitnet_product& p, const bitnet_routing* r, bool by_slot,
+                          int64_t slots, hipStream_t stream) {
+  const bitnet::ExpertArgs a{r ? r->offset : nullptr,
+                             r && !by_slot ? r->pair : nullptr,
+                             p.w, p.up, p.w_scale, p.up_scale, p.bias, p.up_bias, p.x_q, p.x_scale,
+                             p.residual, p.y, (int)slots, (int)p.rows, r ? r->experts : 1,
+                             r ? r->topk : 1, (int)p.N, (int)p.K, p.act,
+                             p.y_dtype == BITNET_BF16 ? 1 : 0};
+  if (!bitnet::experts_fit(a)) return BITNET_ERR_SHAPE;
+  return from_hip(bitnet::launch_experts(a, stream));
 }
 
 }  // namespace
@@ -767,6 +812,78 @@ bitnet_status bitnet_residual_norm(const bitnet_residual* args, hipStream_t stre
                                r.scale, r.eps};
   return from_hip(bitnet::launch_residual(a, r.y_dtype == BITNET_BF16, r.h_dtype == BITNET_BF16,
                                           r.u && r.u_dtype == BITNET_BF16, r.M, stream));
+}
+
+size_t bitnet_route_workspace_bytes(int64_t tokens, int topk, int experts) {
+  if (!routing_fits(tokens, topk, experts) || tokens == 0) return 0;
+  return bitnet::route_workspace_bytes(tokens, topk, experts);
+}
+
+bitnet_status bitnet_route(const bitnet_routing* routing, const void* logits, int dtype,
+                           int64_t stride, int score, float scale, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  if (!routing) return BITNET_ERR_NULL;
+  const bitnet_routing& r = *routing;
+  if (logits && !valid_dtype(dtype)) return BITNET_ERR_DTYPE;
+  if (!routing_fits(r.tokens, r.topk, r.experts) ||
+      (logits && (stride < r.experts || score < BITNET_SOFTMAX || score > BITNET_SIGMOID ||
+                  !finite(scale))))
+    return BITNET_ERR_SHAPE;
+  if (!r.offset) return BITNET_ERR_NULL;
+  if (r.tokens > 0 && (!r.expert || (logits && !r.weight) || !r.pair || !r.slot))
+    return BITNET_ERR_NULL;
+  if (!aligned(r.expert, 4) || !aligned(r.weight, 4) || !aligned(r.offset, 4) ||
+      !aligned(r.pair, 4) || !aligned(r.slot, 4) || (logits && !aligned(logits, esize(dtype))))
+    return BITNET_ERR_ALIGN;
+  const size_t need = bitnet_route_workspace_bytes(r.tokens, r.topk, r.experts);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return BITNET_ERR_WORKSPACE;
+    if (!aligned(workspace, 4)) return BITNET_ERR_ALIGN;
+  }
+  return from_hip(bitnet::launch_route(routing_of(r), logits, dtype == BITNET_BF16, stride, score,
+                                       scale, workspace, stream));
+}
+
+bitnet_status bitnet_ternary_linear_act(const bitnet_product* product, hipStream_t stream) {
+  if (!product) return BITNET_ERR_NULL;
+  bool nothing = false;
+  const bitnet_status st = check_product(*product, product->rows, &nothing);
+  if (st != BITNET_OK || nothing) return st;
+  return run_product(*product, nullptr, false, product->rows, stream);
+}
+
+bitnet_status bitnet_expert_linear(const bitnet_routing* routing, const bitnet_product* product,
+                                   int by_slot, hipStream_t stream) {
+  if (!routing || !product) return BITNET_ERR_NULL;
+  const bitnet_routing& r = *routing;
+  if (!routing_fits(r.tokens, r.topk, r.experts) || (by_slot != 0 && by_slot != 1))
+    return BITNET_ERR_SHAPE;
+  const int64_t pairs = r.tokens * r.topk;
+  bool nothing = false;
+  const bitnet_status st = check_product(*product, pairs, &nothing);
+  if (st != BITNET_OK) return st;
+  if (product->rows != (by_slot ? pairs : r.tokens) || product->residual ||
+      (!by_slot && r.tokens * product->K >= ((int64_t)1 << 32)))
+    return BITNET_ERR_SHAPE;
+  if (nothing) return BITNET_OK;
+  if (!r.offset || (!by_slot && !r.pair)) return BITNET_ERR_NULL;
+  if (!aligned(r.offset, 4) || !aligned(r.pair, 4)) return BITNET_ERR_ALIGN;
+  return run_product(*product, routing, by_slot != 0, pairs, stream);
+}
+
+bitnet_status bitnet_combine(const bitnet_routing* routing, const void* y, int y_dtype, int64_t K,
+                             const void* residual, void* out, int out_dtype, hipStream_t stream) {
+  if (!routing) return BITNET_ERR_NULL;
+  const bitnet_routing& r = *routing;
+  if (!valid_dtype(y_dtype) || !valid_dtype(out_dtype)) return BITNET_ERR_DTYPE;
+  if (!routing_fits(r.tokens, r.topk, r.experts) || K < 0 || K > kInt32Max) return BITNET_ERR_SHAPE;
+  if (r.tokens == 0 || K == 0) return BITNET_OK;
+  if (!r.weight || !r.slot || !y || !out) return BITNET_ERR_NULL;
+  if (!aligned(r.weight, 4) || !aligned(r.slot, 4) || !aligned(y, esize(y_dtype)) ||
+      !aligned(residual, esize(out_dtype)) || !aligned(out, esize(out_dtype)))
+    return BITNET_ERR_ALIGN;
+  return from_hip(bitnet::launch_combine(routing_of(r), y, y_dtype == BITNET_BF16, K, residual, out,
+                                         out_dtype == BITNET_BF16, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,146 @@
+// Internal declarations of a feed-forward of ternary experts: routing, products grouped by
+// expert, and the combination of their outputs.
+#pragma once
+
+#include "layer_internal.h"
+
+namespace bitnet {
+
+constexpr int kMaxExperts = 1024;   // counters of a workgroup's pairs by expert lie in LDS
+constexpr int kMaxTopk = 32;        // a lane a choice
+
+// Which rows belong to which expert (bitnet_routing, validated).
+struct Routing {
+  int32_t* expert;     // [tokens][topk]
+  float* weight;       // [tokens][topk]
+  int32_t* offset;     // [experts + 1]
+  int32_t* pair;       // [pairs]
+  int32_t* slot;       // [pairs]
+  int tokens, topk, experts, pairs;
+};
+enum RouteScore { kSoftmax = 0, kChosen = 1, kSigmoid = 2 };
+size_t route_workspace_bytes(int64_t tokens, int topk, int experts);
+// logits nullptr: r.expert is given and only the plan is made.
+hipError_t launch_route(const Routing& r, const void* logits, bool bf16, int64_t stride, int score,
+                        float scale, void* workspace, hipStream_t s);
+
+// A ternary product with what follows it.  Slots are rows of y; with `offset` they belong to
+// experts, without it all to matrix 0.
+enum Act { kActNone = 0, kActRelu2 = 1, kActSilu = 2, kActGelu = 3 };
+struct ExpertArgs {
+  const int32_t* offset;     // [experts + 1] first slot of each expert, or nullptr: one matrix
+  const int32_t* pair;       // [slots] input row times `topk`, or nullptr: a slot is its input row
+  const uint8_t *w, *up;     // [experts] matrices in the prefill layout; up: nullptr for none
+  const float *w_scale, *up_scale;     // [experts]
+  const float *bias, *up_bias;         // [experts][N] or nullptr
+  const int8_t* xq;          // [rows][K]
+  const float* xs;           // [rows]
+  const void* residual;      // [slots][N] like y, or nullptr
+  void* y;                   // [slots][N]
+  int slots, rows, experts, topk, N, K, act, y_bf16;
+};
+// Most tiles of `rows` slots that `slots` slots of `experts` experts make.
+inline int64_t expert_tiles(int64_t slots, int64_t experts, int rows) {
+  return slots / rows + (slots < experts ? slots : experts);
+}
+bool experts_fit(const ExpertArgs& a);
+hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
+
+// out[m] = residual[m] + sum_j weight[m][j] y[slot[m][j]].
+hipError_t launch_combine(const Routing& r, const void* y, bool y_bf16, int64_t K,
+                          const void* residual, void* out, bool out_bf16, hipStream_t s);
+
+// Tile t of the experts' slots cut into tiles of `rows`: its expert, first slot and rows (0: none).
+// The offsets lie in device memory, where the host cannot check them: they are clamped to the
+// batch.  A wave reads 64 experts' offsets at once.
+struct ExpertTile {
+  int expert, slot0, rows;
+};
+__device__ __forceinline__ int wave_scan(int v) {   // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o, 64);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+template <int ROWS>
+__device__ __forceinline__ ExpertTile expert_tile(const ExpertArgs& a, int t) {
+  if (!a.offset) {
+    const int s0 = t * ROWS;
+    return {0, s0, max(min(a.slots - s0, ROWS), 0)};
+  }
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0, base = 0; e0 < a.experts; e0 += 64) {
+    const int e = e0 + lane;
+    int lo = 0, n = 0;
+    if (e < a.experts) {
+      lo = min(max(a.offset[e], 0), a.slots);
+      n = min(max(a.offset[e + 1], lo), a.slots) - lo;
+    }
+    const int tiles = (n + ROWS - 1) / ROWS;
+    const int upto = base + wave_scan(tiles);
+    const uint64_t past = __ballot(upto > t);
+    if (past) {
+      const int l = __ffsll((unsigned long long)past) - 1;
+      const int i = t - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l));
+      ExpertTile r;
+      r.expert = e0 + l;
+      r.slot0 = __builtin_amdgcn_readlane(lo, l) + i * ROWS;
+      r.rows = min(__builtin_amdgcn_readlane(n, l) - i * ROWS, ROWS);
+      return r;
+    }
+    base = __builtin_amdgcn_readlane(upto, 63);
+  }
+  return {0, 0, 0};
+}
+// Input row of a slot; -1 where the device's numbers name none.
+__device__ __forceinline__ int input_row(const ExpertArgs& a, int slot) {
+  if (!a.pair) return slot < a.rows ? slot : -1;
+  const int p = a.pair[slot];
+  if (p < 0) return -1;
+  const int row = (int)((uint32_t)p / (uint32_t)a.topk);
+  return row < a.rows ? row : -1;
+}
+
+// 16 weights of the prefill layout (codes q + 1) as the int8 operand -64 q, in natural k order: the
+// code XOR 1 is -q in two bits, and a field moved to a byte's two top bits is 64 times that, so
+// that a shift and a mask make four weights and no sum of x has to be taken off the products.
+// The products' sums are -64 acc: at most 64 * 128 * K <= 2^30.
+__device__ __forceinline__ v4i weights_64(uint32_t w) {
+  w ^= 0x55555555u;
+  v4i a;
+  a.x = (int)((w << 6) & 0xc0c0c0c0u);
+  a.y = (int)((w << 4) & 0xc0c0c0c0u);
+  a.z = (int)((w << 2) & 0xc0c0c0c0u);
+  a.w = (int)(w & 0xc0c0c0c0u);
+  return a;
+}
+__device__ __forceinline__ float acc_64(int acc) { return (float)(-(acc >> 6)); }   // exact
+
+// e^x for x <= 0, the rounding of x log2 e made up for (it is x 2^-24 otherwise).
+__device__ __forceinline__ float exp_neg(float x) {
+  const float t = x * 0x1.715476p+0f;                       // log2 e, rounded
+  const float lo = fmaf(x, 0x1.4ae0cp-26f, fmaf(x, 0x1.715476p+0f, -t));
+  const float p = __builtin_amdgcn_exp2f(t);
+  return fmaf(p, lo * 0x1.62e43p-1f, p);
+}
+__device__ __forceinline__ float activate(float v, int act) {
+  switch (act) {
+    case kActRelu2: {
+      const float a = fmaxf(v, 0.0f);
+      return a * a;
+    }
+    case kActSilu: {      // v / (1 + e^-v), by e^-|v| so that nothing overflows
+      const float e = exp_neg(-fabsf(v));
+      return (v < 0.0f ? v * e : v) * __builtin_amdgcn_rcpf(1.0f + e);
+    }
+    case kActGelu:        // v times the normal distribution's integral up to v
+      return v * (0.5f * erfcf(v * -0x1.6a09e6p-1f));
+    default:
+      return v;
+  }
+}
+
+}  // namespace bitnet

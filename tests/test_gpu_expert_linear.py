@@ -1,0 +1,200 @@
+"""bitnet_expert_linear and bitnet_ternary_linear_act on the GPU against the oracle: bit for bit
+without silu and gelu, within their stated bounds with them."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import experts_oracle as E
+from ternary_weight_linear_bit_amd import _native as N
+
+from experts_util import F32, TORCH, acts, assign, close, dev, host, matrices, routing, same, typed
+from gpu_helpers import DEV
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    N.lib()
+
+
+def compare(t, a, tol, dt):
+    if tol is None:
+        same(t, a, dt)
+    else:
+        close(t, a, tol, dt)
+
+
+def run(counts, tokens, topk, n, k, act="none", gated=False, bias=False, slots=False, dt="f32", seed=0, expert=None,
+        offset=0):
+    """One call against the oracle, rows behind the last slot and around y looked at too."""
+    print(f"counts={counts} tokens={tokens} topk={topk} N={n} K={k} {act} gated={gated} slots={slots} {dt}", flush=True)
+    experts = len(counts)
+    expert = assign(counts, tokens, topk, seed) if expert is None else expert
+    r, (first, pair, _) = routing(expert, experts)
+    pairs = tokens * topk
+    xq, d = acts(pairs if slots else tokens, k, seed)
+    rng = np.random.default_rng(seed + 77)
+    mats = [matrices(experts, n, k, seed + 1 + i) for i in range(1 + gated)]
+    b = [rng.standard_normal((experts, n)).astype(F32) if bias else None for _ in mats]
+    buf = torch.full((pairs * n + 64,), 7.0, dtype=TORCH[dt], device=DEV)
+    y = buf[32 + offset:32 + offset + pairs * n].view(pairs, n)
+    got = N.bitnet_expert_linear(r, mats[0][2], dev(xq), dev(d), slots=slots, act=act, bias=None if not bias else dev(b[0]),
+                                 up=mats[1][2] if gated else None, up_bias=dev(b[1]) if gated and bias else None, y=y)
+    assert got is y
+    for e in range(experts):
+        s0, s1 = int(first[e]), int(first[e + 1])
+        if s0 == s1:
+            continue
+        rows = np.arange(s0, s1) if slots else pair[s0:s1] // topk
+        up = (mats[1][0][e], mats[1][1][e], b[1][e] if bias else None) if gated else None
+        want = E.product(mats[0][0][e], mats[0][1][e], xq[rows], d[rows], b[0][e] if bias else None, act, up)
+        compare(y[s0:s1], *want, dt)
+    torch.cuda.synchronize()
+    left = buf.float().cpu().numpy()
+    assert (left[:32 + offset] == 7).all() and (left[32 + offset + pairs * n:] == 7).all()
+    assert (y[int(first[-1]):].float().cpu().numpy() == 7).all()
+    return y
+
+
+# rows of each expert around the tiles' edges; every N and K is a different raggedness
+COUNTS = [([1], 1, 1), ([0, 1, 0], 1, 1), ([1, 1], 1, 2), ([5, 0, 31, 32, 33], 60, 2), ([63, 0, 64, 65, 0, 1], 100, 2),
+          ([127, 129, 128, 2], 200, 2), ([255, 0, 257, 256], 400, 2), ([0, 0, 600], 300, 2), ([1] * 70, 25, 3),
+          ([0] * 64 + [3, 0, 2] + [0] * 61, 5, 1)]
+
+
+@pytest.mark.parametrize("counts,tokens,topk", COUNTS)
+@pytest.mark.parametrize("n,k", [(1, 64), (33, 192), (100, 128), (257, 320)])
+def test_ragged(counts, tokens, topk, n, k):
+    run(counts, tokens, topk, n, k, seed=len(counts))
+
+
+@pytest.mark.parametrize("counts,tokens,topk", [COUNTS[1], COUNTS[3], COUNTS[6]])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("slots", [False, True])
+@pytest.mark.parametrize("act", ["none", "relu2", "silu", "gelu"])
+@pytest.mark.parametrize("gated,bias", [(False, False), (True, False), (True, True), (False, True)])
+def test_epilogues(counts, tokens, topk, act, gated, bias, slots, dt):
+    run(counts, tokens, topk, 90, 192, act, gated, bias, slots, dt, seed=3)
+
+
+@pytest.mark.parametrize("n,k,dt", [(2560, 1152, "f32"), (864, 2560, "bf16"), (64, 14336, "bf16"), (40, 131072, "f32")])
+def test_model_sizes(n, k, dt):
+    run([70, 0, 3, 300], 190, 2, n, k, "relu2", True, False, False, dt, seed=5)
+    run([2, 1], 3, 1, n, k, "none", False, True, True, dt, seed=6)
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_unaligned_outputs(offset, dt):
+    for counts, tokens, n in (([4, 3], 4, 64), ([300, 200], 250, 64), ([90, 100], 100, 67)):
+        run(counts, tokens, 2, n, 128, "relu2", True, True, False, dt, seed=9, offset=offset)
+
+
+def test_extreme_sums():
+    """All weights +1 and x = -128 over the longest row: the largest accumulator."""
+    k, n = 131072, 33
+    from oracle import bitnet_oracle as O
+    packed = O.pack_codes(np.ones((n, k), np.int8))[None]
+    w = N.TernaryExperts.from_packed(dev(packed), dev(np.array([0.5], F32)))
+    for rows in (3, 200):
+        r, _ = routing(np.zeros((rows, 1), np.int32), 1)
+        x = np.full((rows, k), -128, np.int8)
+        y = N.bitnet_expert_linear(r, w, dev(x), dev(np.ones(rows, F32)))
+        assert (host(y) == -64.0 * k).all()
+
+
+def test_the_same_token_twice():
+    """A pair list that names one expert twice gives the row twice."""
+    e = np.array([[1, 1], [0, 1], [1, 1]], np.int32)
+    y = run([1, 5], 3, 2, 40, 128, expert=e)
+    assert torch.equal(y[1], y[2])
+
+
+def test_contents_that_name_nothing():
+    """Offsets past the batch or backwards, pairs past it or negative: other rows are right, nothing else is
+    written."""
+    xq, d = acts(6, 128, 1)
+    q, g, w = matrices(3, 50, 128, 2)
+    r, (first, pair, _) = routing(assign([4, 4, 4], 6, 2), 3)
+    pair = pair.copy()
+    pair[[1, 5]] = [-7, 1 << 30]
+    r.pair.copy_(dev(pair))
+    r.offset.copy_(torch.tensor([-5, 4, 8, 1 << 30], dtype=torch.int32))
+    y = torch.full((12, 50), 7.0, device=DEV)
+    N.bitnet_expert_linear(r, w, dev(xq), dev(d), y=y)
+    for s in range(12):
+        if s in (1, 5):
+            assert (host(y[s]) == 7).all()
+        else:
+            row = pair[s] // 2
+            same(y[s:s + 1], E.product(q[s // 4], g[s // 4], xq[row:row + 1], d[row:row + 1])[0], "f32")
+    r.offset.copy_(torch.tensor([8, 4, 2, -1], dtype=torch.int32))      # empty experts only
+    y.fill_(7.0)
+    N.bitnet_expert_linear(r, w, dev(xq), dev(d), y=y)
+    assert (host(y) == 7).all()
+
+
+@pytest.mark.parametrize("m", [1, 2, 16, 17, 33, 64, 100, 200, 513])
+@pytest.mark.parametrize("n,k", [(2560, 192), (129, 2560), (40, 64)])
+def test_dense_is_the_prefill_product(m, n, k):
+    xq, d = acts(m, k, m)
+    _, g, w = matrices(1, n, k, 4)
+    for dt in (torch.float32, torch.bfloat16):
+        want = N.bitnet_ternary_linear_prefill([(w.w[0], w.scale, n)], dev(xq), dev(d), y_dtype=dt)[0]
+        got = N.bitnet_ternary_linear_act(w.w[0], w.scale, n, dev(xq), dev(d), y_dtype=dt)
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("m", [1, 5, 40, 150, 300])
+@pytest.mark.parametrize("act,gated", [("none", False), ("relu2", True), ("gelu", False), ("silu", True)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_dense_epilogue(m, act, gated, dt):
+    for n, bias, residual, offset in ((96, True, True, 0), (101, False, True, 0), (64, True, True, 1), (72, True, False, 0)):
+        k = 320
+        xq, d = acts(m, k, m)
+        mats = [matrices(1, n, k, 6 + i) for i in range(1 + gated)]
+        rng = np.random.default_rng(m + n)
+        b = [rng.standard_normal(n).astype(F32) if bias else None for _ in mats]
+        flat = torch.zeros(m * n + 8, dtype=TORCH[dt], device=DEV)
+        res, rf = (None, None)
+        if residual:
+            t, rf = typed(2 * rng.standard_normal((m, n)), dt)
+            res = flat[offset:offset + m * n].view(m, n)
+            res.copy_(t)
+        up = None if not gated else (mats[1][0][0], mats[1][1][0], b[1])
+        want = E.product(mats[0][0][0], mats[0][1][0], xq, d, b[0], act, up, rf)
+        args = dict(act=act, bias=None if not bias else dev(b[0]), up_bias=dev(b[1]) if gated and bias else None,
+                    up=(mats[1][2].w[0], mats[1][2].scale) if gated else None, residual=res, y_dtype=TORCH[dt])
+        w = mats[0][2]
+        compare(N.bitnet_ternary_linear_act(w.w[0], w.scale, n, dev(xq), dev(d), **args), *want, dt)
+        if residual:                                    # y in the residual's place
+            y = N.bitnet_ternary_linear_act(w.w[0], w.scale, n, dev(xq), dev(d), **args, y=res)
+            assert y is res
+            compare(y, *want, dt)
+            assert (flat[:offset] == 0).all() and (flat[offset + m * n:] == 0).all()
+
+
+def test_nothing_to_do():
+    _, _, w = matrices(2, 40, 128, 1)
+    r = N.Routing.empty(0, 2, 2, DEV)
+    assert N.bitnet_expert_linear(r, w, torch.empty((0, 128), dtype=torch.int8, device=DEV), torch.empty(0, device=DEV)).shape == (0, 40)
+    r, _ = routing(np.full((40, 2), -1, np.int32), 2)          # a batch of padding
+    xq, d = acts(40, 128, 1)
+    y = torch.full((80, 40), 7.0, device=DEV)
+    N.bitnet_expert_linear(r, w, dev(xq), dev(d), y=y)
+    assert (host(y) == 7).all()
+
+
+def test_another_stream():
+    xq, d = acts(300, 192, 1)
+    q, g, w = matrices(1, 70, 192, 2)
+    x, dd = dev(xq), dev(d)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = N.bitnet_ternary_linear_act(w.w[0], w.scale, 70, x, dd, act="relu2", stream=s)
+    s.synchronize()
+    same(y, E.product(q[0], g[0], xq, d, act="relu2")[0], "f32")
