@@ -91,19 +91,12 @@ __global__ __launch_bounds__(64 * W) void experts_few_kernel(const ExpertArgs a,
       v = v * u;
     }
     const size_t o = (size_t)(t.slot0 + sl) * a.N + n;
-    if (a.y_bf16) {
-      if (a.residual) v = v + bf16_bits_to_float(static_cast<const uint16_t*>(a.residual)[o]);
-      static_cast<uint16_t*>(a.y)[o] = float_to_bf16_rne(v);
-    } else {
-      if (a.residual) v = v + static_cast<const float*>(a.residual)[o];
-      static_cast<float*>(a.y)[o] = v;
-    }
+    store_output(a, o, v);
   }
 }
 
 int64_t few_grid(const ExpertArgs& a) {
-  return (a.offset ? expert_tiles(a.slots, a.experts, kFewRows)
-                   : ((int64_t)a.slots + kFewRows - 1) / kFewRows) * ((a.N + 31) / 32);
+  return many_tiles(a, kFewRows) * ((a.N + 31) / 32);
 }
 
 }  // namespace
@@ -111,6 +104,16 @@ int64_t few_grid(const ExpertArgs& a) {
 bool experts_fit(const ExpertArgs& a) { return few_grid(a) <= max_grid(512); }
 
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s) {
+  // tiles of each shape, if the slots were spread evenly over the experts
+  const int64_t used = a.experts < a.slots ? a.experts : a.slots, each = (a.slots + used - 1) / used;
+  auto tiles = [&](int rows, int cols) {
+    return used * ((each + rows - 1) / rows) * ((a.N + cols - 1) / cols);
+  };
+  const int wide = a.up ? 128 : 256;
+  if (each > 8 && tiles(kFewRows, 32) > 512) {
+    if (each >= 192 && tiles(128, wide) >= 256) return launch_experts_many(a, 128, s);
+    return launch_experts_many(a, tiles(64, wide) >= 256 ? 64 : 32, s);
+  }
   const int nblocks = (a.N + 31) / 32;
   const dim3 grid((unsigned)few_grid(a));
   if (a.up)

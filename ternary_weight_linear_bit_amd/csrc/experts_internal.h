@@ -43,7 +43,12 @@ struct ExpertArgs {
 inline int64_t expert_tiles(int64_t slots, int64_t experts, int rows) {
   return slots / rows + (slots < experts ? slots : experts);
 }
+inline int64_t many_tiles(const ExpertArgs& a, int rows) {
+  return a.offset ? expert_tiles(a.slots, a.experts, rows) : ((int64_t)a.slots + rows - 1) / rows;
+}
 bool experts_fit(const ExpertArgs& a);
+// Few rows an expert (experts.hip), many (experts_many.hip; tiles of bm slots).
+hipError_t launch_experts_many(const ExpertArgs& a, int bm, hipStream_t s);
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
 
 // out[m] = residual[m] + sum_j weight[m][j] y[slot[m][j]].
@@ -95,6 +100,18 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertArgs& a, int t) {
   }
   return {0, 0, 0};
 }
+// Tiles of all experts.
+template <int ROWS>
+__device__ __forceinline__ int count_tiles(const ExpertArgs& a) {
+  if (!a.offset) return (a.slots + ROWS - 1) / ROWS;
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int e = lane; e < a.experts; e += 64) {
+    const int lo = min(max(a.offset[e], 0), a.slots);
+    n += (min(max(a.offset[e + 1], lo), a.slots) - lo + ROWS - 1) / ROWS;
+  }
+  return wave_sum(n);
+}
 // Input row of a slot; -1 where the device's numbers name none.
 __device__ __forceinline__ int input_row(const ExpertArgs& a, int slot) {
   if (!a.pair) return slot < a.rows ? slot : -1;
@@ -109,12 +126,12 @@ __device__ __forceinline__ int input_row(const ExpertArgs& a, int slot) {
 // that a shift and a mask make four weights and no sum of x has to be taken off the products.
 // The products' sums are -64 acc: at most 64 * 128 * K <= 2^30.
 __device__ __forceinline__ v4i weights_64(uint32_t w) {
-  w ^= 0x55555555u;
+  constexpr uint32_t top = 0xc0c0c0c0u, one = 0x40404040u;
   v4i a;
-  a.x = (int)((w << 6) & 0xc0c0c0c0u);
-  a.y = (int)((w << 4) & 0xc0c0c0c0u);
-  a.z = (int)((w << 2) & 0xc0c0c0c0u);
-  a.w = (int)(w & 0xc0c0c0c0u);
+  a.x = (int)__builtin_amdgcn_bitop3_b32(w << 6, top, one, 0x6a);   // (w & top) ^ one
+  a.y = (int)__builtin_amdgcn_bitop3_b32(w << 4, top, one, 0x6a);
+  a.z = (int)__builtin_amdgcn_bitop3_b32(w << 2, top, one, 0x6a);
+  a.w = (int)__builtin_amdgcn_bitop3_b32(w, top, one, 0x6a);
   return a;
 }
 __device__ __forceinline__ float acc_64(int acc) { return (float)(-(acc >> 6)); }   // exact
@@ -140,6 +157,18 @@ __device__ __forceinline__ float activate(float v, int act) {
       return v * (0.5f * erfcf(v * -0x1.6a09e6p-1f));
     default:
       return v;
+  }
+}
+
+
+// y[o] = RN(a + residual[o])
+__device__ __forceinline__ void store_output(const ExpertArgs& a, size_t o, float v) {
+  if (a.y_bf16) {
+    if (a.residual) v = v + bf16_bits_to_float(static_cast<const uint16_t*>(a.residual)[o]);
+    static_cast<uint16_t*>(a.y)[o] = float_to_bf16_rne(v);
+  } else {
+    if (a.residual) v = v + static_cast<const float*>(a.residual)[o];
+    static_cast<float*>(a.y)[o] = v;
   }
 }
 

@@ -87,6 +87,16 @@ def test_model_sizes(n, k, dt):
     run([2, 1], 3, 1, n, k, "none", False, True, True, dt, seed=6)
 
 
+# wide enough for the kernels of many rows and each of their tiles, ragged in all directions
+@pytest.mark.parametrize("counts,tokens,n", [([300], 150, 24001), ([150], 75, 24001), ([150], 80, 4001), ([40, 0, 33, 70], 72, 6016),
+                                             ([257, 0, 384, 200], 421, 12008)])
+@pytest.mark.parametrize("k,act,gated,bias,slots,dt", [
+    (64, "none", False, False, False, "f32"), (192, "relu2", True, True, True, "bf16"), (128, "silu", False, True, False, "bf16"),
+    (320, "none", False, True, True, "bf16"), (448, "gelu", True, False, False, "f32")])
+def test_wide(counts, tokens, n, k, act, gated, bias, slots, dt):
+    run(counts, tokens, 2, n, k, act, gated, bias, slots, dt, seed=n)
+
+
 @pytest.mark.parametrize("offset", [1, 2, 3])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_unaligned_outputs(offset, dt):
@@ -152,8 +162,12 @@ def test_dense_is_the_prefill_product(m, n, k):
 @pytest.mark.parametrize("m", [1, 5, 40, 150, 300])
 @pytest.mark.parametrize("act,gated", [("none", False), ("relu2", True), ("gelu", False), ("silu", True)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-def test_dense_epilogue(m, act, gated, dt):
+@pytest.mark.parametrize("wide", [0, 3200, 22400])
+def test_dense_epilogue(m, act, gated, dt, wide):
     for n, bias, residual, offset in ((96, True, True, 0), (101, False, True, 0), (64, True, True, 1), (72, True, False, 0)):
+        if wide and (m < 150 or n == 64 and wide > 4000):
+            continue
+        n += wide
         k = 320
         xq, d = acts(m, k, m)
         mats = [matrices(1, n, k, 6 + i) for i in range(1 + gated)]
