@@ -655,8 +655,8 @@ typedef enum bitnet_score { BITNET_SOFTMAX = 0, BITNET_CHOSEN = 1, BITNET_SIGMOI
  *           expert -1 and weight 0.
  *   score, scale   weight = scale * the score, in fp32 (scale finite).  Logits that equal the row's
  *           largest count e^0, +inf too.
- *   workspace  bitnet_route_workspace_bytes() bytes, 4-byte aligned; clobbered; calls that overlap
- *           need one each.  NULL when the size is 0.
+ *   workspace  bitnet_route_workspace_bytes() bytes, 16-byte aligned; clobbered; calls that
+ *           overlap need one each.  NULL when the size is 0.
  * Indices are exact, and the same call gives the same bits.
  */
 bitnet_status bitnet_route(const bitnet_routing *routing, const void *logits, int dtype,

@@ -838,7 +838,7 @@ bitnet_status bitnet_route(const bitnet_routing* routing, const void* logits, in
   const size_t need = bitnet_route_workspace_bytes(r.tokens, r.topk, r.experts);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return BITNET_ERR_WORKSPACE;
-    if (!aligned(workspace, 4)) return BITNET_ERR_ALIGN;
+    if (!aligned(workspace, 16)) return BITNET_ERR_ALIGN;
   }
   return from_hip(bitnet::launch_route(routing_of(r), logits, dtype == BITNET_BF16, stride, score,
                                        scale, workspace, stream));
@@ -876,7 +876,9 @@ bitnet_status bitnet_combine(const bitnet_routing* routing, const void* y, int y
   if (!routing) return BITNET_ERR_NULL;
   const bitnet_routing& r = *routing;
   if (!valid_dtype(y_dtype) || !valid_dtype(out_dtype)) return BITNET_ERR_DTYPE;
-  if (!routing_fits(r.tokens, r.topk, r.experts) || K < 0 || K > kInt32Max) return BITNET_ERR_SHAPE;
+  if (!routing_fits(r.tokens, r.topk, r.experts) || K < 0 || K > kInt32Max ||
+      !bitnet::combine_fits(r.tokens, K))
+    return BITNET_ERR_SHAPE;
   if (r.tokens == 0 || K == 0) return BITNET_OK;
   if (!r.weight || !r.slot || !y || !out) return BITNET_ERR_NULL;
   if (!aligned(r.weight, 4) || !aligned(r.slot, 4) || !aligned(y, esize(y_dtype)) ||

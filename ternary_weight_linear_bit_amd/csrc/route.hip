@@ -6,30 +6,78 @@ namespace bitnet {
 namespace {
 
 // ---------------------------------------------------------------------------
-// choice: a wave a token
+// choice: 16, 32 or 64 lanes a token
 // ---------------------------------------------------------------------------
+//
+// A logit and its expert's number are held as one double in [1, 2), the logit's order-preserving key
+// in the upper and 1023 - e in the lower of 42 mantissa bits, so that a maximum takes one
+// instruction and equal logits go to the lowest number; 0 stands for one that is never chosen.  A
+// lane sorts its V candidates (a comparison is a min and a max), then the token's topk largest are
+// taken from the heads of its lanes' lists.
 
-// Order-preserving key of a logit: 0 for -inf and NaN, which are never chosen; -0 counts as 0.
-__device__ __forceinline__ uint32_t logit_key(float x) {
-  if (!(x > -INFINITY)) return 0u;
-  const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+// 0 for -inf and NaN; -0 counts as 0.
+__device__ __forceinline__ double candidate(float x, int e) {
+  if (!(x > -INFINITY)) return 0.0;
+  uint32_t b = __float_as_uint(x + 0.0f);
+  b ^= (uint32_t)((int)b >> 31) | 0x80000000u;
+  const uint64_t u = (0x3ffull << 52) | ((uint64_t)b << 10) | (uint64_t)(1023 - e);
+  return __longlong_as_double((long long)u);
 }
-__device__ __forceinline__ float key_logit(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+__device__ __forceinline__ int candidate_expert(double c) {
+  return c == 0.0 ? -1 : 1023 - (int)((uint64_t)__double_as_longlong(c) & 1023u);
 }
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, 64));
+__device__ __forceinline__ float candidate_logit(double c) {
+  const uint32_t b = (uint32_t)((uint64_t)__double_as_longlong(c) >> 10);
+  return __uint_as_float(b ^ ((b & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+}
+
+// Maximum (doubles) and sum (floats) over L lanes.
+#define BITNET_ROW(v, ctrl) __builtin_amdgcn_update_dpp(0, (v), (ctrl), 0xf, 0xf, true)
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)BITNET_ROW((int)(uint32_t)u, CTRL);
+  const uint32_t hi = (uint32_t)BITNET_ROW((int)(uint32_t)(u >> 32), CTRL);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(BITNET_ROW(__float_as_int(v), CTRL));
+}
+#undef BITNET_ROW
+struct Larger {
+  __device__ double operator()(double a, double b) const { return __builtin_fmax(a, b); }
+  __device__ float operator()(float a, float b) const { return a + b; }    // floats are summed
+};
+template <int L, typename T>
+__device__ __forceinline__ T over_lanes(T v) {
+  const Larger f;
+  v = f(v, dpp<0xb1>(v));      // lane ^ 1
+  v = f(v, dpp<0x4e>(v));      // lane ^ 2
+  v = f(v, dpp<0x141>(v));     // half-row mirror
+  v = f(v, dpp<0x140>(v));     // row mirror
+  if (L >= 32) v = f(v, __shfl_xor(v, 16, 64));
+  if (L == 64) v = f(v, __shfl_xor(v, 32, 64));
   return v;
 }
-__device__ __forceinline__ float wave_fsum(float v) {
+
+// Batcher's merge exchange of V values, largest first.
+template <int V>
+__device__ __forceinline__ void sort_down(double (&c)[V]) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const double a = c[i + j], b = c[i + j + k];
+            c[i + j] = __builtin_fmax(a, b);
+            c[i + j + k] = __builtin_fmin(a, b);
+          }
 }
-// x - m, 0 where they are the same (infinities too)
-__device__ __forceinline__ float below(float x, float m) { return x == m ? 0.0f : x - m; }
 
 struct RouteArgs {
   Routing r;
@@ -39,270 +87,417 @@ struct RouteArgs {
   float scale;
 };
 
-// Token m's choices, by one wave; lane l holds experts V l .. V l + V - 1, so that the first lane
-// with the largest key has the lowest index.  Lane j < topk returns choice j.
-template <int V, bool BF16>
+// e^(x - m) for x <= m; 1 where they are the same (infinities too)
+__device__ __forceinline__ float power(float x, float m) {
+  return x == m ? 1.0f : exp_neg(fmaxf(x - m, -200.0f));
+}
+
+// Token m's choices by L lanes; lane l of them holds experts V l .. V l + V - 1.  Lane j < topk
+// (<= L) of the token writes choice j and returns its expert.
+template <int L, int V, bool BF16>
 __device__ __forceinline__ int choose(const RouteArgs& a, int m) {
-  const int lane = threadIdx.x & 63;
   const Routing& r = a.r;
-  uint32_t key[V];
+  const int l = threadIdx.x & (L - 1);
+  const int64_t at = (int64_t)m * a.stride + l * V;
+  const int n = r.experts - l * V;
+  float x[V];
+  constexpr int W = 16 / (BF16 ? 2 : 4);       // elements of 16 bytes
+  if (V >= W && n >= V && ((reinterpret_cast<uintptr_t>(a.logits) + (size_t)at * (16 / W)) & 15) == 0) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(a.logits) + at * (16 / W));
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    key[i] = 0u;
-    if (e < r.experts) {
-      const int64_t at = (int64_t)m * a.stride + e;
-      key[i] = logit_key(BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.logits)[at])
-                              : static_cast<const float*>(a.logits)[at]);
+    for (int i = 0; i < V / W; ++i) {
+      const uint4 u = q[i];
+      const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (BF16) {
+          x[(W * i + 2 * e) % V] = __uint_as_float(d[e] << 16);
+          x[(W * i + 2 * e + 1) % V] = __uint_as_float(d[e] & 0xffff0000u);
+        } else {
+          x[(W * i + e) % V] = __uint_as_float(d[e]);
+        }
+      }
     }
-  }
-  uint32_t all[V];
+  } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) all[i] = key[i];
-  int mine = -1;
-  uint32_t mine_key = 0u, top = 0u;
+    for (int i = 0; i < V; ++i)
+      x[i] = i >= n ? -INFINITY
+             : BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.logits)[at + i])
+                    : static_cast<const float*>(a.logits)[at + i];
+  }
+  double c[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) c[i] = candidate(x[i], l * V + i);
+  sort_down(c);
+  double mine = 0.0, first = 0.0;
   for (int j = 0; j < r.topk; ++j) {
-    uint32_t best = key[0];
-    int at = 0;
+    const double most = over_lanes<L>(c[0]);
+    if (j == 0) first = most;
+    if (l == j) mine = most;
+    if (c[0] == most) {         // its next one; of more than 8 no more than the first 8 are taken
 #pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-      }
-    const uint32_t most = wave_umax(best);
-    if (j == 0) top = most;
-    if (most == 0u) break;
-    const int l = __ffsll((unsigned long long)__ballot(best == most)) - 1;
-    const int i = __builtin_amdgcn_readlane(at, l);
-    if (lane == j) {
-      mine = l * V + i;
-      mine_key = most;
-    }
-    if (lane == l) {
-#pragma unroll
-      for (int q = 0; q < V; ++q)
-        if (q == i) key[q] = 0u;
+      for (int i = 0; i < V - 1; ++i)
+        if (i < 8 || r.topk > 8) c[i] = c[i + 1];
+      if (V <= 8 || r.topk > 8) c[V - 1] = 0.0;
     }
   }
-  float w = 0.0f;
-  if (top != 0u) {
-    if (a.score == kSigmoid) {
-      const float z = key_logit(mine_key);
-      w = mine < 0 ? 0.0f : 1.0f / (1.0f + expf(-z));
-    } else {
-      const float big = key_logit(top);
-      const float own = mine < 0 ? 0.0f : expf(below(key_logit(mine_key), big));
-      float total = own;
-      if (a.score == kSoftmax) {
-        total = 0.0f;
+  const int e = candidate_expert(mine);
+  const float z = candidate_logit(mine), top = candidate_logit(first);
+  float w = 0.0f, total = 1.0f;
+  if (a.score == kSigmoid) {
+    // 1 / (1 + e^-z), by e^-|z|
+    const float p = exp_neg(fmaxf(-fabsf(z), -200.0f));
+    w = (z < 0.0f ? p : 1.0f) / (1.0f + p);
+  } else {
+    w = power(z, top);
+    float part = e < 0 ? 0.0f : w;
+    if (a.score == kSoftmax) {
+      part = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (all[i]) total += expf(below(key_logit(all[i]), big));
-      }
-      w = own / wave_fsum(total);
+      for (int i = 0; i < V; ++i)
+        if (x[i] > -INFINITY) part += power(x[i], top);
     }
+    total = over_lanes<L>(part);
   }
-  if (lane < r.topk) {
-    r.expert[(int64_t)m * r.topk + lane] = mine;
-    r.weight[(int64_t)m * r.topk + lane] = w * a.scale;
+  if (l < r.topk) {
+    r.expert[(int64_t)m * r.topk + l] = e;
+    r.weight[(int64_t)m * r.topk + l] = e < 0 ? 0.0f : w / total * a.scale;
   }
-  return mine;
+  return e;
 }
 
 // ---------------------------------------------------------------------------
 // plan: a stable counting sort of the pairs by expert
 // ---------------------------------------------------------------------------
+//
+// A workgroup takes some tokens, at most 1024 pairs: it chooses their experts, ranks each pair among
+// the workgroup's pairs of its expert and leaves the counts.  One workgroup's counts are the plan;
+// of several, a second launch adds those of earlier workgroups.
 
-constexpr int kPairs = 512;      // pairs of a workgroup
+constexpr int kPairs = 1024;     // threads, and most pairs of a workgroup
 constexpr int kWaves = kPairs / 64;
 
-// Lanes of the wave with the same expert (-1: none) as this one.
-__device__ __forceinline__ uint64_t same_expert(int e, int bits) {
+// Tokens of a workgroup: 64 (what its lanes choose for at once, up to 256 experts), more where
+// there would be more than 512 workgroups, whose counts each workgroup of the second launch reads.
+int tokens_of(int64_t tokens, int topk) {
+  const int64_t t = (tokens + 511) / 512, most = kPairs / topk;
+  return (int)(t > most ? most : t > 64 ? t : most < 64 ? most : 64);
+}
+
+// Lanes of the wave with the same expert as this one; none for -1.
+__device__ __forceinline__ uint64_t same_expert(int e, int experts) {
   uint64_t m = __ballot(e >= 0);
   if (e < 0) m = 0;
-  for (int b = 0; b < bits; ++b) {
+  for (int b = 0; (1 << b) < experts; ++b) {
     const uint64_t on = __ballot((e >> b) & 1);
     m &= ((e >> b) & 1) ? on : ~on;
   }
   return m;
 }
 
-// Counts the workgroup's pairs (one a thread, in order) by expert: count[wave][e] becomes the number
-// of the expert's pairs in earlier waves, total[e] of all; returns the pair's rank in its wave.
-__device__ __forceinline__ int count_pairs(int e, int experts, int* count, int* total) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  for (int i = tid; i < kWaves * experts; i += kPairs) count[i] = 0;
-  __syncthreads();
-  int bits = 0;
-  while ((1 << bits) < experts) ++bits;
-  const uint64_t m = same_expert(e, bits);
-  const int rank = __popcll(m & ((1ull << lane) - 1));
-  if (e >= 0 && rank == 0) count[wave * experts + e] = __popcll(m);
-  __syncthreads();
-  for (int x = tid; x < experts; x += kPairs) {
-    int n = 0;
-    for (int w = 0; w < kWaves; ++w) {
-      const int c = count[w * experts + x];
-      count[w * experts + x] = n;
-      n += c;
-    }
-    total[x] = n;
-  }
-  __syncthreads();
-  return rank;
-}
-
-__device__ __forceinline__ int pair_expert(const Routing& r, int p) {
-  if (p >= r.pairs) return -1;
-  const int e = r.expert[p];
-  return e >= 0 && e < r.experts ? e : -1;
-}
-
-template <int V, bool BF16>
-__global__ __launch_bounds__(256) void route_choose_kernel(const RouteArgs a) {
-  const int m = (int)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (m < a.r.tokens) choose<V, BF16>(a, m);
-}
-
-__global__ __launch_bounds__(kPairs) void route_count_kernel(const Routing r, int* hist) {
-  extern __shared__ int lds[];
-  int* total = lds + kWaves * r.experts;
-  count_pairs(pair_expert(r, (int)blockIdx.x * kPairs + threadIdx.x), r.experts, lds, total);
-  for (int x = threadIdx.x; x < r.experts; x += kPairs)
-    hist[(int64_t)blockIdx.x * r.experts + x] = total[x];
-}
-
-__global__ __launch_bounds__(kPairs) void route_place_kernel(const Routing r, const int* hist,
-                                                            int blocks) {
-  extern __shared__ int lds[];
-  int* total = lds + kWaves * r.experts;
-  int* first = total + r.experts;          // first slot of the expert's pairs of this workgroup
-  int* sums = first + r.experts;           // [kWaves]
-  const int tid = threadIdx.x, E = r.experts, b = (int)blockIdx.x;
-  const int p = b * kPairs + tid;
-  const int e = pair_expert(r, p);
-  const int rank = count_pairs(e, E, lds, total);
-  // pairs of each expert in all workgroups, and in earlier ones; then the experts' first slots
+// First slot of each expert from its pairs all(x) and those in earlier workgroups before(x): first[x] =
+// before(x) + the pairs of smaller experts.  Returns the number of all pairs.  sums: [kWaves].
+template <typename All, typename Before>
+__device__ __forceinline__ int first_slots(const Routing& r, All all, Before before, int* first, int* sums,
+                                           bool writes) {
+  const int tid = threadIdx.x;
   int base = 0;
-  for (int x0 = 0; x0 < E; x0 += kPairs) {
-    const int x = x0 + tid;
-    int all = 0, before = 0;
-    if (x < E)
-      for (int q = 0; q < blocks; ++q) {
-        const int c = hist[(int64_t)q * E + x];
-        all += c;
-        if (q < b) before += c;
-      }
-    const int upto = wave_scan(all);
+  for (int x0 = 0; x0 < r.experts; x0 += kPairs) {
+    const int x = x0 + tid, n = x < r.experts ? all(x) : 0;
+    const int upto = wave_scan(n);
     if ((tid & 63) == 63) sums[tid >> 6] = upto;
     __syncthreads();
     int add = base;
-    for (int w = 0; w < (tid >> 6); ++w) add += sums[w];
-    if (x < E) first[x] = add + upto - all + before;
-    if (b == 0 && x < E) {
-      if (x == 0) r.offset[0] = 0;
-      r.offset[x + 1] = add + upto;
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < (tid >> 6)) add += sums[w];
+      base += sums[w];
     }
-    for (int w = 0; w < kWaves; ++w) base += sums[w];
+    if (x < r.experts) {
+      first[x] = add + upto - n + before(x);
+      if (writes) {
+        if (x == 0) r.offset[0] = 0;
+        r.offset[x + 1] = add + upto;
+      }
+    }
     __syncthreads();
   }
-  if (p < r.pairs) {
-    int slot = -1;
-    if (e >= 0) {
-      slot = first[e] + lds[(tid >> 6) * E + e] + rank;
-      r.pair[slot] = p;
-    }
-    r.slot[p] = slot;
-    if (p >= base) r.pair[p] = -1;         // slots behind the last pair
+  return base;
+}
+
+__device__ __forceinline__ void place(const Routing& r, int p, int e, int rank, const int* first, int used) {
+  int slot = -1;
+  if (e >= 0) {
+    slot = first[e] + rank;
+    r.pair[slot] = p;
   }
+  r.slot[p] = slot;
+  if (p >= used) r.pair[p] = -1;         // places behind the last slot
+}
+
+// L = 0: the experts are given.  ONE: one workgroup has all pairs; otherwise slot[] holds each
+// pair's rank in its workgroup, and hist [workgroups][experts rounded up to 8] its counts.
+template <int L, int V, bool BF16, bool ONE>
+__global__ __launch_bounds__(kPairs) void route_kernel(const RouteArgs a, int tokens, uint16_t* hist) {
+  extern __shared__ int lds[];
+  const Routing& r = a.r;
+  const int E = r.experts, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int* count = lds;                      // [kWaves][E]: the expert's pairs in the wave, then in earlier ones
+  int* total = count + kWaves * E;       // [E]
+  int* first = total + E;                // [E]
+  int* sums = first + E;                 // [kWaves]
+  int* chosen = sums + kWaves;           // [kPairs]
+  const int m0 = (int)blockIdx.x * tokens, m1 = min(m0 + tokens, r.tokens);
+  const int pairs = (m1 - m0) * r.topk, p = m0 * r.topk + tid;
+  for (int i = tid; i < kWaves * E; i += kPairs) count[i] = 0;
+  int e = -1;
+  if constexpr (L == 0) {
+    if (tid < pairs) e = r.expert[p];
+    if (e >= E) e = -1;
+  } else {
+    for (int m = m0 + tid / L; m < m1; m += kPairs / L) {
+      const int c = choose<L, V, BF16>(a, m);
+      if ((tid & (L - 1)) < r.topk) chosen[(m - m0) * r.topk + (tid & (L - 1))] = c;
+    }
+  }
+  __syncthreads();
+  if (L != 0 && tid < pairs) e = chosen[tid];
+  const uint64_t same = same_expert(e, E);
+  int rank = __popcll(same & ((1ull << lane) - 1));
+  if (e >= 0 && rank == 0) count[wave * E + e] = __popcll(same);
+  __syncthreads();
+  for (int x = tid; x < E; x += kPairs) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const int c = count[w * E + x];
+      count[w * E + x] = n;
+      n += c;
+    }
+    total[x] = n;
+    if (!ONE) hist[(size_t)blockIdx.x * ((E + 7) & ~7) + x] = (uint16_t)n;
+  }
+  __syncthreads();
+  if (e >= 0) rank += count[wave * E + e];
+  if constexpr (ONE) {
+    const int used = first_slots(r, [&](int x) { return total[x]; }, [](int) { return 0; }, first, sums, true);
+    if (tid < pairs) place(r, p, e, rank, first, used);
+  } else {
+    if (tid < pairs) r.slot[p] = rank;
+  }
+}
+
+__global__ __launch_bounds__(kPairs) void route_place_kernel(const Routing r, int tokens,
+                                                            const uint16_t* hist, int blocks) {
+  extern __shared__ int lds[];
+  const int E = r.experts, E8 = (E + 7) & ~7, tid = threadIdx.x, b = (int)blockIdx.x;
+  int *all = lds, *before = all + E8, *first = before + E8, *sums = first + E;
+  for (int i = tid; i < 2 * E8; i += kPairs) lds[i] = 0;
+  const int m0 = b * tokens, pairs = (min(m0 + tokens, r.tokens) - m0) * r.topk, p = m0 * r.topk + tid;
+  int e = -1, rank = 0;
+  if (tid < pairs) {
+    e = r.expert[p];
+    if (e >= E) e = -1;
+    rank = r.slot[p];
+  }
+  __syncthreads();
+  // a thread adds 8 experts' counts of every (groups)th workgroup, 8 loads in flight
+  const int per = E8 / 8, groups = min(kPairs / per, 64), g = tid / per, x8 = tid - g * per;
+  if (g < groups) {
+    int na[8] = {}, nb[8] = {};
+    for (int q0 = g; q0 < blocks; q0 += 8 * groups) {
+      uint4 u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int q = q0 + j * groups;
+        u[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (q < blocks) u[j] = *reinterpret_cast<const uint4*>(hist + (size_t)q * E8 + 8 * x8);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t d[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = (int)((d[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+          na[i] += c;
+          nb[i] += q0 + j * groups < b ? c : 0;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (8 * x8 + i < E) {      // (counts behind the last expert were not written)
+        atomicAdd(&all[i * per + x8], na[i]);       // neighbouring lanes in neighbouring banks
+        atomicAdd(&before[i * per + x8], nb[i]);
+      }
+  }
+  __syncthreads();
+  const int used = first_slots(r, [&](int x) { return all[(x & 7) * per + (x >> 3)]; },
+                               [&](int x) { return before[(x & 7) * per + (x >> 3)]; }, first, sums, b == 0);
+  if (tid < pairs) place(r, p, e, rank, first, used);
 }
 
 // ---------------------------------------------------------------------------
 // combination
 // ---------------------------------------------------------------------------
 
-template <bool YB, bool OB>
-__global__ __launch_bounds__(256) void combine_kernel(const Routing r, const void* y, int64_t K,
-                                                      const void* residual, void* out) {
-  const int64_t total = (int64_t)r.tokens * K;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t m = i / K, k = i - m * K;
-    float v = 0.0f;
-    if (residual)
-      v = OB ? bf16_bits_to_float(static_cast<const uint16_t*>(residual)[i])
-             : static_cast<const float*>(residual)[i];
-    for (int j = 0; j < r.topk; ++j) {
-      const int s = r.slot[m * r.topk + j];
-      if (s < 0 || s >= r.pairs) continue;
-      const int64_t o = (int64_t)s * K + k;
-      const float x = YB ? bf16_bits_to_float(static_cast<const uint16_t*>(y)[o])
-                         : static_cast<const float*>(y)[o];
-      v = v + r.weight[m * r.topk + j] * x;
+// A workgroup takes a token's columns, W = 8 of them (or 1, unaligned) a thread, and the rows of four
+// choices at once, so that their loads overlap; which rows they are is the same for all threads.
+template <bool BF16, int W>
+__device__ __forceinline__ void load_cols(const void* p, int64_t at, float (&v)[W]) {
+  if constexpr (W == 1) {
+    v[0] = BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p)[at]) : static_cast<const float*>(p)[at];
+  } else if constexpr (BF16) {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    const uint32_t d[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(d[i] << 16);
+      v[2 * i + 1] = __uint_as_float(d[i] & 0xffff0000u);
     }
-    if (OB)
-      static_cast<uint16_t*>(out)[i] = float_to_bf16_rne(v);
-    else
-      static_cast<float*>(out)[i] = v;
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 u = q[i];
+      v[4 * i] = u.x;
+      v[4 * i + 1] = u.y;
+      v[4 * i + 2] = u.z;
+      v[4 * i + 3] = u.w;
+    }
   }
 }
 
-int route_blocks(int64_t pairs) { return (int)((pairs + kPairs - 1) / kPairs); }
+template <bool YB, bool OB, int W>
+__global__ __launch_bounds__(256) void combine_kernel(const Routing r, const void* y, int64_t K,
+                                                      const void* residual, void* out, int parts) {
+  const int64_t m = blockIdx.x / (unsigned)parts;
+  const int64_t k = ((int64_t)(blockIdx.x % (unsigned)parts) * blockDim.x + threadIdx.x) * W;
+  if (k >= K) return;
+  float v[W] = {};
+  if (residual) load_cols<OB, W>(residual, m * K + k, v);
+  const int32_t* slot = r.slot + m * r.topk;
+  const float* weight = r.weight + m * r.topk;
+  for (int j0 = 0; j0 < r.topk; j0 += 4) {
+    float x[4][W], w[4];
+    bool on[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      on[j] = false;
+      if (j0 + j < r.topk) {
+        const int s = slot[j0 + j];
+        on[j] = s >= 0 && s < r.pairs;
+        w[j] = weight[j0 + j];
+        if (on[j]) load_cols<YB, W>(y, (int64_t)s * K + k, x[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (on[j]) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = v[i] + w[j] * x[j][i];
+      }
+  }
+  if constexpr (W == 1) {
+    if (OB)
+      static_cast<uint16_t*>(out)[m * K + k] = float_to_bf16_rne(v[0]);
+    else
+      static_cast<float*>(out)[m * K + k] = v[0];
+  } else if constexpr (OB) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + m * K + k) =
+        make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+  } else {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + m * K + k);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+int route_blocks(int64_t tokens, int topk) {
+  const int t = tokens_of(tokens, topk);
+  return (int)((tokens + t - 1) / t);
+}
+
+template <int L, int V, bool BF16>
+void launch_first(const RouteArgs& a, int blocks, uint16_t* hist, hipStream_t s) {
+  const size_t lds = ((kWaves + 2) * a.r.experts + kWaves + kPairs) * sizeof(int);
+  const int tokens = tokens_of(a.r.tokens, a.r.topk);
+  if (blocks <= 1)
+    hipLaunchKernelGGL((route_kernel<L, V, BF16, true>), dim3(1), dim3(kPairs), lds, s, a, tokens, hist);
+  else
+    hipLaunchKernelGGL((route_kernel<L, V, BF16, false>), dim3(blocks), dim3(kPairs), lds, s, a, tokens, hist);
+}
+
+template <bool BF16>
+void launch_choice(const RouteArgs& a, int blocks, uint16_t* hist, hipStream_t s) {
+  const int E = a.r.experts;
+  if (a.r.topk <= 16 && E <= 64)
+    launch_first<16, 4, BF16>(a, blocks, hist, s);
+  else if (a.r.topk <= 16 && E <= 256)
+    launch_first<16, 16, BF16>(a, blocks, hist, s);
+  else if (E <= 512)
+    launch_first<32, 16, BF16>(a, blocks, hist, s);
+  else
+    launch_first<64, 16, BF16>(a, blocks, hist, s);
+}
 
 }  // namespace
 
 size_t route_workspace_bytes(int64_t tokens, int topk, int experts) {
-  return (size_t)route_blocks(tokens * topk) * experts * sizeof(int);
+  const int blocks = route_blocks(tokens, topk);
+  return blocks <= 1 ? 0 : (size_t)blocks * ((experts + 7) & ~7) * sizeof(uint16_t);
 }
 
 hipError_t launch_route(const Routing& r, const void* logits, bool bf16, int64_t stride, int score,
                         float scale, void* workspace, hipStream_t s) {
-  if (logits && r.tokens > 0) {
-    const RouteArgs a{r, logits, stride, score, scale};
-    const dim3 grid((unsigned)((r.tokens + 3) / 4));
-#define BITNET_CHOOSE(V)                                                                      \
-  if (bf16)                                                                                   \
-    hipLaunchKernelGGL((route_choose_kernel<V, true>), grid, dim3(256), 0, s, a);             \
-  else                                                                                        \
-    hipLaunchKernelGGL((route_choose_kernel<V, false>), grid, dim3(256), 0, s, a)
-    if (r.experts <= 64) {
-      BITNET_CHOOSE(1);
-    } else if (r.experts <= 256) {
-      BITNET_CHOOSE(4);
-    } else {
-      BITNET_CHOOSE(16);
-    }
-#undef BITNET_CHOOSE
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  const int blocks = route_blocks(r.pairs);    // (0 without tokens: the offsets are written)
-  int* hist = static_cast<int*>(workspace);
-  if (blocks > 0) {
-    hipLaunchKernelGGL(route_count_kernel, dim3(blocks), dim3(kPairs),
-                       (kWaves + 1) * r.experts * sizeof(int), s, r, hist);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(route_place_kernel, dim3(blocks > 0 ? blocks : 1), dim3(kPairs),
-                     ((kWaves + 2) * r.experts + kWaves) * sizeof(int), s, r, hist, blocks);
+  const int blocks = route_blocks(r.tokens, r.topk);     // (0 without tokens: the offsets are written)
+  uint16_t* hist = static_cast<uint16_t*>(workspace);
+  const RouteArgs a{r, logits, stride, score, scale};
+  if (!logits)
+    launch_first<0, 1, false>(a, blocks, hist, s);
+  else if (bf16)
+    launch_choice<true>(a, blocks, hist, s);
+  else
+    launch_choice<false>(a, blocks, hist, s);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || blocks <= 1) return e;
+  const int E8 = (r.experts + 7) & ~7;
+  hipLaunchKernelGGL(route_place_kernel, dim3(blocks), dim3(kPairs), (2 * E8 + r.experts + kWaves) * sizeof(int), s,
+                     r, tokens_of(r.tokens, r.topk), hist, blocks);
   return hipGetLastError();
 }
 
+namespace {
+template <int W>
+hipError_t launch_combine_w(const Routing& r, const void* y, bool y_bf16, int64_t K, const void* residual,
+                            void* out, bool out_bf16, hipStream_t s) {
+  const int64_t cols = (K + W - 1) / W;
+  const int threads = cols >= 256 ? 256 : (int)((cols + 63) / 64) * 64;
+  const int64_t parts = (cols + threads - 1) / threads;
+  if ((int64_t)r.tokens * parts > max_grid(256)) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)(r.tokens * parts)), block(threads);
+#define BITNET_COMBINE(YB, OB) \
+  hipLaunchKernelGGL((combine_kernel<YB, OB, W>), grid, block, 0, s, r, y, K, residual, out, (int)parts)
+  if (y_bf16 && out_bf16)
+    BITNET_COMBINE(true, true);
+  else if (y_bf16)
+    BITNET_COMBINE(true, false);
+  else if (out_bf16)
+    BITNET_COMBINE(false, true);
+  else
+    BITNET_COMBINE(false, false);
+#undef BITNET_COMBINE
+  return hipGetLastError();
+}
+}  // namespace
+
+bool combine_fits(int64_t tokens, int64_t K) { return tokens * ((K + 255) / 256) <= max_grid(256); }
+
 hipError_t launch_combine(const Routing& r, const void* y, bool y_bf16, int64_t K,
                           const void* residual, void* out, bool out_bf16, hipStream_t s) {
-  int64_t blocks = ((int64_t)r.tokens * K + 255) / 256;
-  if (blocks > 65536) blocks = 65536;
-  const dim3 grid((unsigned)blocks);
-  if (y_bf16 && out_bf16)
-    hipLaunchKernelGGL((combine_kernel<true, true>), grid, dim3(256), 0, s, r, y, K, residual, out);
-  else if (y_bf16)
-    hipLaunchKernelGGL((combine_kernel<true, false>), grid, dim3(256), 0, s, r, y, K, residual, out);
-  else if (out_bf16)
-    hipLaunchKernelGGL((combine_kernel<false, true>), grid, dim3(256), 0, s, r, y, K, residual, out);
-  else
-    hipLaunchKernelGGL((combine_kernel<false, false>), grid, dim3(256), 0, s, r, y, K, residual, out);
-  return hipGetLastError();
+  const uintptr_t at = reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(residual) |
+                       reinterpret_cast<uintptr_t>(out);
+  return K % 8 == 0 && (at & 15) == 0 ? launch_combine_w<8>(r, y, y_bf16, K, residual, out, out_bf16, s)
+                                      : launch_combine_w<1>(r, y, y_bf16, K, residual, out, out_bf16, s);
 }
 
 }  // namespace bitnet

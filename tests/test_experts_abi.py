@@ -65,7 +65,7 @@ def test_route_workspace(lib):   # noqa: F811
     need = lib.bitnet_route_workspace_bytes(100000, 2, 8)
     assert need > 0 and lib.bitnet_route_workspace_bytes(0, 2, 8) == 0
     assert route(lib, r, ws=None) == EWS and route(lib, r, ws_bytes=need - 1) == EWS
-    assert route(lib, r, ws=A + 2, ws_bytes=need) == EALIGN
+    assert route(lib, r, ws=A + 8, ws_bytes=need) == EALIGN
 
 
 BAD_PRODUCT = [
