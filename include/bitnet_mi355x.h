@@ -712,7 +712,7 @@ bitnet_status bitnet_ternary_linear_act(const bitnet_product *product, hipStream
 /*
  * The products of each expert with its slots: y[s] for slot s of expert e is the product of
  * matrix e with the slot's input row.
- *   by_slot  0: input row pair[s] / topk (x_q has routing->tokens rows, tokens * K < 2^32);
+ *   by_slot  0: input row pair[s] / topk (x_q has routing->tokens rows, tokens * K <= 2^31);
  *            1: input row s (x_q has tokens * topk rows).  product->rows has to say the same.
  *   product  as above, without residual.  Rows of y behind the last slot are left as they are.
  * Of the routing offset and pair are read (pair with by_slot 0).

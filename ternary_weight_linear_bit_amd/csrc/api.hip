@@ -863,7 +863,7 @@ bitnet_status bitnet_expert_linear(const bitnet_routing* routing, const bitnet_p
   const bitnet_status st = check_product(*product, pairs, &nothing);
   if (st != BITNET_OK) return st;
   if (product->rows != (by_slot ? pairs : r.tokens) || product->residual ||
-      (!by_slot && r.tokens * product->K >= ((int64_t)1 << 32)))
+      (!by_slot && r.tokens * product->K > ((int64_t)1 << 31)))
     return BITNET_ERR_SHAPE;
   if (nothing) return BITNET_OK;
   if (!r.offset || (!by_slot && !r.pair)) return BITNET_ERR_NULL;

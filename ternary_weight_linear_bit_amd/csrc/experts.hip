@@ -16,16 +16,17 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 // few rows an expert: the weights stream once from memory
 // ---------------------------------------------------------------------------
 //
-// A workgroup takes 32 output rows of one expert (of both its matrices) and up to 32 slots; its W
-// waves share the k steps, and their integer sums meet in LDS (order does not matter to them).
-// Lane (r, h) of the 32 x 32 x 32 product holds row r: weights as the layout's 16 bytes a lane,
-// the slots' rows straight from memory (a few KiB that all workgroups share; lanes without a slot
-// read the first slot's, and nothing of theirs is kept).
-constexpr int kFewRows = 32;
+// A workgroup takes up to 32 slots of one expert and 32 output rows (of both its matrices); its 8
+// waves share the k steps, S of them in flight a wave, and their integer sums meet in LDS (order
+// does not matter to them).  Lane (r, h) of the 32 x 32 x 32 product holds row r: weights as the
+// layout's 16 bytes a lane, the slots' rows straight from memory (a few KiB that all workgroups
+// share; lanes without a slot read another's, and nothing of theirs is kept).  Past the end of K, and
+// in steps past the last, x is read outside its buffer, which gives zeros.
+constexpr int kFewRows = 32, kFewWaves = 8;
 
-template <int W, bool GATED>
-__global__ __launch_bounds__(64 * W) void experts_few_kernel(const ExpertArgs a, int nblocks) {
-  constexpr int NM = GATED ? 2 : 1;
+template <int S, bool GATED>
+__global__ __launch_bounds__(64 * kFewWaves) void experts_few_kernel(const ExpertArgs a, int nblocks) {
+  constexpr int NM = GATED ? 2 : 1, W = kFewWaves;
   __shared__ int sum[NM][kFewRows][33];
   __shared__ int row_of[kFewRows];
   __shared__ float d_of[kFewRows];
@@ -33,35 +34,57 @@ __global__ __launch_bounds__(64 * W) void experts_few_kernel(const ExpertArgs a,
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
   const int nb = (int)blockIdx.x % nblocks;
-  const ExpertTile t = expert_tile<kFewRows>(a, (int)blockIdx.x / nblocks);
-  if (t.rows <= 0) return;
-  const int steps = (a.K + 127) / 128;
-  const size_t at = ((size_t)t.expert * nblocks + nb) * steps * 1024;
-  const uint4* wp[2] = {reinterpret_cast<const uint4*>(a.w + at) + lane,
-                        reinterpret_cast<const uint4*>((GATED ? a.up : a.w) + at) + lane};
+  const int tile = (int)blockIdx.x / nblocks;
+  const ExpertSpan t = expert_span<kFewRows>(a, tile);
+  if (t.n == 0) return;
+  const int slot0 = t.slot0 + (tile - t.tile0) * kFewRows, rows = min(t.slot0 + t.n - slot0, kFewRows);
+  const int K = a.K, steps = (K + 127) / 128;
+  const uint32_t bytes = (uint32_t)steps * 1024u;
+  const size_t at = ((size_t)t.expert * nblocks + nb) * bytes;
+  __amdgpu_buffer_rsrc_t wr[NM];
+  wr[0] = make_uniform_rsrc(a.w + at, bytes);
+  if (GATED) wr[NM - 1] = make_uniform_rsrc(a.up + at, bytes);
+  uint4 wv[S][NM];
+  v4i xv[S][4];
+  auto wload = [&](int i, int s) {
+#pragma unroll
+    for (int m = 0; m < NM; ++m) wv[i][m] = bload16_nt(wr[m], (uint32_t)s * 1024u + 16u * (uint32_t)lane);
+  };
+#pragma unroll
+  for (int i = 0; i < S; ++i) wload(i, wave + i * W);     // these need the expert alone
+  const bool gather = a.pair != nullptr;
+  const int mine = r < rows ? input_row(a, slot0 + r) : -1;
+  const auto xr = gather ? make_uniform_rsrc(a.xq, (uint32_t)((int64_t)a.rows * K))
+                         : make_uniform_rsrc(a.xq + (size_t)slot0 * K, (uint32_t)(rows * K));
+  const uint32_t xo = (uint32_t)(gather ? max(mine, 0) : min(r, rows - 1)) * (uint32_t)K + 64u * (uint32_t)h;
+  auto xload = [&](int i, int s) {
+    const uint32_t o = 128 * s + 64 * h < K ? xo + 128u * (uint32_t)s : kOob;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      xv[i][j] = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(o + 16u * (uint32_t)j), 0, 0);
+  };
+#pragma unroll
+  for (int i = 0; i < S; ++i) xload(i, wave + i * W);
   for (int i = tid; i < NM * kFewRows * 33; i += 64 * W) (&sum[0][0][0])[i] = 0;
-  const int mine = r < t.rows ? input_row(a, t.slot0 + r) : -1;
   if (wave == 0 && h == 0) {
     row_of[r] = mine;
     d_of[r] = mine < 0 ? 0.0f : a.xs[mine];
   }
-  const int8_t* x = a.xq + (size_t)max(mine, 0) * a.K;
   v16i acc[NM];
 #pragma unroll
   for (int m = 0; m < NM; ++m) acc[m] = (v16i){};
-  for (int s = wave; s < steps; s += W) {
-    const int k = 128 * s + 64 * h;
-    const int8_t* xk = x + (k < a.K ? k : 0);      // past K the weights are 0
-    v4i xv[4];
+  for (int s = wave; s < steps; s += S * W) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) xv[j] = *reinterpret_cast<const v4i*>(xk + 16 * j);
+    for (int i = 0; i < S; ++i) {
 #pragma unroll
-    for (int m = 0; m < NM; ++m) {
-      const uint4 w = wp[m][(size_t)s * 64];
-      const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+      for (int m = 0; m < NM; ++m) {
+        const uint32_t wd[4] = {wv[i][m].x, wv[i][m].y, wv[i][m].z, wv[i][m].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(xv[j], weights_64(wd[j]), acc[m], 0, 0, 0);
+        for (int j = 0; j < 4; ++j)
+          acc[m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(xv[i][j], weights_64(wd[j]), acc[m], 0, 0, 0);
+      }
+      wload(i, s + (i + S) * W);
+      xload(i, s + (i + S) * W);
     }
   }
   __syncthreads();
@@ -71,56 +94,77 @@ __global__ __launch_bounds__(64 * W) void experts_few_kernel(const ExpertArgs a,
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
       const int sl = 8 * (v >> 2) + 4 * h + (v & 3);
-      if (sl < t.rows) atomicAdd(&sum[m][sl][r], acc[m][v]);
+      if (sl < rows) atomicAdd(&sum[m][sl][r], acc[m][v]);
     }
   __syncthreads();
-  const int n = 32 * nb + (tid & 31);
+  const int c = tid & 31, n = 32 * nb + c;
   if (n >= a.N) return;
   const size_t en = (size_t)t.expert * a.N + n;
   const float g0 = a.w_scale[t.expert], b0 = a.bias ? a.bias[en] : 0.0f;
   const float g1 = GATED ? a.up_scale[t.expert] : 0.0f, b1 = GATED && a.up_bias ? a.up_bias[en] : 0.0f;
-  for (int sl = tid >> 5; sl < t.rows; sl += 2 * W) {
+  for (int sl = tid >> 5; sl < rows; sl += 2 * W) {
     if (row_of[sl] < 0) continue;
     const float d = d_of[sl];
-    float v = acc_64(sum[0][sl][tid & 31]) * (g0 * d);
+    float v = acc_64(sum[0][sl][c]) * (g0 * d);
     if (a.bias) v = v + b0;
     v = activate(v, a.act);
     if (GATED) {
-      float u = acc_64(sum[NM - 1][sl][tid & 31]) * (g1 * d);
+      float u = acc_64(sum[NM - 1][sl][c]) * (g1 * d);
       if (a.up_bias) u = u + b1;
       v = v * u;
     }
-    const size_t o = (size_t)(t.slot0 + sl) * a.N + n;
-    store_output(a, o, v);
+    store_output(a, (size_t)(slot0 + sl) * a.N + n, v);
   }
 }
 
-int64_t few_grid(const ExpertArgs& a) {
-  return many_tiles(a, kFewRows) * ((a.N + 31) / 32);
+int64_t few_grid(const ExpertArgs& a) { return many_tiles(a, kFewRows) * ((a.N + 31) / 32); }
+
+template <int S>
+hipError_t launch_few(const ExpertArgs& a, hipStream_t s) {
+  const int nblocks = (a.N + 31) / 32;
+  const dim3 grid((unsigned)few_grid(a)), block(64 * kFewWaves);
+  if (a.up)
+    hipLaunchKernelGGL((experts_few_kernel<S, true>), grid, block, 0, s, a, nblocks);
+  else
+    hipLaunchKernelGGL((experts_few_kernel<S, false>), grid, block, 0, s, a, nblocks);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-bool experts_fit(const ExpertArgs& a) { return few_grid(a) <= max_grid(512); }
+// (the other kernels' grids are smaller, but for rounding up to the XCDs)
+bool experts_fit(const ExpertArgs& a) { return few_grid(a) + 8 <= max_grid(64 * kFewWaves); }
 
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s) {
-  // tiles of each shape, if the slots were spread evenly over the experts
-  const int64_t used = a.experts < a.slots ? a.experts : a.slots, each = (a.slots + used - 1) / used;
-  auto tiles = [&](int rows, int cols) {
-    return used * ((each + rows - 1) / rows) * ((a.N + cols - 1) / cols);
+  // The kernel is chosen for slots spread evenly over the experts; how they are spread is known
+  // on the device alone.  An expert's last tile is half full on average.
+  const int64_t used = a.experts < a.slots ? a.experts : a.slots;
+  const double each = (double)a.slots / (double)used;
+  auto tiles = [&](int rows) {
+    if (!a.offset) return (double)((a.slots + rows - 1) / rows);
+    const double t = each / rows + 0.5;
+    return (double)used * (t < 1.0 ? 1.0 : t);
   };
-  const int wide = a.up ? 128 : 256;
-  if (each > 8 && tiles(kFewRows, 32) > 512) {
-    if (each >= 192 && tiles(128, wide) >= 256) return launch_experts_many(a, 128, s);
-    return launch_experts_many(a, tiles(64, wide) >= 256 ? 64 : 32, s);
-  }
-  const int nblocks = (a.N + 31) / 32;
-  const dim3 grid((unsigned)few_grid(a));
-  if (a.up)
-    hipLaunchKernelGGL((experts_few_kernel<8, true>), grid, dim3(512), 0, s, a, nblocks);
-  else
-    hipLaunchKernelGGL((experts_few_kernel<8, false>), grid, dim3(512), 0, s, a, nblocks);
-  return hipGetLastError();
+  const int blocks = (a.N + 31) / 32, weights = a.up ? 2 * blocks : blocks, steps = (a.K + 127) / 128;
+  auto groups = [&](int rows, int wide) { return tiles(rows) * ((weights + wide - 1) / wide); };
+  // Few rows: one block of weights a workgroup, while that gives at most a workgroup a compute
+  // unit (two where the rows are few, and one with few or short rows, whose loads are its cost).
+  const double few = tiles(kFewRows) * blocks;
+  if ((few <= 256 && (each <= 16 || steps <= 64)) || (few <= 512 && each <= 8))
+    return steps > 32 ? launch_few<2>(a, s) : launch_few<1>(a, s);
+  // 32 slots, and the k steps shared by eight or four groups of waves while the workgroups do
+  // not fill the compute units otherwise
+  if (groups(32, 2) <= 256) return launch_experts_many(a, kMany32x2, s);
+  if (groups(32, 4) <= 256) return launch_experts_many(a, kMany32x4, s);
+  // 32, 64 or 128 slots x 8 blocks: the least of rounds times a round's time (us a step, measured),
+  // a partly filled last round counting whole while rounds are few
+  auto time = [&](int rows, double step) {
+    const double r = groups(rows, 8) / 256;
+    return step * (r <= 1 ? 1 : r <= 2 ? 2 : r <= 3 ? 3 : r + 0.4);
+  };
+  const double t32 = time(32, 0.26), t64 = time(64, 0.49), t128 = time(128, 0.85);
+  if (t32 <= t64 && t32 <= t128) return launch_experts_many(a, kMany32, s);
+  return launch_experts_many(a, t64 <= t128 ? kMany64 : kMany128, s);
 }
 
 }  // namespace bitnet

@@ -47,8 +47,10 @@ inline int64_t many_tiles(const ExpertArgs& a, int rows) {
   return a.offset ? expert_tiles(a.slots, a.experts, rows) : ((int64_t)a.slots + rows - 1) / rows;
 }
 bool experts_fit(const ExpertArgs& a);
-// Few rows an expert (experts.hip), many (experts_many.hip; tiles of bm slots).
-hipError_t launch_experts_many(const ExpertArgs& a, int bm, hipStream_t s);
+// Tiles of the kernel for many rows (experts_many.hip): slots, by 8 blocks of 32 weight rows, or by
+// 2 and 4 with the k steps shared by 8 and 4 groups of waves.
+enum ManyTile { kMany32x2, kMany32x4, kMany32, kMany64, kMany128 };
+hipError_t launch_experts_many(const ExpertArgs& a, ManyTile tile, hipStream_t s);
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
 
 // out[m] = residual[m] + sum_j weight[m][j] y[slot[m][j]].
@@ -56,27 +58,27 @@ bool combine_fits(int64_t tokens, int64_t K);
 hipError_t launch_combine(const Routing& r, const void* y, bool y_bf16, int64_t K,
                           const void* residual, void* out, bool out_bf16, hipStream_t s);
 
-// Tile t of the experts' slots cut into tiles of `rows`: its expert, first slot and rows (0: none).
-// The offsets lie in device memory, where the host cannot check them: they are clamped to the
-// batch.  A wave reads 64 experts' offsets at once.
-struct ExpertTile {
-  int expert, slot0, rows;
+// The expert that tile t belongs to, where each expert's slots are cut into tiles of ROWS: its first
+// slot, its slots (0: there is no such tile) and its first tile.  The offsets lie in device memory,
+// where the host cannot check them: they are clamped to the batch.  A wave reads 64 experts' offsets
+// at once.
+struct ExpertSpan {
+  int expert, slot0, n, tile0;
 };
-__device__ __forceinline__ int wave_scan(int v) {   // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(v, o, 64);
-    if (lane >= o) v += u;
-  }
+__device__ __forceinline__ int wave_scan(int v) {   // inclusive; within rows of 16 lanes, then across
+#define BITNET_SCAN(ctrl, rows) v += __builtin_amdgcn_update_dpp(0, v, ctrl, rows, 0xf, false)
+  BITNET_SCAN(0x111, 0xf);
+  BITNET_SCAN(0x112, 0xf);
+  BITNET_SCAN(0x114, 0xf);
+  BITNET_SCAN(0x118, 0xf);
+  BITNET_SCAN(0x142, 0xa);
+  BITNET_SCAN(0x143, 0xc);
+#undef BITNET_SCAN
   return v;
 }
 template <int ROWS>
-__device__ __forceinline__ ExpertTile expert_tile(const ExpertArgs& a, int t) {
-  if (!a.offset) {
-    const int s0 = t * ROWS;
-    return {0, s0, max(min(a.slots - s0, ROWS), 0)};
-  }
+__device__ __forceinline__ ExpertSpan expert_span(const ExpertArgs& a, int t) {
+  if (!a.offset) return {0, 0, t * (int64_t)ROWS < a.slots ? a.slots : 0, 0};
   const int lane = threadIdx.x & 63;
   for (int e0 = 0, base = 0; e0 < a.experts; e0 += 64) {
     const int e = e0 + lane;
@@ -90,16 +92,12 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertArgs& a, int t) {
     const uint64_t past = __ballot(upto > t);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
-      const int i = t - (__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l));
-      ExpertTile r;
-      r.expert = e0 + l;
-      r.slot0 = __builtin_amdgcn_readlane(lo, l) + i * ROWS;
-      r.rows = min(__builtin_amdgcn_readlane(n, l) - i * ROWS, ROWS);
-      return r;
+      return {e0 + l, __builtin_amdgcn_readlane(lo, l), __builtin_amdgcn_readlane(n, l),
+              __builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(tiles, l)};
     }
     base = __builtin_amdgcn_readlane(upto, 63);
   }
-  return {0, 0, 0};
+  return {0, 0, 0, 0};
 }
 // Tiles of all experts.
 template <int ROWS>
@@ -154,8 +152,20 @@ __device__ __forceinline__ float activate(float v, int act) {
       const float e = exp_neg(-fabsf(v));
       return (v < 0.0f ? v * e : v) * __builtin_amdgcn_rcpf(1.0f + e);
     }
-    case kActGelu:        // v times the normal distribution's integral up to v
-      return v * (0.5f * erfcf(v * -0x1.6a09e6p-1f));
+    case kActGelu: {      // v times the normal distribution's integral up to v
+      // integral up to -a = e^(-a^2 / 2) t Q(t), t = 1 / (1 + 0.28 a): a fit of the least largest error
+      // over a in [0, 6], 9.3e-9, by weighted least squares (Lawson's method)
+      const float a = fabsf(v);
+      const float t = __builtin_amdgcn_rcpf(fmaf(a, 0.28f, 1.0f));
+      float q = -0x1.b163fcp-4f;
+      q = fmaf(q, t, 0x1.8f3b24p-2f);
+      q = fmaf(q, t, -0x1.e55cd8p-3f);
+      q = fmaf(q, t, 0x1.135d3p-2f);
+      q = fmaf(q, t, 0x1.147778p-4f);
+      q = fmaf(q, t, 0x1.dd44e4p-4f);
+      q = q * t * __builtin_amdgcn_exp2f(a * a * -0x1.715476p-1f);
+      return v * (v < 0.0f ? q : 1.0f - q);
+    }
     default:
       return v;
   }

@@ -1,8 +1,8 @@
 // Experts' products with many rows: int8 contraction on the matrix cores.
 //
 // A workgroup takes BM slots of one expert and 64 WN rows of weights (of gate and up 32 WN each, so
-// that a lane holds both values of an output and the activation needs no memory); 2 WN waves,
-// each with (BM / 2) slots x 64 rows as 32 x 32 blocks of int32 sums.  K advances in steps of 128:
+// that a lane holds both values of an output and the activation needs no memory), in 32 x 32 blocks
+// of int32 sums.  K advances in steps of 128:
 //  * the slots' rows, gathered, are staged in LDS (two buffers, a barrier a step), step s + 1
 //    between the matrix instructions of step s;
 //  * each wave loads its weights straight from memory, 1 KiB a load, and expands them with a
@@ -18,6 +18,7 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 
 constexpr int kXcds = 8;
 constexpr int kStep = 128;      // k of a step
+constexpr int kChunk = 1 << 21; // bytes of x that a chunk of tiles reads
 
 // Byte of 16-byte group g of staged row t.  A 16-byte access takes 16 lanes at a time, lanes 0-3,
 // 12-15, 20-23, 24-27 and 4-7, 8-11, 16-19, 28-31 of each half wave, whose groups have to differ
@@ -25,50 +26,58 @@ constexpr int kStep = 128;      // k of a step
 // matrix instruction reads 32 rows and where 8 lanes write a row.
 __device__ __forceinline__ int group_at(int t, int g) { return t * kStep + 16 * (g ^ ((t >> 1) & 7)); }
 
-template <int BM, int WN, int DX, int OCC, bool GATED>
-__global__ __launch_bounds__(128 * WN, OCC) void experts_many_kernel(const ExpertArgs a, int ntiles) {
-  constexpr int T = 128 * WN;              // threads
+// WT x WN waves of TB 32-slot blocks x 64 weight rows; KS groups of them share the k steps.
+template <int TB, int WT, int WN, int KS, int DX, int OCC, bool GATED>
+__global__ __launch_bounds__(64 * WT * WN * KS, OCC) void experts_many_kernel(const ExpertArgs a, int ntiles) {
+  constexpr int BM = 32 * TB * WT;         // slots of a workgroup
+  constexpr int T = 64 * WT * WN;          // threads of a group
   constexpr int COLS = GATED ? 32 : 64;    // outputs of a wave
-  constexpr int TB = BM / 64;              // 32-slot blocks of a wave
   constexpr int XG = BM * 8 / T;           // 16-byte groups a thread stages
   constexpr int OUT = 16 * COLS;           // floats of the unit that leaves through LDS
-  constexpr int BUF = BM * kStep > 4 * WN * OUT ? BM * kStep : 4 * WN * OUT;   // half of the units too
-  static_assert(XG >= 1 && BM <= T, "shapes");
-  __shared__ __attribute__((aligned(16))) uint8_t xs[2][BUF];
+  constexpr int STAGED = 2 * KS * BM * kStep, UNITS = WT * WN * OUT * 4;
+  // half of the groups' sums at a time (a quarter, and so on) meet those of the others
+  constexpr int SUMS = KS / 2 * WT * WN * TB * 2 * 16 * 64 * 4;
+  constexpr int BYTES = STAGED > UNITS ? (STAGED > SUMS ? STAGED : SUMS) : (UNITS > SUMS ? UNITS : SUMS);
+  static_assert(XG >= 1 && (KS & (KS - 1)) == 0, "shapes");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[BYTES];
   __shared__ float d_of[BM];
   __shared__ int row_of[BM];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wt = wave / WN, wr = wave % WN;
+  const int kg = wave / (WT * WN), wt = wave / WN % WT, wr = wave % WN, gt = tid % T;
   const int r = lane & 31, h = lane >> 5;
   const int K = a.K, steps = (K + kStep - 1) / kStep, nblocks = (a.N + 31) / 32;
-  // workgroup b runs on XCD b % 8: each XCD takes a contiguous run of tiles, those of one
-  // expert's slots beside each other, so that they share its L2
+  // Workgroup b runs on XCD b % 8: each XCD takes a contiguous run of tiles.  An expert's tiles go by
+  // chunks of slot tiles whose rows stay in its L2, and in a chunk slot tiles first, so that each
+  // block of weights is read by them one after another.
   const int tiles = ntiles * count_tiles<BM>(a);
   const int per_xcd = (tiles + kXcds - 1) / kXcds;
   const int t = (int)(blockIdx.x % kXcds) * per_xcd + (int)(blockIdx.x / kXcds);
   if ((int)(blockIdx.x / kXcds) >= per_xcd || t >= tiles) return;
-  const int mt = t / ntiles, nt = t - mt * ntiles;
-  const ExpertTile et = expert_tile<BM>(a, mt);
-  if (et.rows <= 0) return;
+  const ExpertSpan et = expert_span<BM>(a, t / ntiles);
+  if (et.n == 0) return;
+  const int mtiles = (et.n + BM - 1) / BM, most = max(1, min(8, kChunk / (BM * K)));
+  const int u = t - et.tile0 * ntiles, chunk = u / (most * ntiles), v = u - chunk * most * ntiles;
+  const int across = min(most, mtiles - chunk * most), nt = v / across;
+  const int slot0 = et.slot0 + (chunk * most + v - nt * across) * BM, rows = min(et.slot0 + et.n - slot0, BM);
 
-  if (tid < BM) {
-    const int row = tid < et.rows ? input_row(a, et.slot0 + tid) : -1;
-    row_of[tid] = row;
-    d_of[tid] = row < 0 ? 0.0f : a.xs[row];
+  for (int i = tid; i < BM; i += T * KS) {
+    const int row = i < rows ? input_row(a, slot0 + i) : -1;
+    row_of[i] = row;
+    d_of[i] = row < 0 ? 0.0f : a.xs[row];
   }
   // rows without a slot read the tile's first row or row 0; nothing of theirs is kept
   const bool gather = a.pair != nullptr;
   const auto xr = gather
       ? make_uniform_rsrc(a.xq, (uint32_t)min((int64_t)a.rows * K, (int64_t)0xffffffffu))
-      : make_uniform_rsrc(a.xq + (size_t)et.slot0 * K, (uint32_t)(et.rows * K));
+      : make_uniform_rsrc(a.xq + (size_t)slot0 * K, (uint32_t)(rows * K));
   uint32_t xo[XG];
 #pragma unroll
   for (int i = 0; i < XG; ++i) {
-    const int sl = (tid >> 3) + T / 8 * i;
+    const int sl = (gt >> 3) + T / 8 * i;
     int row = 0;
-    if (sl < et.rows) row = gather ? max(input_row(a, et.slot0 + sl), 0) : sl;
-    xo[i] = (uint32_t)row * (uint32_t)K + 16u * (uint32_t)(tid & 7);
+    if (sl < rows) row = gather ? max(input_row(a, slot0 + sl), 0) : sl;
+    xo[i] = (uint32_t)row * (uint32_t)K + 16u * (uint32_t)(gt & 7);
   }
   // this wave's two blocks of 32 weight rows: neighbours, or the same of gate and up
   const int rb = nt * ((GATED ? 32 : 64) * WN / 32) + (GATED ? wr : 2 * wr);
@@ -79,20 +88,20 @@ __global__ __launch_bounds__(128 * WN, OCC) void experts_many_kernel(const Exper
   const auto wr1 = GATED ? make_uniform_rsrc(a.up + expert_at + (size_t)rb * blk, (uint32_t)nb * blk) : wr0;
 
   // (steps past the end read what lies there, or zeros past the buffers; nothing uses them)
-  auto xload = [&](uint4 (&v)[XG], int s) {
+  auto xload = [&](uint4 (&v)[XG], int it) {
 #pragma unroll
-    for (int i = 0; i < XG; ++i) v[i] = bload16(xr, xo[i] + (uint32_t)s * kStep);
+    for (int i = 0; i < XG; ++i) v[i] = bload16(xr, xo[i] + (uint32_t)(it * KS + kg) * kStep);
   };
-  auto wload = [&](uint4 (&v)[2], int s) {
-    const uint32_t o = (uint32_t)s * 1024u + 16u * (uint32_t)lane;
+  auto wload = [&](uint4 (&v)[2], int it) {
+    const uint32_t o = (uint32_t)(it * KS + kg) * 1024u + 16u * (uint32_t)lane;
     v[0] = bload16(wr0, o);
     v[1] = bload16(wr1, GATED ? o : o + blk);
   };
   auto stage = [&](const uint4& v, int i, uint8_t* buf) {
-    *reinterpret_cast<uint4*>(buf + group_at((tid >> 3) + T / 8 * i, tid & 7)) = v;
+    *reinterpret_cast<uint4*>(buf + group_at((gt >> 3) + T / 8 * i, gt & 7)) = v;
   };
   auto aread = [&](const uint8_t* buf, int i, int j) -> v4i {
-    return *reinterpret_cast<const v4i*>(buf + group_at(wt * (BM / 2) + 32 * i + r, 4 * h + j));
+    return *reinterpret_cast<const v4i*>(buf + group_at(32 * (wt * TB + i) + r, 4 * h + j));
   };
 
   v16i acc[TB][2];
@@ -101,10 +110,13 @@ __global__ __launch_bounds__(128 * WN, OCC) void experts_many_kernel(const Exper
 #pragma unroll
     for (int b = 0; b < 2; ++b) acc[i][b] = (v16i){};
 
-  auto body = [&](uint4 (&xv)[XG], uint4 (&wv)[2], int s) {
-    const uint8_t* cur = xs[s & 1];
-    uint8_t* nxt = xs[(s + 1) & 1];
+  // Iteration it of this group: step it KS + kg, staged in buffer it & 1.
+  auto buffer = [&](int it) { return lds + ((it & 1) * KS + kg) * (BM * kStep); };
+  auto body = [&](uint4 (&xv)[XG], uint4 (&wv)[2], int it) {
+    const uint8_t* cur = buffer(it);
+    uint8_t* nxt = buffer(it + 1);
     const uint32_t wd[2][4] = {{wv[0].x, wv[0].y, wv[0].z, wv[0].w}, {wv[1].x, wv[1].y, wv[1].z, wv[1].w}};
+    const bool on = KS == 1 || it * KS + kg < steps;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v4i x[TB], w[2];
@@ -118,16 +130,18 @@ __global__ __launch_bounds__(128 * WN, OCC) void experts_many_kernel(const Exper
       if (j == 3) {
         // every use of xv and wv is above: the loads reuse their registers
         asm volatile("" : "+v"(w[0]), "+v"(w[1])::"memory");
-        xload(xv, s + 1 + DX);
-        wload(wv, s + 2);
+        xload(xv, it + 1 + DX);
+        wload(wv, it + 2);
       }
+      if (on) {
 #pragma unroll
-      for (int i = 0; i < TB; ++i)
+        for (int i = 0; i < TB; ++i)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-          acc[i][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(x[i], w[b], acc[i][b], 0, 0, 0);
+          for (int b = 0; b < 2; ++b)
+            acc[i][b] = __builtin_amdgcn_mfma_i32_32x32x32_i8(x[i], w[b], acc[i][b], 0, 0, 0);
+      }
     }
-    lds_barrier();     // step s + 1 is staged; nobody reads xs[s & 1] any more
+    lds_barrier();     // iteration it + 1 is staged; nobody reads this one's buffer any more
   };
 
   uint4 x0[XG], xv[DX][XG], wv[2][2];
@@ -139,18 +153,41 @@ __global__ __launch_bounds__(128 * WN, OCC) void experts_many_kernel(const Exper
     wload(wv[d], d);
   }
 #pragma unroll
-  for (int i = 0; i < XG; ++i) stage(x0[i], i, xs[0]);
+  for (int i = 0; i < XG; ++i) stage(x0[i], i, buffer(0));
   lds_barrier();
-  int s = 0;
-  for (; s + 1 < steps; s += 2) {
-    body(xv[0], wv[0], s);
-    body(xv[DX - 1], wv[1], s + 1);
+  const int its = (steps + KS - 1) / KS;
+  int it = 0;
+  for (; it + 1 < its; it += 2) {
+    body(xv[0], wv[0], it);
+    body(xv[DX - 1], wv[1], it + 1);
   }
-  if (s < steps) body(xv[0], wv[0], s);
+  if (it < its) body(xv[0], wv[0], it);
+
+  // the groups' sums: the upper half's go to the lower half, until group 0 has all
+  if constexpr (KS > 1) {
+    int* sums = reinterpret_cast<int*>(lds) + lane;
+    constexpr int R = TB * 2 * 16;
+#pragma unroll
+    for (int half = KS / 2; half >= 1; half /= 2) {
+      if (kg >= half && kg < 2 * half) {
+        int* to = sums + (wave - half * WT * WN) * (R * 64);
+#pragma unroll
+        for (int q = 0; q < R; ++q) to[q * 64] = acc[q / 32][q / 16 % 2][q % 16];
+      }
+      __syncthreads();
+      if (kg < half) {
+        const int* from = sums + wave * (R * 64);
+#pragma unroll
+        for (int q = 0; q < R; ++q) acc[q / 32][q / 16 % 2][q % 16] += from[q * 64];
+      }
+      __syncthreads();
+    }
+    if (kg > 0) return;
+  }
 
   // 16 slots at a time through LDS (free behind the last barrier), so that rows leave in 16 bytes
   // a lane.  Lane l holds weight row l % 32 and slots 8 (v / 4) + 4 (l / 32) + v % 4.
-  float* unit = reinterpret_cast<float*>(&xs[0][0]) + wave * OUT;
+  float* unit = reinterpret_cast<float*>(lds) + wave * OUT;
   const int n0 = rb * 32;
   float gamma[2], bias[2];
 #pragma unroll
@@ -172,7 +209,7 @@ __global__ __launch_bounds__(128 * WN, OCC) void experts_many_kernel(const Exper
       float v0[8], v1[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = d_of[wt * (BM / 2) + 32 * i + 16 * q + 8 * (e >> 2) + 4 * h + (e & 3)];
+        const float d = d_of[32 * (wt * TB + i) + 16 * q + 8 * (e >> 2) + 4 * h + (e & 3)];
         v0[e] = acc_64(acc[i][0][8 * q + e]) * (gamma[0] * d);
         v1[e] = acc_64(acc[i][1][8 * q + e]) * (gamma[1] * d);
         if (has0) v0[e] = v0[e] + bias[0];
@@ -204,9 +241,9 @@ __global__ __launch_bounds__(128 * WN, OCC) void experts_many_kernel(const Exper
         const float4 lo = *reinterpret_cast<const float4*>(from);
         const float4 hi = *reinterpret_cast<const float4*>(from + 4);
         float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const int ml = wt * (BM / 2) + 32 * i + 16 * q + sl, n = n0 + c;
+        const int ml = 32 * (wt * TB + i) + 16 * q + sl, n = n0 + c;
         if (row_of[ml] < 0 || n >= a.N) continue;
-        const size_t o = (size_t)(et.slot0 + ml) * a.N + n;
+        const size_t o = (size_t)(slot0 + ml) * a.N + n;
         if (wide && n + 8 <= a.N) {
           typedef uint32_t u4 __attribute__((ext_vector_type(4)));
           if (a.y_bf16) {
@@ -247,26 +284,29 @@ __global__ __launch_bounds__(128 * WN, OCC) void experts_many_kernel(const Exper
     }
 }
 
-template <int BM, int WN, int DX, int OCC>
+template <int TB, int WT, int WN, int KS, int DX, int OCC>
 hipError_t launch_many(const ExpertArgs& a, hipStream_t s) {
   const int bn = a.up ? 32 * WN : 64 * WN;
   const int ntiles = (a.N + bn - 1) / bn;
-  const int64_t grid = (many_tiles(a, BM) * ntiles + kXcds - 1) / kXcds * kXcds;
+  const dim3 grid((unsigned)((many_tiles(a, 32 * TB * WT) * ntiles + kXcds - 1) / kXcds * kXcds)), block(64 * WT * WN * KS);
   if (a.up)
-    hipLaunchKernelGGL((experts_many_kernel<BM, WN, DX, OCC, true>), dim3((unsigned)grid), dim3(128 * WN), 0, s, a, ntiles);
+    hipLaunchKernelGGL((experts_many_kernel<TB, WT, WN, KS, DX, OCC, true>), grid, block, 0, s, a, ntiles);
   else
-    hipLaunchKernelGGL((experts_many_kernel<BM, WN, DX, OCC, false>), dim3((unsigned)grid), dim3(128 * WN), 0, s, a, ntiles);
+    hipLaunchKernelGGL((experts_many_kernel<TB, WT, WN, KS, DX, OCC, false>), grid, block, 0, s, a, ntiles);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_experts_many(const ExpertArgs& a, int bm, hipStream_t s) {
-  switch (bm) {
-    case 128: return launch_many<128, 4, 1, 4>(a, s);
-    case 64: return launch_many<64, 4, 2, 4>(a, s);
-    default: return launch_many<64, 2, 2, 2>(a, s);
+hipError_t launch_experts_many(const ExpertArgs& a, ManyTile tile, hipStream_t s) {
+  switch (tile) {
+    case kMany32x2: return launch_many<1, 1, 1, 8, 1, 4>(a, s);
+    case kMany32x4: return launch_many<1, 1, 2, 4, 2, 4>(a, s);
+    case kMany32: return launch_many<1, 1, 4, 1, 2, 4>(a, s);
+    case kMany64: return launch_many<1, 2, 4, 1, 2, 4>(a, s);
+    case kMany128: return launch_many<2, 2, 4, 1, 1, 4>(a, s);
   }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace bitnet

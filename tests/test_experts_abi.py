@@ -95,8 +95,8 @@ def test_expert_routing_refusals(lib):   # noqa: F811
     assert experts(lib, routing(offset=None), p) == ENULL and experts(lib, routing(pair=None), p) == ENULL
     assert experts(lib, routing(offset=A + 2), p) == EALIGN and experts(lib, routing(), p, 2) == ESHAPE
     assert experts(lib, routing(), product(rows=5), 1) == ESHAPE             # by slot: 10 rows
-    # a gathered row lies within 2^32 bytes of x_q
-    assert experts(lib, routing(tokens=1 << 25, topk=1), product(rows=1 << 25, K=128)) == ESHAPE
+    # gathered rows lie within 2^31 bytes
+    assert experts(lib, routing(tokens=(1 << 24) + 1, topk=1), product(rows=(1 << 24) + 1, K=128)) == ESHAPE
     # a grid that the runtime cannot count
     huge = product(rows=1 << 30, N=1 << 24, K=64)
     assert lib.bitnet_ternary_linear_act(ctypes.byref(huge), None) == ESHAPE
