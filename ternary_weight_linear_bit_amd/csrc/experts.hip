@@ -156,15 +156,18 @@ hipError_t launch_experts(const ExpertArgs& a, hipStream_t s) {
   // not fill the compute units otherwise
   if (groups(32, 2) <= 256) return launch_experts_many(a, kMany32x2, s);
   if (groups(32, 4) <= 256) return launch_experts_many(a, kMany32x4, s);
-  // 32, 64 or 128 slots x 8 blocks: the least of rounds times a round's time (us a step, measured),
-  // a partly filled last round counting whole while rounds are few
-  auto time = [&](int rows, double step) {
-    const double r = groups(rows, 8) / 256;
-    return step * (r <= 1 ? 1 : r <= 2 ? 2 : r <= 3 ? 3 : r + 0.4);
+  // 32 x 8, 64 x 8 or 64 x 16 blocks: the least of rounds (a workgroup for each of 256 compute units)
+  // times a round's time, us a step and beside the steps, as measured in one round and in many; a
+  // partly filled last round counts whole while rounds are few
+  auto time = [&](int rows, int wide, double one, double step, double beside) {
+    const double r = groups(rows, wide) / 256;
+    return r <= 1 ? one * steps + beside
+                  : (step * steps + beside) * (r <= 2 ? 2 : r <= 3 ? 3 : r + 0.4);
   };
-  const double t32 = time(32, 0.26), t64 = time(64, 0.49), t128 = time(128, 0.85);
-  if (t32 <= t64 && t32 <= t128) return launch_experts_many(a, kMany32, s);
-  return launch_experts_many(a, t64 <= t128 ? kMany64 : kMany128, s);
+  const double t32 = time(32, 8, 0.28, 0.25, 0.8), t64 = time(64, 8, 0.55, 0.38, 2.2),
+               t64w = time(64, 16, 0.75, 0.72, 3.3);
+  if (t32 <= t64 && t32 <= t64w) return launch_experts_many(a, kMany32x8, s);
+  return launch_experts_many(a, t64 <= t64w ? kMany64x8 : kMany64x16, s);
 }
 
 }  // namespace bitnet

@@ -47,9 +47,9 @@ inline int64_t many_tiles(const ExpertArgs& a, int rows) {
   return a.offset ? expert_tiles(a.slots, a.experts, rows) : ((int64_t)a.slots + rows - 1) / rows;
 }
 bool experts_fit(const ExpertArgs& a);
-// Tiles of the kernel for many rows (experts_many.hip): slots, by 8 blocks of 32 weight rows, or by
-// 2 and 4 with the k steps shared by 8 and 4 groups of waves.
-enum ManyTile { kMany32x2, kMany32x4, kMany32, kMany64, kMany128 };
+// Tiles of the kernel for many rows (experts_many.hip): slots x blocks of 32 weight rows; in the first
+// two eight and four groups of waves share the k steps.
+enum ManyTile { kMany32x2, kMany32x4, kMany32x8, kMany64x8, kMany64x16 };
 hipError_t launch_experts_many(const ExpertArgs& a, ManyTile tile, hipStream_t s);
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
 

@@ -26,17 +26,18 @@ constexpr int kChunk = 1 << 21; // bytes of x that a chunk of tiles reads
 // matrix instruction reads 32 rows and where 8 lanes write a row.
 __device__ __forceinline__ int group_at(int t, int g) { return t * kStep + 16 * (g ^ ((t >> 1) & 7)); }
 
-// WT x WN waves of TB 32-slot blocks x 64 weight rows; KS groups of them share the k steps.
-template <int TB, int WT, int WN, int KS, int DX, int OCC, bool GATED>
-__global__ __launch_bounds__(64 * WT * WN * KS, OCC) void experts_many_kernel(const ExpertArgs a, int ntiles) {
-  constexpr int BM = 32 * TB * WT;         // slots of a workgroup
-  constexpr int T = 64 * WT * WN;          // threads of a group
+// WN waves of TB 32-slot blocks x 64 weight rows; KS groups of them share the k steps.  DX: steps that
+// x is loaded ahead of its staging.
+template <int TB, int WN, int KS, int DX, bool GATED>
+__global__ __launch_bounds__(64 * WN * KS, 4) void experts_many_kernel(const ExpertArgs a, int ntiles) {
+  constexpr int BM = 32 * TB;              // slots of a workgroup
+  constexpr int T = 64 * WN;               // threads of a group
   constexpr int COLS = GATED ? 32 : 64;    // outputs of a wave
   constexpr int XG = BM * 8 / T;           // 16-byte groups a thread stages
   constexpr int OUT = 16 * COLS;           // floats of the unit that leaves through LDS
-  constexpr int STAGED = 2 * KS * BM * kStep, UNITS = WT * WN * OUT * 4;
+  constexpr int STAGED = 2 * KS * BM * kStep, UNITS = WN * OUT * 4;
   // half of the groups' sums at a time (a quarter, and so on) meet those of the others
-  constexpr int SUMS = KS / 2 * WT * WN * TB * 2 * 16 * 64 * 4;
+  constexpr int SUMS = KS / 2 * WN * TB * 2 * 16 * 64 * 4;
   constexpr int BYTES = STAGED > UNITS ? (STAGED > SUMS ? STAGED : SUMS) : (UNITS > SUMS ? UNITS : SUMS);
   static_assert(XG >= 1 && (KS & (KS - 1)) == 0, "shapes");
   __shared__ __attribute__((aligned(16))) uint8_t lds[BYTES];
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(64 * WT * WN * KS, OCC) void experts_many_kernel(co
   __shared__ int row_of[BM];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int kg = wave / (WT * WN), wt = wave / WN % WT, wr = wave % WN, gt = tid % T;
+  const int kg = wave / WN, wr = wave % WN, gt = tid % T;
   const int r = lane & 31, h = lane >> 5;
   const int K = a.K, steps = (K + kStep - 1) / kStep, nblocks = (a.N + 31) / 32;
   // Workgroup b runs on XCD b % 8: each XCD takes a contiguous run of tiles.  An expert's tiles go by
@@ -101,7 +102,7 @@ __global__ __launch_bounds__(64 * WT * WN * KS, OCC) void experts_many_kernel(co
     *reinterpret_cast<uint4*>(buf + group_at((gt >> 3) + T / 8 * i, gt & 7)) = v;
   };
   auto aread = [&](const uint8_t* buf, int i, int j) -> v4i {
-    return *reinterpret_cast<const v4i*>(buf + group_at(32 * (wt * TB + i) + r, 4 * h + j));
+    return *reinterpret_cast<const v4i*>(buf + group_at(32 * i + r, 4 * h + j));
   };
 
   v16i acc[TB][2];
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(64 * WT * WN * KS, OCC) void experts_many_kernel(co
 #pragma unroll
     for (int half = KS / 2; half >= 1; half /= 2) {
       if (kg >= half && kg < 2 * half) {
-        int* to = sums + (wave - half * WT * WN) * (R * 64);
+        int* to = sums + (wave - half * WN) * (R * 64);
 #pragma unroll
         for (int q = 0; q < R; ++q) to[q * 64] = acc[q / 32][q / 16 % 2][q % 16];
       }
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(64 * WT * WN * KS, OCC) void experts_many_kernel(co
       float v0[8], v1[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = d_of[32 * (wt * TB + i) + 16 * q + 8 * (e >> 2) + 4 * h + (e & 3)];
+        const float d = d_of[32 * i + 16 * q + 8 * (e >> 2) + 4 * h + (e & 3)];
         v0[e] = acc_64(acc[i][0][8 * q + e]) * (gamma[0] * d);
         v1[e] = acc_64(acc[i][1][8 * q + e]) * (gamma[1] * d);
         if (has0) v0[e] = v0[e] + bias[0];
@@ -241,7 +242,7 @@ __global__ __launch_bounds__(64 * WT * WN * KS, OCC) void experts_many_kernel(co
         const float4 lo = *reinterpret_cast<const float4*>(from);
         const float4 hi = *reinterpret_cast<const float4*>(from + 4);
         float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        const int ml = 32 * (wt * TB + i) + 16 * q + sl, n = n0 + c;
+        const int ml = 32 * i + 16 * q + sl, n = n0 + c;
         if (row_of[ml] < 0 || n >= a.N) continue;
         const size_t o = (size_t)(slot0 + ml) * a.N + n;
         if (wide && n + 8 <= a.N) {
@@ -284,15 +285,15 @@ __global__ __launch_bounds__(64 * WT * WN * KS, OCC) void experts_many_kernel(co
     }
 }
 
-template <int TB, int WT, int WN, int KS, int DX, int OCC>
+template <int TB, int WN, int KS, int DX>
 hipError_t launch_many(const ExpertArgs& a, hipStream_t s) {
   const int bn = a.up ? 32 * WN : 64 * WN;
   const int ntiles = (a.N + bn - 1) / bn;
-  const dim3 grid((unsigned)((many_tiles(a, 32 * TB * WT) * ntiles + kXcds - 1) / kXcds * kXcds)), block(64 * WT * WN * KS);
+  const dim3 grid((unsigned)((many_tiles(a, 32 * TB) * ntiles + kXcds - 1) / kXcds * kXcds)), block(64 * WN * KS);
   if (a.up)
-    hipLaunchKernelGGL((experts_many_kernel<TB, WT, WN, KS, DX, OCC, true>), grid, block, 0, s, a, ntiles);
+    hipLaunchKernelGGL((experts_many_kernel<TB, WN, KS, DX, true>), grid, block, 0, s, a, ntiles);
   else
-    hipLaunchKernelGGL((experts_many_kernel<TB, WT, WN, KS, DX, OCC, false>), grid, block, 0, s, a, ntiles);
+    hipLaunchKernelGGL((experts_many_kernel<TB, WN, KS, DX, false>), grid, block, 0, s, a, ntiles);
   return hipGetLastError();
 }
 
@@ -300,11 +301,11 @@ hipError_t launch_many(const ExpertArgs& a, hipStream_t s) {
 
 hipError_t launch_experts_many(const ExpertArgs& a, ManyTile tile, hipStream_t s) {
   switch (tile) {
-    case kMany32x2: return launch_many<1, 1, 1, 8, 1, 4>(a, s);
-    case kMany32x4: return launch_many<1, 1, 2, 4, 2, 4>(a, s);
-    case kMany32: return launch_many<1, 1, 4, 1, 2, 4>(a, s);
-    case kMany64: return launch_many<1, 2, 4, 1, 2, 4>(a, s);
-    case kMany128: return launch_many<2, 2, 4, 1, 1, 4>(a, s);
+    case kMany32x2: return launch_many<1, 1, 8, 1>(a, s);
+    case kMany32x4: return launch_many<1, 2, 4, 2>(a, s);
+    case kMany32x8: return launch_many<1, 4, 1, 2>(a, s);
+    case kMany64x8: return launch_many<2, 4, 1, 1>(a, s);
+    case kMany64x16: return launch_many<2, 8, 1, 1>(a, s);
   }
   return hipErrorInvalidValue;
 }
