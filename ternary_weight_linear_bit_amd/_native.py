@@ -1073,6 +1073,7 @@ class TernaryExperts(_Fixed):
         _expect(scale, (scale.shape[0],), torch.float32, "scale")
         self.device = _one_device(w, scale)
         self.w, self.scale, self.experts, self.n, self.k = w, scale, scale.shape[0], n, k
+        self.ptrs = (w.data_ptr(), scale.data_ptr())
 
     @staticmethod
     def from_packed(packed, scale, stream=None):
@@ -1121,49 +1122,63 @@ def bitnet_route(routing, logits=None, score="softmax", scale=1.0, workspace=Non
             have = workspace.numel() * workspace.element_size()
         if have:
             wp = workspace.data_ptr()
-        # (an empty tensor has no address: its plan is that of no tokens)
+        # (logits of no tokens have no address: the plan alone, which is all there is to do)
         status = l.bitnet_route(routing.ref, ptr, dt, stride, code, scale, wp, have, s)
     if status:
         raise BitnetError("bitnet_route", status)
     return routing
 
 
-def _product(name, w, w_scale, n, k, rows, x_q, x_scale, up, bias, up_bias, act, residual, y, y_dtype, experts, stream,
-             call):
-    """Checks a product's operands, makes y where none is given and calls with the C struct."""
+def _matrix_ptrs(w, scale, shape, u8, f32, name):
+    """Addresses of one matrix in the prefill layout and of its scale."""
+    if w.dtype is not u8 or w.shape != shape or not w.is_contiguous():
+        _expect(w, shape, u8, name)
+    if scale.dtype is not f32 or scale.numel() < 1:
+        _check_scale(scale)
+    return w.data_ptr(), scale.data_ptr()
+
+
+def _product(name, call, stream, n, k, rows, x_q, x_scale, ptrs, up_ptrs, mats, bias, up_bias, many, act, residual, y,
+             y_dtype):
+    """Checks what a product's operands have in common, makes y where none is given and calls with the
+    C struct.  ptrs, up_ptrs: addresses of the matrices and scales; mats: their tensors; many: leading
+    sizes of the biases."""
     import torch
-    f32, many = torch.float32, () if experts is None else (experts,)
-    code = _named(act, ACTS, "act")
-    up_w = up_scale = None
-    if up is not None:
-        up_w, up_scale = up
-    elif up_bias is not None:
-        raise ValueError("up_bias without up")
-    for t, what in ((bias, "bias"), (up_bias, "up_bias")):
-        if t is not None:
-            _like(t, (*many, n), f32, what)
-    if x_q.dim() != 2 or x_q.shape[1] != k:
-        raise ValueError(f"x_q: expected [rows, {k}], got {tuple(x_q.shape)}")
-    _like(x_q, x_q.shape, torch.int8, "x_q")
-    _like(x_scale, x_q.shape[:1], f32, "x_scale")
+    f32 = torch.float32
+    code = ACTS.get(act)
+    if code is None:
+        _named(act, ACTS, "act")
+    b0 = b1 = res = 0
+    if bias is not None:
+        _like(bias, (*many, n), f32, "bias")
+        b0 = bias.data_ptr()
+    if up_bias is not None:
+        if up_ptrs[0] == 0:
+            raise ValueError("up_bias without up")
+        _like(up_bias, (*many, n), f32, "up_bias")
+        b1 = up_bias.data_ptr()
+    xs = x_q.shape
+    if len(xs) != 2 or xs[1] != k or x_q.dtype is not torch.int8 or not x_q.is_contiguous():
+        _expect(x_q, (xs[0], k), torch.int8, "x_q")
+    if x_scale.dtype is not f32 or x_scale.shape != xs[:1] or not x_scale.is_contiguous():
+        _expect(x_scale, xs[:1], f32, "x_scale")
     if y is not None:
         if y_dtype is not None and y_dtype is not y.dtype:
             raise ValueError(f"y is {y.dtype}, y_dtype {y_dtype}")
         y_dtype = y.dtype
         _like(y, (rows, n), y_dtype, "y")
-    y_dtype = y_dtype or (f32 if residual is None else residual.dtype)
+    elif y_dtype is None:
+        y_dtype = f32 if residual is None else residual.dtype
     dt = _code(y_dtype, "y")
     if residual is not None:
         _like(residual, (rows, n), y_dtype, "residual")
-    device = _one_device(w, w_scale, up_w, up_scale, bias, up_bias, x_q, x_scale, residual, y)
+        res = residual.data_ptr()
+    device = _one_device(x_q, x_scale, y, residual, bias, up_bias, *mats)
     with _On(device, stream) as s:
         if y is None:
             y = torch.empty((rows, n), dtype=y_dtype, device=device)
-        args = _PRODUCT.pack(w.data_ptr(), 0 if up is None else up_w.data_ptr(), w_scale.data_ptr(),
-                             0 if up is None else up_scale.data_ptr(), 0 if bias is None else bias.data_ptr(),
-                             0 if up_bias is None else up_bias.data_ptr(), x_q.data_ptr(), x_scale.data_ptr(),
-                             0 if residual is None else residual.data_ptr(), y.data_ptr(), x_q.shape[0], n, k, code, dt)
-        status = call(args, s)
+        status = call(_PRODUCT.pack(ptrs[0], up_ptrs[0], ptrs[1], up_ptrs[1], b0, b1, x_q.data_ptr(), x_scale.data_ptr(),
+                                    res, y.data_ptr(), xs[0], n, k, code, dt), s)
     if status:
         raise BitnetError(name, status)
     return y
@@ -1179,11 +1194,12 @@ def bitnet_ternary_linear_act(w_prefill, w_scale, n, x_q, x_scale, up=None, bias
     if x_q.dim() != 2:
         raise ValueError("x_q must be 2-D [M, K]")
     m, k = x_q.shape
-    for t, what in (((w_prefill, w_scale), "w"), *(() if up is None else ((up, "up"),))):
-        _like(t[0], prefill_layout_shape(n, k), torch.uint8, what)
-        _check_scale(t[1])
-    return _product("bitnet_ternary_linear_act", w_prefill, w_scale, n, k, m, x_q, x_scale, up, bias, up_bias, act,
-                    residual, y, y_dtype, None, stream, lib().bitnet_ternary_linear_act)
+    shape, u8, f32 = prefill_layout_shape(n, k), torch.uint8, torch.float32
+    ptrs, up_ptrs, mats = _matrix_ptrs(w_prefill, w_scale, shape, u8, f32, "w_prefill"), (0, 0), (w_prefill, w_scale)
+    if up is not None:
+        up_ptrs, mats = _matrix_ptrs(*up, shape, u8, f32, "up"), (w_prefill, w_scale, *up)
+    return _product("bitnet_ternary_linear_act", lib().bitnet_ternary_linear_act, stream, n, k, m, x_q, x_scale, ptrs,
+                    up_ptrs, mats, bias, up_bias, (), act, residual, y, y_dtype)
 
 
 def bitnet_expert_linear(routing, w, x_q, x_scale, slots=False, up=None, bias=None, up_bias=None, act="none",
@@ -1194,16 +1210,17 @@ def bitnet_expert_linear(routing, w, x_q, x_scale, slots=False, up=None, bias=No
     bitnet_ternary_linear_act."""
     if w.experts != routing.experts:
         raise ValueError(f"{w.experts} matrices for {routing.experts} experts")
-    if up is not None and (up.experts, up.n, up.k) != (w.experts, w.n, w.k):
-        raise ValueError("up must have w's sizes")
+    up_ptrs, mats = (0, 0), (routing.offset, w.w)
+    if up is not None:
+        if up.experts != w.experts or up.n != w.n or up.k != w.k:
+            raise ValueError("up must have w's sizes")
+        up_ptrs, mats = up.ptrs, (routing.offset, w.w, up.w)
     pairs = routing.tokens * routing.topk
     if x_q.shape[0] != (pairs if slots else routing.tokens):
         raise ValueError(f"x_q: expected {pairs if slots else routing.tokens} rows, got {x_q.shape[0]}")
-    _one_device(routing.offset, w.w, x_q)
     f, ref, by_slot = lib().bitnet_expert_linear, routing.ref, 1 if slots else 0
-    return _product("bitnet_expert_linear", w.w, w.scale, w.n, w.k, pairs, x_q, x_scale,
-                    None if up is None else (up.w, up.scale), bias, up_bias, act, None, y, y_dtype, w.experts, stream,
-                    lambda args, s: f(ref, args, by_slot, s))
+    return _product("bitnet_expert_linear", lambda args, s: f(ref, args, by_slot, s), stream, w.n, w.k, pairs, x_q, x_scale,
+                    w.ptrs, up_ptrs, mats, bias, up_bias, (w.experts,), act, None, y, y_dtype)
 
 
 def bitnet_combine(routing, y, residual=None, out=None, out_dtype=None, stream=None):

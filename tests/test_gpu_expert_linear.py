@@ -97,6 +97,21 @@ def test_wide(counts, tokens, n, k, act, gated, bias, slots, dt):
     run(counts, tokens, 2, n, k, act, gated, bias, slots, dt, seed=n)
 
 
+# the tiles that the sizes above do not reach: k steps shared by groups of waves, of which some have no
+# step or a half one, and many slots under few columns
+@pytest.mark.parametrize("counts,tokens,topk,n,k,act,gated,bias,slots,dt", [
+    ([70, 33, 0, 90], 100, 2, 1600, 192, "relu2", False, False, False, "f32"),
+    ([70, 33, 0, 90], 100, 2, 1601, 64, "none", False, True, True, "bf16"),
+    ([70, 33, 0, 90], 100, 2, 1600, 192, "silu", True, True, False, "bf16"),
+    ([70, 33, 0, 90], 100, 2, 1597, 704, "relu2", True, False, True, "f32"),
+    ([70, 33, 0, 90], 100, 2, 795, 8256, "relu2", True, True, False, "bf16"),
+    ([3, 0, 1], 2, 2, 70, 8256, "relu2", True, False, True, "f32"),
+    ([10870], 10870, 1, 763, 576, "relu2", False, True, False, "bf16"),
+    ([10880], 10880, 1, 379, 448, "relu2", True, False, True, "f32")])
+def test_each_tile(counts, tokens, topk, n, k, act, gated, bias, slots, dt):
+    run(counts, tokens, topk, n, k, act, gated, bias, slots, dt, seed=k)
+
+
 @pytest.mark.parametrize("offset", [1, 2, 3])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_unaligned_outputs(offset, dt):
@@ -212,3 +227,44 @@ def test_another_stream():
     y = N.bitnet_ternary_linear_act(w.w[0], w.scale, 70, x, dd, act="relu2", stream=s)
     s.synchronize()
     same(y, E.product(q[0], g[0], xq, d, act="relu2")[0], "f32")
+
+
+def test_captured_products_follow_the_routing():
+    """Two captured calls over one routing whose contents change between replays, with eager calls between."""
+    experts, tokens, k, n = 5, 60, 192, 130
+    q, g, w = matrices(experts, n, k, 3)
+    xq, d = acts(tokens, k, 1)
+    xs, ds = acts(tokens * 2, k, 2)
+    x, dd, x2, d2 = dev(xq), dev(d), dev(xs), dev(ds)
+    r = N.Routing.empty(tokens, 2, experts, DEV)
+    r.expert.fill_(-1)
+    N.bitnet_route(r)
+    ys = [torch.zeros((tokens * 2, n), device=DEV) for _ in range(2)]
+    calls = [lambda: N.bitnet_expert_linear(r, w, x, dd, act="relu2", y=ys[0]),
+             lambda: N.bitnet_expert_linear(r, w, x2, d2, slots=True, y=ys[1])]
+    graphs = []
+    for f in calls:
+        f()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f()
+    for seed in range(4):
+        e = assign([[0, 0, 120, 0, 0], [10, 20, 30, 40, 20], [1, 0, 0, 0, 2], [33, 0, 32, 31, 1]][seed], tokens, 2, seed)
+        r.expert.copy_(dev(e))
+        N.bitnet_route(r)
+        for y in ys:
+            y.fill_(7.0)
+        for gr in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        first, pair, _ = E.plan(e, experts)
+        for i in range(experts):
+            s0, s1 = first[i], first[i + 1]
+            rows = pair[s0:s1] // 2
+            if s1 > s0:
+                same(ys[0][s0:s1], E.product(q[i], g[i], xq[rows], d[rows], act="relu2")[0], "f32")
+                same(ys[1][s0:s1], E.product(q[i], g[i], xs[s0:s1], ds[s0:s1])[0], "f32")
+        assert all((host(y[first[-1]:]) == 7).all() for y in ys)
+        N.bitnet_expert_linear(r, w, x, dd)
+        torch.cuda.synchronize()
