@@ -649,6 +649,7 @@ typedef enum bitnet_score { BITNET_SOFTMAX = 0, BITNET_CHOSEN = 1, BITNET_SIGMOI
 /*
  * Each token's topk largest logits, their weights, and the plan of the pairs; fills all arrays of
  * `routing`.  With logits == NULL `expert` is an input (and `weight` is not touched): the plan alone.
+ * tokens * topk <= 2^24.
  *   logits  [tokens] rows of [experts], fp32 or bf16 (dtype, element-aligned), `stride` elements
  *           apart (>= experts).  Chosen in order of size, ties lowest index first (-0 is 0);
  *           -inf and NaN are never chosen, and where fewer than topk are left the rest have
@@ -726,7 +727,7 @@ bitnet_status bitnet_expert_linear(const bitnet_routing *routing, const bitnet_p
  * left out.  Bit-exact against that definition.
  *   y         [tokens * topk][K] fp32 or bf16 (y_dtype), element-aligned.
  *   residual  NULL or [tokens][K] of out's type; out may be it.
- *   out       [tokens][K] fp32 or bf16 (out_dtype), element-aligned.  K >= 0, K < 2^31.
+ *   out       [tokens][K] fp32 or bf16 (out_dtype), element-aligned.  0 <= K <= 2^23.
  */
 bitnet_status bitnet_combine(const bitnet_routing *routing, const void *y, int y_dtype, int64_t K,
                              const void *residual, void *out, int out_dtype, hipStream_t stream);

@@ -95,7 +95,8 @@ def activate(v, act):
     """act(v): fp32 for none and relu2, float64 for the others."""
     if act == "relu2":
         a = np.maximum(v, F32(0))
-        return (a * a).astype(F32)
+        with np.errstate(over="ignore"):
+            return (a * a).astype(F32)
     z = np.asarray(v, np.float64)
     if act == "silu":
         e = np.exp(-np.abs(z))

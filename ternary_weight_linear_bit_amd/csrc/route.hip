@@ -177,11 +177,13 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int m) {
 constexpr int kPairs = 1024;     // threads, and most pairs of a workgroup
 constexpr int kWaves = kPairs / 64;
 
-// Tokens of a workgroup: 64 (what its lanes choose for at once, up to 256 experts), more where
-// there would be more than 512 workgroups, whose counts each workgroup of the second launch reads.
+// Tokens of a workgroup: 64 (what its lanes choose for at once, up to 256 experts), and more, in
+// rounds of up to 1024 pairs, where there would be more than 512 workgroups: each of them reads the
+// counts of all in the second launch.
 int tokens_of(int64_t tokens, int topk) {
-  const int64_t t = (tokens + 511) / 512, most = kPairs / topk;
-  return (int)(t > most ? most : t > 64 ? t : most < 64 ? most : 64);
+  const int64_t round = kPairs / topk, each = (tokens + 511) / 512, least = round < 64 ? round : 64;
+  if (each <= round) return (int)(each > least ? each : least);
+  return (int)((each + round - 1) / round * round);
 }
 
 // Lanes of the wave with the same expert as this one; none for -1.
@@ -246,44 +248,50 @@ __global__ __launch_bounds__(kPairs) void route_kernel(const RouteArgs a, int to
   int* first = total + E;                // [E]
   int* sums = first + E;                 // [kWaves]
   int* chosen = sums + kWaves;           // [kPairs]
-  const int m0 = (int)blockIdx.x * tokens, m1 = min(m0 + tokens, r.tokens);
-  const int pairs = (m1 - m0) * r.topk, p = m0 * r.topk + tid;
-  for (int i = tid; i < kWaves * E; i += kPairs) count[i] = 0;
-  int e = -1;
-  if constexpr (L == 0) {
-    if (tid < pairs) e = r.expert[p];
-    if (e >= E) e = -1;
-  } else {
-    for (int m = m0 + tid / L; m < m1; m += kPairs / L) {
-      const int c = choose<L, V, BF16>(a, m);
-      if ((tid & (L - 1)) < r.topk) chosen[(m - m0) * r.topk + (tid & (L - 1))] = c;
+  const int m1 = (int)min(((int64_t)blockIdx.x + 1) * tokens, (int64_t)r.tokens), round = kPairs / r.topk;
+  int m0 = (int)blockIdx.x * tokens;
+  for (int x = tid; x < E; x += kPairs) total[x] = 0;
+  do {
+    const int here = min(m1 - m0, round), pairs = here * r.topk, p = m0 * r.topk + tid;
+    for (int i = tid; i < kWaves * E; i += kPairs) count[i] = 0;
+    int e = -1;
+    if constexpr (L == 0) {
+      if (tid < pairs) e = r.expert[p];
+      if (e >= E) e = -1;
+    } else {
+      for (int m = tid / L; m < here; m += kPairs / L) {
+        const int c = choose<L, V, BF16>(a, m0 + m);
+        if ((tid & (L - 1)) < r.topk) chosen[m * r.topk + (tid & (L - 1))] = c;
+      }
     }
-  }
-  __syncthreads();
-  if (L != 0 && tid < pairs) e = chosen[tid];
-  const uint64_t same = same_expert(e, E);
-  int rank = __popcll(same & ((1ull << lane) - 1));
-  if (e >= 0 && rank == 0) count[wave * E + e] = __popcll(same);
-  __syncthreads();
-  for (int x = tid; x < E; x += kPairs) {
-    int n = 0;
+    __syncthreads();
+    if (L != 0 && tid < pairs) e = chosen[tid];
+    const uint64_t same = same_expert(e, E);
+    int rank = __popcll(same & ((1ull << lane) - 1));
+    if (e >= 0 && rank == 0) count[wave * E + e] = __popcll(same);
+    __syncthreads();
+    for (int x = tid; x < E; x += kPairs) {
+      int n = total[x];                  // in earlier rounds
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const int c = count[w * E + x];
-      count[w * E + x] = n;
-      n += c;
+      for (int w = 0; w < kWaves; ++w) {
+        const int c = count[w * E + x];
+        count[w * E + x] = n;
+        n += c;
+      }
+      total[x] = n;
     }
-    total[x] = n;
-    if (!ONE) hist[(size_t)blockIdx.x * ((E + 7) & ~7) + x] = (uint16_t)n;
-  }
-  __syncthreads();
-  if (e >= 0) rank += count[wave * E + e];
-  if constexpr (ONE) {
-    const int used = first_slots(r, [&](int x) { return total[x]; }, [](int) { return 0; }, first, sums, true);
-    if (tid < pairs) place(r, p, e, rank, first, used);
-  } else {
+    __syncthreads();
+    if (e >= 0) rank += count[wave * E + e];
+    if constexpr (ONE) {
+      const int used = first_slots(r, [&](int x) { return total[x]; }, [](int) { return 0; }, first, sums, true);
+      if (tid < pairs) place(r, p, e, rank, first, used);
+      return;
+    }
     if (tid < pairs) r.slot[p] = rank;
-  }
+    m0 += round;
+    __syncthreads();
+  } while (m0 < m1);
+  for (int x = tid; x < E; x += kPairs) hist[(size_t)blockIdx.x * ((E + 7) & ~7) + x] = (uint16_t)total[x];
 }
 
 __global__ __launch_bounds__(kPairs) void route_place_kernel(const Routing r, int tokens,
@@ -292,13 +300,16 @@ __global__ __launch_bounds__(kPairs) void route_place_kernel(const Routing r, in
   const int E = r.experts, E8 = (E + 7) & ~7, tid = threadIdx.x, b = (int)blockIdx.x;
   int *all = lds, *before = all + E8, *first = before + E8, *sums = first + E;
   for (int i = tid; i < 2 * E8; i += kPairs) lds[i] = 0;
-  const int m0 = b * tokens, pairs = (min(m0 + tokens, r.tokens) - m0) * r.topk, p = m0 * r.topk + tid;
-  int e = -1, rank = 0;
-  if (tid < pairs) {
-    e = r.expert[p];
-    if (e >= E) e = -1;
-    rank = r.slot[p];
-  }
+  const int p1 = (int)min(((int64_t)b + 1) * tokens, (int64_t)r.tokens) * r.topk;
+  int p = b * tokens * r.topk + tid, e = -1, rank = 0;
+  auto load = [&]() {
+    if (p < p1) {
+      e = r.expert[p];
+      if (e >= E) e = -1;
+      rank = r.slot[p];
+    }
+  };
+  load();
   __syncthreads();
   // a thread adds 8 experts' counts of every (groups)th workgroup, 8 loads in flight
   const int per = E8 / 8, groups = min(kPairs / per, 64), g = tid / per, x8 = tid - g * per;
@@ -333,7 +344,11 @@ __global__ __launch_bounds__(kPairs) void route_place_kernel(const Routing r, in
   __syncthreads();
   const int used = first_slots(r, [&](int x) { return all[(x & 7) * per + (x >> 3)]; },
                                [&](int x) { return before[(x & 7) * per + (x >> 3)]; }, first, sums, b == 0);
-  if (tid < pairs) place(r, p, e, rank, first, used);
+  while (p < p1) {
+    place(r, p, e, rank, first, used);
+    p += kPairs;
+    load();
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -369,46 +384,47 @@ __device__ __forceinline__ void load_cols(const void* p, int64_t at, float (&v)[
 
 template <bool YB, bool OB, int W>
 __global__ __launch_bounds__(256) void combine_kernel(const Routing r, const void* y, int64_t K,
-                                                      const void* residual, void* out, int parts) {
-  const int64_t m = blockIdx.x / (unsigned)parts;
-  const int64_t k = ((int64_t)(blockIdx.x % (unsigned)parts) * blockDim.x + threadIdx.x) * W;
+                                                      const void* residual, void* out) {
+  const int64_t k = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * W;
   if (k >= K) return;
-  float v[W] = {};
-  if (residual) load_cols<OB, W>(residual, m * K + k, v);
-  const int32_t* slot = r.slot + m * r.topk;
-  const float* weight = r.weight + m * r.topk;
-  for (int j0 = 0; j0 < r.topk; j0 += 4) {
-    float x[4][W], w[4];
-    bool on[4];
+  for (int64_t m = blockIdx.x; m < r.tokens; m += gridDim.x) {
+    float v[W] = {};
+    if (residual) load_cols<OB, W>(residual, m * K + k, v);
+    const int32_t* slot = r.slot + m * r.topk;
+    const float* weight = r.weight + m * r.topk;
+    for (int j0 = 0; j0 < r.topk; j0 += 4) {
+      float x[4][W], w[4];
+      bool on[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      on[j] = false;
-      if (j0 + j < r.topk) {
-        const int s = slot[j0 + j];
-        on[j] = s >= 0 && s < r.pairs;
-        w[j] = weight[j0 + j];
-        if (on[j]) load_cols<YB, W>(y, (int64_t)s * K + k, x[j]);
+      for (int j = 0; j < 4; ++j) {
+        on[j] = false;
+        if (j0 + j < r.topk) {
+          const int s = slot[j0 + j];
+          on[j] = s >= 0 && s < r.pairs;
+          w[j] = weight[j0 + j];
+          if (on[j]) load_cols<YB, W>(y, (int64_t)s * K + k, x[j]);
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (on[j]) {
+#pragma unroll
+          for (int i = 0; i < W; ++i) v[i] = v[i] + w[j] * x[j][i];
+        }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (on[j]) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) v[i] = v[i] + w[j] * x[j][i];
-      }
-  }
-  if constexpr (W == 1) {
-    if (OB)
-      static_cast<uint16_t*>(out)[m * K + k] = float_to_bf16_rne(v[0]);
-    else
-      static_cast<float*>(out)[m * K + k] = v[0];
-  } else if constexpr (OB) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + m * K + k) =
-        make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
-  } else {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + m * K + k);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    if constexpr (W == 1) {
+      if (OB)
+        static_cast<uint16_t*>(out)[m * K + k] = float_to_bf16_rne(v[0]);
+      else
+        static_cast<float*>(out)[m * K + k] = v[0];
+    } else if constexpr (OB) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + m * K + k) =
+          make_uint4(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]), bf16x2_rne(v[4], v[5]), bf16x2_rne(v[6], v[7]));
+    } else {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + m * K + k);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 
@@ -473,10 +489,12 @@ hipError_t launch_combine_w(const Routing& r, const void* y, bool y_bf16, int64_
   const int64_t cols = (K + W - 1) / W;
   const int threads = cols >= 256 ? 256 : (int)((cols + 63) / 64) * 64;
   const int64_t parts = (cols + threads - 1) / threads;
-  if ((int64_t)r.tokens * parts > max_grid(256)) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)(r.tokens * parts)), block(threads);
+  // (columns in the grid's second dimension; with very many workgroups one takes several tokens)
+  const int64_t across = parts > 65535 ? 0 : max_grid(256) / parts;
+  if (across == 0) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)(r.tokens < across ? r.tokens : across), (unsigned)parts), block(threads);
 #define BITNET_COMBINE(YB, OB) \
-  hipLaunchKernelGGL((combine_kernel<YB, OB, W>), grid, block, 0, s, r, y, K, residual, out, (int)parts)
+  hipLaunchKernelGGL((combine_kernel<YB, OB, W>), grid, block, 0, s, r, y, K, residual, out)
   if (y_bf16 && out_bf16)
     BITNET_COMBINE(true, true);
   else if (y_bf16)
@@ -489,8 +507,6 @@ hipError_t launch_combine_w(const Routing& r, const void* y, bool y_bf16, int64_
   return hipGetLastError();
 }
 }  // namespace
-
-bool combine_fits(int64_t tokens, int64_t K) { return tokens * ((K + 255) / 256) <= max_grid(256); }
 
 hipError_t launch_combine(const Routing& r, const void* y, bool y_bf16, int64_t K,
                           const void* residual, void* out, bool out_bf16, hipStream_t s) {

@@ -61,6 +61,9 @@ def test_route_refusals(lib, rbad, bad, want):   # noqa: F811
 
 
 def test_route_workspace(lib):   # noqa: F811
+    big = routing(tokens=1 << 24, topk=2)
+    assert route(lib, big) == ESHAPE and lib.bitnet_route_workspace_bytes(1 << 24, 2, 8) == 0
+    assert lib.bitnet_route_workspace_bytes(1 << 23, 2, 8) > 0
     r = routing(tokens=100000)
     need = lib.bitnet_route_workspace_bytes(100000, 2, 8)
     assert need > 0 and lib.bitnet_route_workspace_bytes(0, 2, 8) == 0
@@ -106,7 +109,7 @@ def test_expert_routing_refusals(lib):   # noqa: F811
 
 
 @pytest.mark.parametrize("rbad,bad,want", [
-    ({}, dict(y_dtype=2), EDTYPE), ({}, dict(out_dtype=-1), EDTYPE), ({}, dict(k=-1), ESHAPE), ({}, dict(k=1 << 31), ESHAPE),
+    ({}, dict(y_dtype=2), EDTYPE), ({}, dict(out_dtype=-1), EDTYPE), ({}, dict(k=-1), ESHAPE), ({}, dict(k=(1 << 23) + 1), ESHAPE),
     (dict(weight=None), {}, ENULL), (dict(slot=None), {}, ENULL), ({}, dict(y=None), ENULL), ({}, dict(out=None), ENULL),
     (dict(slot=A + 2), {}, EALIGN), ({}, dict(y=A + 2), EALIGN), ({}, dict(residual=A + 1), EALIGN),
     ({}, dict(out_dtype=1, out=A + 1), EALIGN)])

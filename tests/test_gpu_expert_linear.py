@@ -132,6 +132,27 @@ def test_extreme_sums():
         assert (host(y) == -64.0 * k).all()
 
 
+@pytest.mark.parametrize("act", ["relu2", "silu", "gelu"])
+@pytest.mark.parametrize("n", [64, 24064])
+def test_activations_over_their_range(act, n):
+    """v = +-code * d, from 2^-40 to 2^60, dense around 0, through the kernels for few and many rows."""
+    q = np.zeros((n, 64), np.int8)
+    q[np.arange(n), np.arange(n) % 64] = 1 - 2 * (np.arange(n) // 64 % 2)
+    from oracle import bitnet_oracle as O
+    w = N.bitnet_repack_prefill(dev(O.pack_codes(q)))
+    rows = 40 if n == 64 else 130
+    x = np.random.default_rng(1).integers(-127, 128, (rows, 64)).astype(np.int8)
+    d = np.r_[2.0 ** np.linspace(-40, 60, 10), np.linspace(1e-3, 0.3, rows - 10)].astype(F32)
+    y = N.bitnet_ternary_linear_act(w, dev(np.ones(1, F32)), n, dev(x), dev(d), act=act)
+    compare(y, *E.product(q, F32(1), x, d, act=act), "f32")
+
+
+def test_a_thousand_experts():
+    counts = np.zeros(1000, int)
+    counts[[0, 3, 64, 500, 999]] = [1, 33, 2, 7, 40]
+    run(list(counts), 83, 1, 33, 64, "relu2", True, False, False, "f32", seed=2)
+
+
 def test_the_same_token_twice():
     """A pair list that names one expert twice gives the row twice."""
     e = np.array([[1, 1], [0, 1], [1, 1]], np.int32)

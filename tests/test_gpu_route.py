@@ -50,7 +50,7 @@ def logits(tokens, experts, seed, dt, ties=False):
 @pytest.mark.parametrize("tokens,experts,topk,dt", [
     (1, 1, 1, "f32"), (1, 8, 2, "bf16"), (3, 63, 32, "f32"), (64, 64, 6, "bf16"), (65, 65, 1, "f32"), (129, 128, 8, "bf16"),
     (200, 129, 3, "f32"), (37, 256, 8, "f32"), (300, 257, 7, "bf16"), (33, 512, 5, "f32"), (40, 513, 9, "bf16"), (17, 1024, 32, "f32"),
-    (1500, 16, 4, "f32"), (5, 2, 5, "f32"), (700, 1000, 3, "bf16")])
+    (1500, 16, 4, "f32"), (5, 2, 5, "f32"), (700, 1000, 3, "bf16"), (17000, 40, 32, "bf16")])
 def test_route(tokens, experts, topk, dt, score):
     t, x = logits(tokens, experts, tokens + experts, dt)
     r = N.bitnet_route(N.Routing.empty(tokens, topk, experts, DEV), t, score, 1.25)
@@ -103,7 +103,8 @@ def test_rows_apart_and_unaligned():
         check(N.bitnet_route(N.Routing.empty(90, 4, 50, DEV), t[:, at:at + 50]), x[:, at:at + 50], 4)
 
 
-@pytest.mark.parametrize("tokens,topk,experts", [(1, 1, 1), (7, 3, 5), (512, 1, 3), (300, 7, 64), (171, 3, 1000), (4000, 8, 33)])
+@pytest.mark.parametrize("tokens,topk,experts", [(1, 1, 1), (7, 3, 5), (512, 1, 3), (300, 7, 64), (171, 3, 1000), (4000, 8, 33),
+                                                 (70001, 16, 300), (600000, 1, 5)])
 def test_plan_of_given_experts(tokens, topk, experts):
     """Numbers outside the experts have no slot; the same expert may come twice; weights stay."""
     e = np.random.default_rng(tokens).integers(-3, experts + 3, (tokens, topk)).astype(np.int32)
@@ -197,6 +198,22 @@ def test_combine(tokens, topk, k, residual, offset, yd, od):
     if residual:                                  # in place
         assert N.bitnet_combine(r, y, res, out=res) is res
         same(res, want, od)
+
+
+def test_combine_of_many_tokens():
+    """More tokens than workgroups in the first dimension: 65535 parts of a row leave 255 of them."""
+    k, tokens = 65535 * 256 // 2, 3
+    r, (_, _, slot) = routing([[0], [-1], [0]], 1)
+    y = torch.zeros((tokens, k), dtype=torch.bfloat16, device=DEV)
+    y[0], y[1] = 2.0, -4.0
+    out = N.bitnet_combine(r, y)
+    w = host(r.weight)
+    for m, v in ((0, 2.0 * w[0, 0]), (1, 0.0), (2, -4.0 * w[2, 0])):
+        assert bool((out[m] == torch.tensor(v, dtype=torch.float32).to(torch.bfloat16).to(DEV)).all())
+    tokens = 200000
+    r, (_, _, slot) = routing(np.zeros((tokens, 1), np.int32), 1)
+    y, yf = typed(np.random.default_rng(2).standard_normal((tokens, 33)), "f32")
+    same(N.bitnet_combine(r, y), (host(r.weight) * yf).astype(F32), "f32")
 
 
 def test_combine_leaves_out_what_has_no_slot():
