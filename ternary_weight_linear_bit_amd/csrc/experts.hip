@@ -7,6 +7,8 @@
 // Weights lie in the prefill layout (blocks of 32 rows x 128 k, 1024 bytes, in the lanes' order).
 #include "experts_internal.h"
 
+#include <math.h>
+
 namespace bitnet {
 namespace {
 
@@ -156,18 +158,34 @@ hipError_t launch_experts(const ExpertArgs& a, hipStream_t s) {
   // not fill the compute units otherwise
   if (groups(32, 2) <= 256) return launch_experts_many(a, kMany32x2, s);
   if (groups(32, 4) <= 256) return launch_experts_many(a, kMany32x4, s);
-  // 32 x 8, 64 x 8 or 64 x 16 blocks: the least of rounds (a workgroup for each of 256 compute units)
-  // times a round's time, us a step and beside the steps, as measured in one round and in many; a
-  // partly filled last round counts whole while rounds are few
-  auto time = [&](int rows, int wide, double one, double step, double beside) {
-    const double r = groups(rows, wide) / 256;
-    return r <= 1 ? one * steps + beside
-                  : (step * steps + beside) * (r <= 2 ? 2 : r <= 3 ? 3 : r + 0.4);
+  // 32 x 8, 64 x 8, 96 x 8 or 64 x 16 blocks: the least time, with what a step and what lies beside
+  // the steps of a workgroup takes alone on its compute unit, and among `held` of them (us, fitted to
+  // measured calls).  A last round's workgroups count as those that run alone while rounds are few.
+  struct Shape {
+    ManyTile tile;
+    int rows, wide, held;
+    double alone, among, beside;
   };
-  const double t32 = time(32, 8, 0.28, 0.25, 0.8), t64 = time(64, 8, 0.55, 0.38, 2.2),
-               t64w = time(64, 16, 0.75, 0.72, 3.3);
-  if (t32 <= t64 && t32 <= t64w) return launch_experts_many(a, kMany32x8, s);
-  return launch_experts_many(a, t64 <= t64w ? kMany64x8 : kMany64x16, s);
+  const Shape shapes[] = {{kMany32x8, 32, 8, 4, 0.30, 0.23, 0.9},
+                          {kMany64x8, 64, 8, 4, 0.58, 0.35, 2.0},
+                          {kMany96x8, 96, 8, 3, 0.85, 0.50, 3.0},
+                          {kMany64x16, 64, 16, 2, 0.68, 0.57, 6.3}};
+  ManyTile best = kMany32x8;
+  double least = 0;
+  for (const Shape& p : shapes) {
+    const double r = groups(p.rows, p.wide) / 256, each_round = p.among * steps + p.beside;
+    auto some = [&](double n) {
+      return n <= 0 ? 0 : n <= 1 ? p.alone * steps + p.beside : each_round * ceil(n);
+    };
+    const double time = r <= p.held ? some(r)
+                        : r <= 2 * p.held ? each_round * p.held + some(r - p.held)
+                                          : each_round * (r + 0.4);
+    if (least == 0 || time < least) {
+      least = time;
+      best = p.tile;
+    }
+  }
+  return launch_experts_many(a, best, s);
 }
 
 }  // namespace bitnet

@@ -49,7 +49,7 @@ inline int64_t many_tiles(const ExpertArgs& a, int rows) {
 bool experts_fit(const ExpertArgs& a);
 // Tiles of the kernel for many rows (experts_many.hip): slots x blocks of 32 weight rows; in the first
 // two eight and four groups of waves share the k steps.
-enum ManyTile { kMany32x2, kMany32x4, kMany32x8, kMany64x8, kMany64x16 };
+enum ManyTile { kMany32x2, kMany32x4, kMany32x8, kMany64x8, kMany96x8, kMany64x16 };
 hipError_t launch_experts_many(const ExpertArgs& a, ManyTile tile, hipStream_t s);
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
 
@@ -133,7 +133,8 @@ __device__ __forceinline__ v4i weights_64(uint32_t w) {
   a.w = (int)__builtin_amdgcn_bitop3_b32(w, top, one, 0x6a);
   return a;
 }
-__device__ __forceinline__ float acc_64(int acc) { return (float)(-(acc >> 6)); }   // exact
+// acc from that sum (exact: 24 bits times 2^6; a sum of 0 is +0).
+__device__ __forceinline__ float acc_64(int sum) { return fmaf((float)sum, -0x1p-6f, 0.0f); }
 
 // e^x for x <= 0, the rounding of x log2 e made up for (it is x 2^-24 otherwise).
 __device__ __forceinline__ float exp_neg(float x) {

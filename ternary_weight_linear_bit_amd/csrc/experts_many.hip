@@ -29,7 +29,7 @@ __device__ __forceinline__ int group_at(int t, int g) { return t * kStep + 16 * 
 // WN waves of TB 32-slot blocks x 64 weight rows; KS groups of them share the k steps.  DX: steps that
 // x is loaded ahead of its staging.
 template <int TB, int WN, int KS, int DX, bool GATED>
-__global__ __launch_bounds__(64 * WN * KS, 4) void experts_many_kernel(const ExpertArgs a, int ntiles) {
+__global__ __launch_bounds__(64 * WN * KS, TB == 3 ? 3 : 4) void experts_many_kernel(const ExpertArgs a, int ntiles) {
   constexpr int BM = 32 * TB;              // slots of a workgroup
   constexpr int T = 64 * WN;               // threads of a group
   constexpr int COLS = GATED ? 32 : 64;    // outputs of a wave
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(64 * WN * KS, 4) void experts_many_kernel(const Exp
   constexpr int BYTES = STAGED > UNITS ? (STAGED > SUMS ? STAGED : SUMS) : (UNITS > SUMS ? UNITS : SUMS);
   static_assert(XG >= 1 && (KS & (KS - 1)) == 0, "shapes");
   __shared__ __attribute__((aligned(16))) uint8_t lds[BYTES];
-  __shared__ float d_of[BM];
+  __shared__ float scale_of[GATED ? 2 : 1][BM];      // gamma d of each matrix
   __shared__ int row_of[BM];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -64,8 +64,10 @@ __global__ __launch_bounds__(64 * WN * KS, 4) void experts_many_kernel(const Exp
 
   for (int i = tid; i < BM; i += T * KS) {
     const int row = i < rows ? input_row(a, slot0 + i) : -1;
+    const float d = row < 0 ? 0.0f : a.xs[row];
     row_of[i] = row;
-    d_of[i] = row < 0 ? 0.0f : a.xs[row];
+    scale_of[0][i] = a.w_scale[et.expert] * d;
+    if (GATED) scale_of[GATED ? 1 : 0][i] = a.up_scale[et.expert] * d;
   }
   // rows without a slot read the tile's first row or row 0; nothing of theirs is kept
   const bool gather = a.pair != nullptr;
@@ -190,13 +192,11 @@ __global__ __launch_bounds__(64 * WN * KS, 4) void experts_many_kernel(const Exp
   // a lane.  Lane l holds weight row l % 32 and slots 8 (v / 4) + 4 (l / 32) + v % 4.
   float* unit = reinterpret_cast<float*>(lds) + wave * OUT;
   const int n0 = rb * 32;
-  float gamma[2], bias[2];
+  float bias[2];
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    const float* sc = GATED && b ? a.up_scale : a.w_scale;
     const float* bs = GATED && b ? a.up_bias : a.bias;
     const int n = n0 + r + (GATED ? 0 : 32 * b);
-    gamma[b] = sc[et.expert];
     bias[b] = bs && n < a.N ? bs[(size_t)et.expert * a.N + n] : 0.0f;
   }
   const bool has0 = a.bias != nullptr, has1 = GATED ? a.up_bias != nullptr : has0;
@@ -210,9 +210,9 @@ __global__ __launch_bounds__(64 * WN * KS, 4) void experts_many_kernel(const Exp
       float v0[8], v1[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float d = d_of[32 * i + 16 * q + 8 * (e >> 2) + 4 * h + (e & 3)];
-        v0[e] = acc_64(acc[i][0][8 * q + e]) * (gamma[0] * d);
-        v1[e] = acc_64(acc[i][1][8 * q + e]) * (gamma[1] * d);
+        const int sl = 32 * i + 16 * q + 8 * (e >> 2) + 4 * h + (e & 3);
+        v0[e] = acc_64(acc[i][0][8 * q + e]) * scale_of[0][sl];
+        v1[e] = acc_64(acc[i][1][8 * q + e]) * scale_of[GATED ? 1 : 0][sl];
         if (has0) v0[e] = v0[e] + bias[0];
         if (has1) v1[e] = v1[e] + bias[1];
       }
@@ -305,6 +305,7 @@ hipError_t launch_experts_many(const ExpertArgs& a, ManyTile tile, hipStream_t s
     case kMany32x4: return launch_many<1, 2, 4, 2>(a, s);
     case kMany32x8: return launch_many<1, 4, 1, 2>(a, s);
     case kMany64x8: return launch_many<2, 4, 1, 1>(a, s);
+    case kMany96x8: return launch_many<3, 4, 1, 1>(a, s);
     case kMany64x16: return launch_many<2, 8, 1, 1>(a, s);
   }
   return hipErrorInvalidValue;

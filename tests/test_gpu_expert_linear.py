@@ -106,6 +106,7 @@ def test_wide(counts, tokens, n, k, act, gated, bias, slots, dt):
     ([70, 33, 0, 90], 100, 2, 1597, 704, "relu2", True, False, True, "f32"),
     ([70, 33, 0, 90], 100, 2, 795, 8256, "relu2", True, True, False, "bf16"),
     ([3, 0, 1], 2, 2, 70, 8256, "relu2", True, False, True, "f32"),
+    ([436], 436, 1, 12008, 320, "relu2", True, True, False, "bf16"),
     ([10870], 10870, 1, 763, 576, "relu2", False, True, False, "bf16"),
     ([10880], 10880, 1, 379, 448, "relu2", True, False, True, "f32")])
 def test_each_tile(counts, tokens, topk, n, k, act, gated, bias, slots, dt):
@@ -193,6 +194,30 @@ def test_dense_is_the_prefill_product(m, n, k):
         want = N.bitnet_ternary_linear_prefill([(w.w[0], w.scale, n)], dev(xq), dev(d), y_dtype=dt)[0]
         got = N.bitnet_ternary_linear_act(w.w[0], w.scale, n, dev(xq), dev(d), y_dtype=dt)
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("gated,m,n", [(False, 3137, 4090), (True, 3130, 2043)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_prompts(gated, m, n, dt):
+    """Enough rows for the widest tile: against the plain products of the prefill call, whose epilogue in elementary
+    operations rounds as the definition does."""
+    k = 4160
+    xq, d = acts(m, k, 1)
+    x, dd = dev(xq), dev(d)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    ws = [torch.randint(0, 256, (n, k // 4), generator=g, device=DEV, dtype=torch.uint8) for _ in range(1 + gated)]
+    ws = [N.bitnet_repack_prefill(w & ~((w >> 1) & w & 0x55)) for w in ws]        # (no code 3)
+    scale = torch.full((1,), 0.013, device=DEV)
+    v = [N.bitnet_ternary_linear_prefill([(w, scale, n)], x, dd)[0] for w in ws]
+    res = torch.randn(m, n, generator=g, device=DEV).to(dt)
+    bias = torch.randn(n, generator=g, device=DEV)
+    a = torch.relu(v[0] + bias)
+    want = a * a
+    if gated:
+        want = want * v[1]
+    got = N.bitnet_ternary_linear_act(ws[0], scale, n, x, dd, up=(ws[1], scale) if gated else None, bias=bias, act="relu2",
+                                      residual=res, y_dtype=dt)
+    assert torch.equal(got, (want + res.float()).to(dt))
 
 
 @pytest.mark.parametrize("m", [1, 5, 40, 150, 300])
