@@ -1082,9 +1082,11 @@ class TernaryExperts(_Fixed):
         if packed.dim() != 3:
             raise ValueError("packed must be [experts, N, K/4]")
         e, n, kb = packed.shape
-        w = torch.empty((e, *prefill_layout_shape(n, 4 * kb)), dtype=torch.uint8, device=packed.device)
-        for i in range(e):
-            bitnet_repack_prefill(packed[i], w[i], stream)
+        device = _one_device(packed, scale)
+        with _On(device, stream):           # the stream is current in it
+            w = torch.empty((e, *prefill_layout_shape(n, 4 * kb)), dtype=torch.uint8, device=device)
+            for i in range(e):
+                bitnet_repack_prefill(packed[i], w[i])
         return TernaryExperts(w, scale, n, 4 * kb)
 
 

@@ -140,8 +140,12 @@ hipError_t launch_few(const ExpertArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// (the other kernels' grids are smaller, but for rounding up to the XCDs)
-bool experts_fit(const ExpertArgs& a) { return few_grid(a) + 8 <= max_grid(64 * kFewWaves); }
+// Of the kernels that take large calls the one with 32 x 8 blocks has most threads (rounded up to the
+// XCDs).
+bool experts_fit(const ExpertArgs& a) {
+  const int64_t blocks = ((int64_t)a.N + 31) / 32, weights = a.up ? 2 * blocks : blocks;
+  return many_tiles(a, 32) * ((weights + 7) / 8) + 8 <= max_grid(256);
+}
 
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s) {
   // The kernel is chosen for slots spread evenly over the experts; how they are spread is known

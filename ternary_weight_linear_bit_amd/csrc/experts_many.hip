@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * WN * KS, TB == 3 ? 3 : 4) void experts_many_ke
   // rows without a slot read the tile's first row or row 0; nothing of theirs is kept
   const bool gather = a.pair != nullptr;
   const auto xr = gather
-      ? make_uniform_rsrc(a.xq, (uint32_t)min((int64_t)a.rows * K, (int64_t)0xffffffffu))
+      ? make_uniform_rsrc(a.xq, (uint32_t)((int64_t)a.rows * K))       // (at most 2^31)
       : make_uniform_rsrc(a.xq + (size_t)slot0 * K, (uint32_t)(rows * K));
   uint32_t xo[XG];
 #pragma unroll

@@ -103,6 +103,7 @@ def test_expert_routing_refusals(lib):   # noqa: F811
     # a grid that the runtime cannot count
     huge = product(rows=1 << 30, N=1 << 24, K=64)
     assert lib.bitnet_ternary_linear_act(ctypes.byref(huge), None) == ESHAPE
+    assert experts(lib, routing(tokens=1 << 30, topk=1), product(rows=1 << 30, N=1 << 24, K=64), 1) == ESHAPE
     assert lib.bitnet_ternary_linear_act(None, None) == ENULL
     assert lib.bitnet_expert_linear(None, ctypes.byref(p), 0, None) == ENULL
     assert lib.bitnet_expert_linear(ctypes.byref(routing()), None, 0, None) == ENULL

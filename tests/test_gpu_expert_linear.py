@@ -273,6 +273,12 @@ def test_another_stream():
     y = N.bitnet_ternary_linear_act(w.w[0], w.scale, 70, x, dd, act="relu2", stream=s)
     s.synchronize()
     same(y, E.product(q[0], g[0], xq, d, act="relu2")[0], "f32")
+    packed = torch.randint(0, 3, (2, 40, 16), device=DEV, dtype=torch.uint8)
+    torch.cuda.synchronize()
+    again = N.TernaryExperts.from_packed(packed, torch.ones(2, device=DEV), stream=s)
+    s.synchronize()
+    for i in range(2):
+        assert torch.equal(again.w[i], N.bitnet_repack_prefill(packed[i]))
 
 
 def test_captured_products_follow_the_routing():
