@@ -273,7 +273,7 @@ __global__ __launch_bounds__(kPairs) void route_kernel(const RouteArgs a, int to
     if (e >= 0 && rank == 0) count[wave * E + e] = __popcll(same);
     __syncthreads();
     for (int x = tid; x < E; x += kPairs) {
-      int n = total[x];                  // in earlier rounds
+      int n = total[x];                  // those of the tokens before
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const int c = count[w * E + x];
