@@ -668,7 +668,7 @@ bitnet_status bitnet_route(const bitnet_routing *routing, const void *logits, in
 size_t bitnet_route_workspace_bytes(int64_t tokens, int topk, int experts);
 
 /* Activations: none, max(v, 0)^2, v / (1 + e^-v), v * Phi(v) (Phi the standard normal
- * distribution function). */
+ * distribution function).  The last two of -inf are NaN (infinity times 0). */
 typedef enum bitnet_act {
   BITNET_ACT_NONE = 0,
   BITNET_ACT_RELU2 = 1,

@@ -136,7 +136,8 @@ __device__ __forceinline__ v4i weights_64(uint32_t w) {
 // acc from that sum (exact: 24 bits times 2^6; a sum of 0 is +0).
 __device__ __forceinline__ float acc_64(int sum) { return fmaf((float)sum, -0x1p-6f, 0.0f); }
 
-// e^x for x <= 0, the rounding of x log2 e made up for (it is x 2^-24 otherwise).
+// e^x for x <= 0, the rounding of x log2 e made up for (it is x 2^-24 otherwise).  x log2 e is finite: an
+// infinite one has no rounding to make up for and would leave NaN, so callers bound x.
 __device__ __forceinline__ float exp_neg(float x) {
   const float t = x * 0x1.715476p+0f;                       // log2 e, rounded
   const float lo = fmaf(x, 0x1.4ae0cp-26f, fmaf(x, 0x1.715476p+0f, -t));
@@ -149,8 +150,8 @@ __device__ __forceinline__ float activate(float v, int act) {
       const float a = fmaxf(v, 0.0f);
       return a * a;
     }
-    case kActSilu: {      // v / (1 + e^-v), by e^-|v| so that nothing overflows
-      const float e = exp_neg(-fabsf(v));
+    case kActSilu: {      // v / (1 + e^-v), by e^-|v|, which is 0 long before -200
+      const float e = exp_neg(fmaxf(-fabsf(v), -200.0f));
       return (v < 0.0f ? v * e : v) * __builtin_amdgcn_rcpf(1.0f + e);
     }
     case kActGelu: {      // v times the normal distribution's integral up to v
