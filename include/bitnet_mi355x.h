@@ -683,7 +683,7 @@ typedef enum bitnet_act {
  *   a = RN32(a * u) where there is a second matrix `up`, u as v of it (its own bias);
  *   a = RN32(a + residual) where there is one;  y = a rounded to y_dtype.
  * Bit-exact against that definition, but for silu, within 2^-20 of its value, and gelu, within 2^-20
- * of its value and 2^-24 of |v| together.
+ * of its value and 2^-24 of |v| together (where the value is below 2^-126, 2^-149 beside that).
  *   w, up    matrices of [N][K] in the prefill layout (bitnet_repack_prefill), 16-byte aligned;
  *            up may be NULL.  Experts' matrices lie one behind the other,
  *            bitnet_prefill_layout_bytes(N, K) bytes each.

@@ -110,7 +110,7 @@ def product(q, gamma, x_q, d, bias=None, act="none", up=None, residual=None):
     """E4 before the last rounding; up: (q, gamma, bias).  Returns (a, tol): a fp32 and tol None
     where the definition is exact, else float64 with the bound that silu's and gelu's errors
     (2^-20 of the value, gelu 2^-24 of |v| beside it) and the roundings of the gating and the
-    residual (2^-24 of the result each) leave."""
+    residual (2^-24 of the result each) leave, and a subnormal's half step, 2^-150, for each rounding."""
     v = linear(q, gamma, x_q, d, bias)
     a = activate(v, act)
     u = None if up is None else linear(up[0], up[1], x_q, d, up[2])
@@ -120,9 +120,9 @@ def product(q, gamma, x_q, d, bias=None, act="none", up=None, residual=None):
         if residual is not None:
             a = (a + np.asarray(residual, F32)).astype(F32)
         return a, None
-    tol = 2.0 ** -20 * np.abs(a) + (2.0 ** -24 * np.abs(np.float64(v)) if act == "gelu" else 0) + 1e-36
+    tol = 2.0 ** -20 * np.abs(a) + (2.0 ** -24 * np.abs(np.float64(v)) if act == "gelu" else 0) + 2.0 ** -149
     if u is not None:
-        tol = tol * np.abs(np.float64(u)) + 2.0 ** -24 * np.abs(a * u)
+        tol = tol * np.abs(np.float64(u)) + 2.0 ** -24 * np.abs(a * u) + 2.0 ** -150
         a = a * u
     if residual is not None:
         a = a + np.asarray(residual, np.float64)

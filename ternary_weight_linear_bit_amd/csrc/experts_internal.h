@@ -151,8 +151,12 @@ __device__ __forceinline__ float activate(float v, int act) {
       return a * a;
     }
     case kActSilu: {      // v / (1 + e^-v), by e^-|v|, which is 0 long before -200
-      const float e = exp_neg(fmaxf(-fabsf(v), -200.0f));
-      return (v < 0.0f ? v * e : v) * __builtin_amdgcn_rcpf(1.0f + e);
+      // The exponential gives 0 for what is below 2^-126, 88 times which is not: from 87 on a factor e^-32
+      // stays apart (and 1 + e^-|v| is 1 with and without it).
+      const float a = fminf(fabsf(v), 200.0f);
+      const bool far = a > 87.0f;
+      const float e = exp_neg(far ? 32.0f - a : -a);
+      return (v < 0.0f ? v * e * (far ? 0x1.c846500000000p-47f : 1.0f) : v) * __builtin_amdgcn_rcpf(1.0f + e);
     }
     case kActGelu: {      // v times the normal distribution's integral up to v
       // integral up to -a = e^(-a^2 / 2) t Q(t), t = 1 / (1 + 0.28 a): a fit of the least largest error

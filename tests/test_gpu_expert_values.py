@@ -46,3 +46,15 @@ def test_silu_of_large_values(n):
     np.testing.assert_array_equal(y[:, 0::2], np.repeat(v[:, None], n // 2, 1))
     assert (y[:-1, 1::2].view(np.uint32) == 0x80000000).all()
     assert np.isnan(y[-1, 1::2]).all()
+
+
+@pytest.mark.parametrize("n", [FEW, MANY])
+def test_silu_where_its_power_is_subnormal(n):
+    """From -80 to -110 silu goes from 1.4e-33 to 0: within 2^-20 of its value and, where it is subnormal, a step
+    of those, 2^-149 (two roundings), beside it."""
+    v = np.r_[np.linspace(80, 110, 121), 87.0, 87.33, 87.34, 88.0, 91.0].astype(F32)
+    y = values(v, n, "silu").astype(np.float64)
+    z = v.astype(np.float64)[:, None]
+    low, high = -z * np.exp(-z) / (1 + np.exp(-z)), z / (1 + np.exp(-z))
+    assert (np.abs(y[:, 1::2] - low) <= 2.0 ** -20 * np.abs(low) + 2.0 ** -149).all()
+    assert (np.abs(y[:, 0::2] - high) <= 2.0 ** -20 * high).all()
