@@ -147,7 +147,7 @@ __device__ __forceinline__ float exp_neg(float x) {
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case kActRelu2: {
-      const float a = fmaxf(v, 0.0f);
+      const float a = v < 0.0f ? 0.0f : v;       // (NaN stays, which a maximum would drop)
       return a * a;
     }
     case kActSilu: {      // v / (1 + e^-v), by e^-|v|, which is 0 long before -200

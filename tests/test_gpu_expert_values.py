@@ -9,7 +9,8 @@ from oracle import bitnet_oracle as O
 from oracle import experts_oracle as E
 from ternary_weight_linear_bit_amd import _native as N
 
-from experts_util import F32, dev, host
+from experts_util import F32, acts, assign, dev, host, matrices, routing
+from gpu_helpers import DEV
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +59,52 @@ def test_silu_where_its_power_is_subnormal(n):
     low, high = -z * np.exp(-z) / (1 + np.exp(-z)), z / (1 + np.exp(-z))
     assert (np.abs(y[:, 1::2] - low) <= 2.0 ** -20 * np.abs(low) + 2.0 ** -149).all()
     assert (np.abs(y[:, 0::2] - high) <= 2.0 ** -20 * high).all()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [FEW, MANY])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", ["none", "relu2", "silu", "gelu"])
+def test_no_number_stays_none(act, gated, n, dt):
+    """A row whose scale is NaN and a column whose bias is NaN are NaN, and nothing else is; infinite biases
+    give what the activation gives."""
+    rng = np.random.default_rng(n)
+    q, w = signs(n)
+    x, d = rng.integers(-127, 128, (40, 64)).astype(np.int8), np.full(40, 0.01, F32)
+    bias = rng.standard_normal(n).astype(F32)
+    d[[3, 39]] = np.nan
+    bias[[1, n - 1]] = np.nan
+    bias[2], bias[4] = np.inf, -np.inf
+    up = (w, torch.ones(1, device=DEV)) if gated else None
+    ub = np.full(n, 5, F32)             # (u is not 0, so that infinities stay)
+    args = dict(act=act, bias=dev(bias), up=up, up_bias=dev(ub) if gated else None, y_dtype=dt)
+    y = host(N.bitnet_ternary_linear_act(w, dev(np.ones(1, F32)), n, dev(x), dev(d), **args).float())
+    with np.errstate(all="ignore"):
+        want, _ = E.product(q, F32(1), x, d, bias, act, (q, F32(1), ub) if gated else None)
+    nan = np.zeros((40, n), bool)
+    nan[[3, 39]] = nan[:, [1, n - 1]] = True
+    nan[:, 4] |= act in ("silu", "gelu")             # -inf times 0
+    np.testing.assert_array_equal(np.isnan(want), nan)
+    np.testing.assert_array_equal(np.isnan(y), nan)
+    inf = np.isinf(np.where(nan, 0, want))
+    assert inf.any()
+    np.testing.assert_array_equal(y[inf], want[inf])
+    # (silu and gelu 2^-20 of the value and 2^-24 of |v| <= 6, times |u| <= 7; the last rounding 2^-8)
+    rest = ~nan & ~inf
+    np.testing.assert_allclose(y[rest], want[rest], rtol=2.0 ** -8 if dt is torch.bfloat16 else 2.0 ** -19,
+                               atol=2.0 ** -18)
+
+
+@pytest.mark.parametrize("n", [40, 6016])
+def test_an_expert_whose_scale_is_no_number(n):
+    """Its rows are NaN through each activation, the other experts' are as they were."""
+    counts = [60, 50, 40]
+    r, (first, _, _) = routing(assign(counts, 75, 2), 3)
+    xq, d = acts(75, 128, 1)
+    _, g, w = matrices(3, n, 128, 2)
+    bad = N.TernaryExperts(w.w, dev(np.array([g[0], np.nan, g[2]], F32)), n, 128)
+    for act in ("none", "relu2", "silu", "gelu"):
+        want = host(N.bitnet_expert_linear(r, w, dev(xq), dev(d), act=act))
+        y = host(N.bitnet_expert_linear(r, bad, dev(xq), dev(d), act=act))
+        want[first[1]:first[2]] = np.nan
+        np.testing.assert_array_equal(y, want)
