@@ -692,7 +692,8 @@ typedef enum bitnet_act {
  *   x_q, x_scale        [rows][K] int8, 16-byte aligned, and [rows].
  *   residual  NULL or [rows][N] of y's type; y may be it.
  *   y         [rows][N] fp32 or bf16, element-aligned; for experts a row for each slot.
- *   rows      0 to 2^30;  N >= 0;  K % 64 == 0, 64 to BITNET_MAX_K;  N * K < BITNET_MAX_WEIGHTS.
+ *   rows      0 to 2^30;  N 0 to 2^31 - 32;  K % 64 == 0, 64 to BITNET_MAX_K;
+ *             N * K < BITNET_MAX_WEIGHTS.
  *   act       bitnet_act.
  */
 typedef struct bitnet_product {

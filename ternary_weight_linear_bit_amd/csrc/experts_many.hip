@@ -296,7 +296,7 @@ __global__ __launch_bounds__(64 * WN * KS, TB == 3 ? 3 : 4) void experts_many_ke
 template <int TB, int WN, int KS, int DX>
 hipError_t launch_many(const ExpertArgs& a, hipStream_t s) {
   const int bn = a.up ? 32 * WN : 64 * WN;
-  const int ntiles = (a.N + bn - 1) / bn;
+  const int ntiles = (int)(((int64_t)a.N + bn - 1) / bn);     // (N is up to 2^31 - 32)
   const dim3 grid((unsigned)((many_tiles(a, 32 * TB) * ntiles + kXcds - 1) / kXcds * kXcds)), block(64 * WN * KS);
   if (a.up)
     hipLaunchKernelGGL((experts_many_kernel<TB, WN, KS, DX, true>), grid, block, 0, s, a, ntiles);

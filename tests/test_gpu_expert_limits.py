@@ -1,0 +1,66 @@
+"""Products, offsets and combination at the largest sizes that the calls take (up to 90 GB)."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import bitnet_oracle as O
+from oracle import experts_oracle as E
+from ternary_weight_linear_bit_amd import _native as N
+from ternary_weight_linear_bit_amd import inputs as I
+
+from experts_util import F32, acts, dev
+from gpu_helpers import DEV
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    N.lib()
+
+
+@pytest.fixture(autouse=True)
+def _memory():
+    yield
+    torch.cuda.empty_cache()
+
+
+def block(seed):
+    """32 x 64 weights and their block of the prefill layout."""
+    q = I.ternary_codes(32, 64, seed)
+    return q, N.bitnet_repack_prefill(dev(O.pack_codes(q)))[0]
+
+
+@pytest.mark.parametrize("gated,n", [(False, 2 ** 31 - 32), (True, 2 ** 31 - 1152)])
+def test_most_outputs_of_a_row(gated, n):
+    """The largest N, which with a tile's width passes 31 bits, and the largest that gate and up leave a launch: one
+    block of weights everywhere but for some at the beginning, the end and in between."""
+    rows = 2
+    q, one = block(1)
+    w = torch.empty(N.prefill_layout_shape(n, 64), dtype=torch.uint8, device=DEV)
+    w.copy_(one.expand_as(w))
+    others = {0: 2, 2 ** 25: 3, n // 32 - 9: 4, n // 32 - 2: 5, n // 32 - 1: 6}
+    for at, seed in others.items():
+        w[at] = block(seed)[1]
+    xq, d = acts(rows, 64, 1)
+    scale = torch.full((1,), 0.5, device=DEV)
+    buf = torch.full((rows * n + 32,), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = buf[:rows * n].view(rows, n)
+    print("weights laid out", flush=True)
+    N.bitnet_ternary_linear_act(w, scale, n, dev(xq), dev(d), up=(w, scale) if gated else None, act="relu2", y=y)
+    torch.cuda.synchronize()
+
+    def want(q):
+        up = (q, F32(0.5), None) if gated else None
+        a = E.bf16(E.product(q, F32(0.5), xq, d, act="relu2", up=up)[0])
+        return torch.from_numpy(a).to(torch.bfloat16).to(DEV)
+    blocks = y.view(rows, n // 32, 32)
+    for at, seed in others.items():
+        assert torch.equal(blocks[:, at], want(block(seed)[0])), at
+        blocks[:, at] = want(q)
+    for m in range(rows):
+        assert bool((blocks[m] == want(q)[m]).all())
+    assert bool((buf[rows * n:] == 7).all())
