@@ -632,7 +632,8 @@ bitnet_status bitnet_residual_norm(const bitnet_residual *args, hipStream_t stre
  *   offset  [experts + 1]; pair [tokens * topk] pair of each slot, -1 behind the last one;
  *   slot    [tokens][topk] slot of each pair, -1 for none.
  * The calls that read a routing do not trust its contents: offsets are clamped to the pairs, and
- * a slot whose pair, or a pair whose slot, is out of range is left out.
+ * a slot whose pair, or a pair whose slot, is out of range is left out.  Where experts' ranges of slots
+ * overlap, a slot's values are those of any of them, or as they were.
  */
 typedef struct bitnet_routing {
   int32_t *expert;

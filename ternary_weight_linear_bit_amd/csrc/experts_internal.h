@@ -99,17 +99,19 @@ __device__ __forceinline__ ExpertSpan expert_span(const ExpertArgs& a, int t) {
   }
   return {0, 0, 0, 0};
 }
-// Tiles of all experts.
+// Tiles of all experts.  Offsets that make experts' slots overlap give more than a plan has, up to experts times
+// slots / ROWS, beyond 31 bits: no more are counted than the grid was made for.  (Each lane's sum is below 2^30,
+// the wave's taken without sign.)
 template <int ROWS>
 __device__ __forceinline__ int count_tiles(const ExpertArgs& a) {
   if (!a.offset) return (a.slots + ROWS - 1) / ROWS;
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, most = a.slots / ROWS + min(a.slots, a.experts);
   int n = 0;
   for (int e = lane; e < a.experts; e += 64) {
     const int lo = min(max(a.offset[e], 0), a.slots);
     n += (min(max(a.offset[e + 1], lo), a.slots) - lo + ROWS - 1) / ROWS;
   }
-  return wave_sum(n);
+  return (int)min((uint32_t)wave_sum(min(n, most)), (uint32_t)most);
 }
 // Input row of a slot; -1 where the device's numbers name none.
 __device__ __forceinline__ int input_row(const ExpertArgs& a, int slot) {

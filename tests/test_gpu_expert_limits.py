@@ -9,7 +9,7 @@ from oracle import experts_oracle as E
 from ternary_weight_linear_bit_amd import _native as N
 from ternary_weight_linear_bit_amd import inputs as I
 
-from experts_util import F32, acts, dev
+from experts_util import F32, acts, dev, matrices, same
 from gpu_helpers import DEV
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +64,25 @@ def test_most_outputs_of_a_row(gated, n):
     for m in range(rows):
         assert bool((blocks[m] == want(q)[m]).all())
     assert bool((buf[rows * n:] == 7).all())
+
+
+def test_overlapping_ranges_of_many_slots():
+    """Every second expert's range is the whole batch: 512 times its tiles, more than 2^31, are no tiles of a plan.  The
+    matrices are alike, so that a slot's values are the same whichever expert it goes to."""
+    pairs, experts, n = 2 ** 29 - 40000, 1024, 8
+    x, d = torch.zeros((pairs, 64), dtype=torch.int8, device=DEV), torch.ones(pairs, device=DEV)
+    at = [0, 12345, 1 << 28, pairs - 97, pairs - 1]
+    xq, ds = acts(len(at), 64, 1)
+    x[at], d[at] = dev(xq), dev(ds)
+    q, g, w = matrices(1, n, 64, 3)
+    w = N.TernaryExperts(w.w.repeat(experts, 1, 1), w.scale.repeat(experts), n, 64)
+    none = torch.empty((pairs, 1), dtype=torch.int32, device=DEV)      # (not read by slot)
+    offset = torch.tensor([0, pairs], dtype=torch.int32, device=DEV).repeat(experts // 2 + 1)[:experts + 1]
+    r = N.Routing(none, none.view(torch.float32), offset, none.view(-1), none)
+    y = torch.full((pairs, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    print("batch laid out", flush=True)
+    N.bitnet_expert_linear(r, w, x, d, slots=True, y=y)
+    torch.cuda.synchronize()
+    same(y[at], E.product(q[0], g[0], xq, ds)[0], "bf16")
+    y[at] = 0.0
+    assert int(torch.count_nonzero(y)) == 0
