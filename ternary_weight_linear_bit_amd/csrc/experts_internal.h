@@ -54,7 +54,7 @@ hipError_t launch_experts_many(const ExpertArgs& a, ManyTile tile, hipStream_t s
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
 
 // out[m] = residual[m] + sum_j weight[m][j] y[slot[m][j]].
-constexpr int64_t kCombineCols = (int64_t)1 << 23;   // most of a row: 256 a workgroup, at most 65535
+constexpr int64_t kCombineCols = (int64_t)1 << 23;   // most of a row
 hipError_t launch_combine(const Routing& r, const void* y, bool y_bf16, int64_t K,
                           const void* residual, void* out, bool out_bf16, hipStream_t s);
 

@@ -492,9 +492,10 @@ hipError_t launch_combine_w(const Routing& r, const void* y, bool y_bf16, int64_
   const int64_t cols = (K + W - 1) / W;
   const int threads = cols >= 256 ? 256 : (int)((cols + 63) / 64) * 64;
   const int64_t parts = (cols + threads - 1) / threads;
-  // (columns in the grid's second dimension; with very many workgroups one takes several tokens)
-  const int64_t across = parts > 65535 ? 0 : max_grid(256) / parts;
-  if (across == 0) return hipErrorInvalidValue;
+  // Columns lie in the grid's second dimension, at most 2^15 parts of them.  What the runtime counts leaves at least
+  // 511 workgroups in the first; where tokens are more, one takes several of them.
+  static_assert(kCombineCols / 256 <= 65535, "the grid's second dimension");
+  const int64_t across = max_grid(256) / parts;
   const dim3 grid((unsigned)(r.tokens < across ? r.tokens : across), (unsigned)parts), block(threads);
 #define BITNET_COMBINE(YB, OB) \
   hipLaunchKernelGGL((combine_kernel<YB, OB, W>), grid, block, 0, s, r, y, K, residual, out)

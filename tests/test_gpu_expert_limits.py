@@ -86,3 +86,25 @@ def test_overlapping_ranges_of_many_slots():
     same(y[at], E.product(q[0], g[0], xq, ds)[0], "bf16")
     y[at] = 0.0
     assert int(torch.count_nonzero(y)) == 0
+
+
+@pytest.mark.parametrize("k,tokens", [(3, 2 ** 24 + 300), (8, 2 ** 24 + 300), (2 ** 23 - 1, 520)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_combined_tokens_beyond_the_grid(k, tokens, residual):
+    """More tokens than the grid's first dimension has workgroups: 2^24 - 1 of them for rows of one part, narrow or in
+    16 bytes, and 511 beside the 32768 parts of the longest rows."""
+    r = N.Routing.empty(tokens, 1, 1, DEV)
+    r.slot.copy_(torch.arange(tokens - 1, -1, -1, device=DEV, dtype=torch.int32)[:, None])
+    r.slot[[1, tokens - 2]] = -1
+    r.weight.fill_(2.0)
+    v = (torch.arange(tokens, device=DEV) % 85).to(torch.bfloat16)          # a row's values; up to 3 * 84 they are exact in bf16
+    y = v[:, None].expand(tokens, k).contiguous()
+    want = 2 * v.flip(0)
+    want[[1, tokens - 2]] = 0
+    base = None
+    if residual:
+        base = y.clone() if k < 100 else y
+        want += v
+    out = N.bitnet_combine(r, y, base, out=torch.full_like(y, 7.0))
+    for m in range(0, tokens, 1 << 22):
+        assert bool((out[m:m + (1 << 22)] == want[m:m + (1 << 22), None]).all()), m
