@@ -656,7 +656,7 @@ typedef enum bitnet_score { BITNET_SOFTMAX = 0, BITNET_CHOSEN = 1, BITNET_SIGMOI
  *           -inf and NaN are never chosen, and where fewer than topk are left the rest have
  *           expert -1 and weight 0.
  *   score, scale   weight = scale * the score, in fp32 (scale finite).  Logits that equal the row's
- *           largest count e^0, +inf too.
+ *           largest count e^0, +inf too.  A score below 2^-126 may be 0.
  *   workspace  bitnet_route_workspace_bytes() bytes, 16-byte aligned; clobbered; calls that
  *           overlap need one each.  NULL when the size is 0.
  * Indices are exact, and the same call gives the same bits.
@@ -694,7 +694,9 @@ typedef enum bitnet_act {
  *   residual  NULL or [rows][N] of y's type; y may be it.
  *   y         [rows][N] fp32 or bf16, element-aligned; for experts a row for each slot.
  *   rows      0 to 2^30;  N 0 to 2^31 - 32;  K % 64 == 0, 64 to BITNET_MAX_K;
- *             N * K < BITNET_MAX_WEIGHTS.
+ *             N * K < BITNET_MAX_WEIGHTS; and T * ceil(N / 256) (with up ceil(N / 128)) at most
+ *             2^24 - 9, what a launch counts, where T = ceil(rows / 32), for experts
+ *             tokens * topk / 32 + min(tokens * topk, experts).
  *   act       bitnet_act.
  */
 typedef struct bitnet_product {

@@ -289,7 +289,6 @@ bool attention_fits(const bitnet_kv_cache& c, const bitnet_kv_batch& b, int q_he
 
 // Limits of a batch of pairs (token, choice).
 constexpr int64_t kMaxPairs = (int64_t)1 << 30;
-constexpr int64_t kMaxRouted = (int64_t)1 << 24;   // a workgroup's counts are held in 16 bits
 
 bool routing_fits(int64_t tokens, int topk, int experts) {
   return tokens >= 0 && topk >= 1 && topk <= bitnet::kMaxTopk && experts >= 1 &&
@@ -816,7 +815,7 @@ bitnet_status bitnet_residual_norm(const bitnet_residual* args, hipStream_t stre
 }
 
 size_t bitnet_route_workspace_bytes(int64_t tokens, int topk, int experts) {
-  if (!routing_fits(tokens, topk, experts) || tokens == 0 || tokens * topk > kMaxRouted) return 0;
+  if (!routing_fits(tokens, topk, experts) || tokens == 0 || tokens * topk > bitnet::kMaxRouted) return 0;
   return bitnet::route_workspace_bytes(tokens, topk, experts);
 }
 
@@ -826,7 +825,7 @@ bitnet_status bitnet_route(const bitnet_routing* routing, const void* logits, in
   if (!routing) return BITNET_ERR_NULL;
   const bitnet_routing& r = *routing;
   if (logits && !valid_dtype(dtype)) return BITNET_ERR_DTYPE;
-  if (!routing_fits(r.tokens, r.topk, r.experts) || r.tokens * r.topk > kMaxRouted ||
+  if (!routing_fits(r.tokens, r.topk, r.experts) || r.tokens * r.topk > bitnet::kMaxRouted ||
       (logits && (stride < r.experts || score < BITNET_SOFTMAX || score > BITNET_SIGMOID ||
                   !finite(scale))))
     return BITNET_ERR_SHAPE;

@@ -8,6 +8,7 @@ namespace bitnet {
 
 constexpr int kMaxExperts = 1024;   // counters of a workgroup's pairs by expert lie in LDS
 constexpr int kMaxTopk = 32;        // a lane a choice
+constexpr int64_t kMaxRouted = (int64_t)1 << 24;   // pairs that are planned: a workgroup's counts are held in 16 bits
 
 // Which rows belong to which expert (bitnet_routing, validated).
 struct Routing {

@@ -171,22 +171,32 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int m) {
 // plan: a stable counting sort of the pairs by expert
 // ---------------------------------------------------------------------------
 //
-// A workgroup takes some tokens, at most 1024 pairs: it chooses their experts, ranks each pair among
-// the workgroup's pairs of its expert and leaves the counts.  One workgroup's counts are the plan;
+// A workgroup takes some tokens, in rounds of at most 1024 pairs: it chooses their experts, ranks each
+// pair among the workgroup's pairs of its expert and leaves the counts.  One workgroup's counts are the plan;
 // of several, a second launch adds those of earlier workgroups (7 us for 256 of them over 256
 // experts; a workgroup reads 128 KiB of counts).  64 tokens over 64 experts: one launch, 6.0 us.
 
-constexpr int kPairs = 1024;     // threads, and most pairs of a workgroup
+constexpr int kPairs = 1024;     // threads, and most pairs of a round
 constexpr int kWaves = kPairs / 64;
 
 // Tokens of a workgroup: 64 (what its lanes choose for at once, up to 256 experts), and more, in
 // rounds of up to 1024 pairs, where there would be more than 512 workgroups: each of them reads the
 // counts of all in the second launch.
-int tokens_of(int64_t tokens, int topk) {
+constexpr int tokens_of(int64_t tokens, int topk) {
   const int64_t round = kPairs / topk, each = (tokens + 511) / 512, least = round < 64 ? round : 64;
   if (each <= round) return (int)(each > least ? each : least);
   return (int)((each + round - 1) / round * round);
 }
+// A workgroup's pairs, 33759 at most, are counted in 16 bits (they grow with the tokens).
+constexpr int most_pairs_of_a_workgroup() {
+  int most = 0;
+  for (int topk = 1; topk <= kMaxTopk; ++topk) {
+    const int pairs = tokens_of(kMaxRouted / topk, topk) * topk;
+    most = pairs > most ? pairs : most;
+  }
+  return most;
+}
+static_assert(most_pairs_of_a_workgroup() <= 65535, "counts of 16 bits");
 
 // Lanes of the wave with the same expert as this one; none for -1.
 __device__ __forceinline__ uint64_t same_expert(int e, int experts) {
