@@ -225,11 +225,8 @@ __global__ __launch_bounds__(64 * WN * KS, TB == 3 ? 3 : 4) void experts_many_ke
         if (has1) v1[e] = v1[e] + bias[1];
       }
       if (a.act != kActNone) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v0[e] = activate(v0[e], a.act);
-          if (!GATED) v1[e] = activate(v1[e], a.act);
-        }
+        activate(v0, a.act);
+        if (!GATED) activate(v1, a.act);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
