@@ -26,10 +26,10 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 // in steps past the last, x is read outside its buffer, which gives zeros.
 // Bound by latency (the offsets, the pair and the row are loads behind each other; the weights need
 // the first alone and are under way meanwhile): one token through gate and up of two 2560 -> 6912
-// experts, 17.7 MB, 6.3 us replayed from a graph; 2560 -> 2560 3.8-4.2.  A load of x touches as many lines as
+// experts, 17.7 MB, 6.3-7.6 us replayed from a graph; 2560 -> 2560 3.8-4.4.  A load of x touches as many lines as
 // there are rows, so that from about 16 rows on the staged kernel is faster where it fills the chip
-// (4096 -> 14336 at 32 rows: 11.7 us here, 9.1 there; at 8 rows 7.3 and 7.9).  Two steps in flight
-// against one: 14336 -> 4096, one row, two experts 9.2 and 10.8 us; K = 2560 7.2 and 6.6.
+// (4096 -> 14336 at 32 rows: 11.9 us here, 9.5 there; at 8 rows 7.5 and 8.4).  Two steps in flight
+// against one: 14336 -> 4096, one row, two experts 9.2 and 10.6 us; K = 2560 8.2 and 7.6.
 constexpr int kFewRows = 32, kFewWaves = 8;
 
 template <int S, bool GATED>
@@ -161,8 +161,8 @@ hipError_t launch_experts(const ExpertArgs& a, hipStream_t s) {
   auto groups = [&](int rows, int wide) { return tiles(rows) * ((weights + wide - 1) / wide); };
   // Few rows: one block of weights a workgroup, while that gives at most a workgroup a compute
   // unit (two with up to 8 rows, and one only with few or short rows, whose loads are its cost):
-  // 2560 -> 2560 at 96 rows, 240 workgroups, 5.9 us against 7.7 of the next choice; at 128, 320 of them,
-  // 8.7 against 7.7.
+  // 2560 -> 2560 at 96 rows, 240 workgroups, 6.1 us against 7.9 of the next choice; at 128, 320 of them,
+  // 8.7 against 8.0.
   const double few = tiles(kFewRows) * blocks;
   if ((few <= 256 && (each <= 16 || steps <= 64)) || (few <= 512 && each <= 8))
     return steps > 32 ? launch_few<2>(a, s) : launch_few<1>(a, s);
@@ -172,7 +172,8 @@ hipError_t launch_experts(const ExpertArgs& a, hipStream_t s) {
   if (groups(32, 4) <= 256) return launch_experts_many(a, kMany32x4, s);
   // 32 x 8, 64 x 8, 96 x 8 or 64 x 16 blocks: the least time, with what a step and what lies beside
   // the steps of a workgroup takes alone on its compute unit, and among `held` of them (us, fitted to
-  // measured calls).  A last round's workgroups count as those that run alone while rounds are few.
+  // measured calls: over 116 of them the choice is 0.8% above the least in the geometric mean, 24% at worst,
+  // 512 tokens through gate and up of two of eight 2560 -> 6912 experts, 41.4 us for 33.5).  A last round's workgroups count as those that run alone while rounds are few.
   struct Shape {
     ManyTile tile;
     int rows, wide, held;

@@ -11,9 +11,9 @@
 //  * weights are loaded two steps ahead, x one or two ahead of its staging (more would cost a wave a
 //    SIMD with 64 slots).
 //
-// Bound by the matrix cores at the clock that power allows: 8192 x 14336 x 8192 dense in 662-676 us
-// (2.9 POPS; matrix instructions alone reach 4.2 on such operands), 4096 tokens through gate and up
-// of two of eight 2560 -> 6912 experts in 231 us (2.5 POPS), where the tiles' beginnings and ends
+// Bound by the matrix cores at the clock that power allows: 8192 x 14336 x 8192 dense in 641-676 us
+// (2.8-3.0 POPS; matrix instructions alone reach 4.2 on such operands), 4096 tokens through gate and up
+// of two of eight 2560 -> 6912 experts in 229-237 us (2.5 POPS), where the tiles' beginnings and ends
 // count.  Weights expanded to -64 q take 4 vector instructions a matrix instruction with 64 slots
 // and 2.7 with 96.  Few rows an expert are bound by memory: 64 tokens over 64 experts of 2560 -> 1152, 94
 // MB of weights, 21 us (4.4 TB/s).
