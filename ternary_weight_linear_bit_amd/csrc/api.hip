@@ -304,7 +304,7 @@ bitnet::Routing routing_of(const bitnet_routing& r) {
 bitnet_status check_product(const bitnet_product& p, int64_t rows, bool* nothing) {
   if (!valid_dtype(p.y_dtype)) return BITNET_ERR_DTYPE;
   if (rows < 0 || rows > kMaxPairs || p.N < 0 || p.K < 64 || p.K % 64 != 0 || p.K > BITNET_MAX_K ||
-      p.N >= BITNET_MAX_WEIGHTS / p.K || p.N > kInt32Max - 31 || p.act < BITNET_ACT_NONE ||
+      p.N > (BITNET_MAX_WEIGHTS - 1) / p.K || p.N > kInt32Max - 31 || p.act < BITNET_ACT_NONE ||
       p.act > BITNET_ACT_GELU || (!p.up && (p.up_scale || p.up_bias)))
     return BITNET_ERR_SHAPE;
   *nothing = rows == 0 || p.N == 0;

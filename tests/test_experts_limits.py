@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from test_experts_abi import experts, product, routing
-from test_layer_abi import ESHAPE, lib  # noqa: F401
+from test_layer_abi import ENULL, ESHAPE, lib  # noqa: F401
 
 
 @pytest.mark.parametrize("topk", range(1, 33))
@@ -36,3 +36,15 @@ def test_products_beyond_a_launch(lib):   # noqa: F811
         return experts(lib, r, product(rows=slots, N=n, K=64, up=None, up_scale=None, up_bias=None), 1)
     assert grouped(32 * (most - 1000 + 1), 1000, 1) == ESHAPE
     assert grouped(40, 1000, 256 * (most // 41) + 1) == ESHAPE
+
+
+@pytest.mark.parametrize("k", [192, 320, 704, 4160, 131008, 128, 131072])
+def test_weights_of_a_product_are_below_2_38(lib, k):   # noqa: F811
+    """The largest N with N * K < 2^38 is no wrong size (the call without a matrix gets as far as its addresses),
+    the next is."""
+    n = (2 ** 38 - 1) // k
+
+    def status(n):
+        p = product(rows=1, N=n, K=k, w=None, up=None, up_scale=None, up_bias=None)
+        return lib.bitnet_ternary_linear_act(ctypes.byref(p), None)
+    assert status(min(n, 2 ** 31 - 32)) == ENULL and status(n + 1) == ESHAPE
