@@ -712,7 +712,7 @@ typedef struct bitnet_product {
 } bitnet_product;
 
 /* The product of one matrix (or gate and up) with all rows.  With nothing behind it the values are those of
- * bitnet_ternary_linear_prefill, which takes several matrices at once; for one matrix this is the quicker call. */
+ * bitnet_ternary_linear_prefill, which takes several matrices at once; for one matrix this is mostly the quicker call. */
 bitnet_status bitnet_ternary_linear_act(const bitnet_product *product, hipStream_t stream);
 
 /*
